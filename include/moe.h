@@ -22,6 +22,8 @@
  *     object), creates no streams or events, and keeps only a per-device
  *     cache of the compute-unit count, the LDS limit and that array's
  *     address.
+ *   - The routing and dense-product calls (moe_route, moe_linear and their
+ *     gradients) stand on their own: they take no plan and no moe_shape.
  *   - Errors the device detects (an expert id out of range, a received-row
  *     count that disagrees with the routing, a consumer wait that timed out)
  *     are written to an error word inside the plan workspace and reported by
@@ -286,6 +288,133 @@ int moe_expert_combine_noalloc(const moe_shape* shape, const void* plan_ws, cons
  */
 int moe_scale(const moe_shape* shape, const void* plan_ws, const uint16_t* recv_self,
               const float* topk_w, uint16_t* out, void* stream);
+
+/*
+ * moe_scale_backward — the gradient of moe_scale: with g = d_out,
+ *   d_recv[pos[t][j]] = bf16(topk_w[t][j] * g[t]),  d_topk_w[t][j] = sum_c g[t][c] * recv_self[pos[t][j]][c]
+ * (fp32 sums).  Every row of d_recv belongs to one (token, slot), so all of
+ * its T_r*k rows are written.
+ *   recv_self  device bf16 [T_r*k, d], as given to moe_scale; may be NULL when d_topk_w is.
+ *   topk_w     device float [T_r, k]; may be NULL when d_recv is.
+ *   d_out      device bf16 [T_r, d].
+ *   d_recv     device bf16 [T_r*k, d], no overlap with the inputs; NULL: not wanted.
+ *   d_topk_w   device float [T_r, k]; NULL: not wanted (one of the two must be).
+ */
+int moe_scale_backward(const moe_shape* shape, const void* plan_ws, const uint16_t* recv_self,
+                       const float* topk_w, const uint16_t* d_out, uint16_t* d_recv, float* d_topk_w,
+                       void* stream);
+
+/* Element types of the routing and dense-product calls below. */
+typedef enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+
+/* How a router's logits become scores, and its scores gate weights. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+typedef struct moe_route_opts {
+  int32_t score;        /* MOE_SCORE_*: over a token's experts, or each by itself */
+  int32_t renorm;       /* nonzero: the k weights are divided by their sum */
+  int32_t n_group;      /* experts in groups of E / n_group neighbours (a divisor of E, at most 64); 0 = 1 */
+  int32_t topk_group;   /* groups a token may choose from; 0 = n_group */
+  int32_t group_score;  /* MOE_GROUP_MAX: a group's best c; MOE_GROUP_TOP2: the sum of its two best (groups of
+                           two experts at least) */
+  float scale;          /* factor on the weights, finite and above 0; 0 = 1 */
+} moe_route_opts;
+
+/*
+ * moe_route — step 1 of the distributed MoE forward: the gate's top-k experts
+ * and weights of every token, in the form moe_plan (topk_ids) and moe_scale
+ * (topk_w) read them.  With z the logits in fp32 and s = softmax(z) or
+ * 1 / (1 + e^-z):
+ *   c = s + bias; an expert is masked (c = -infinity) where its logit or bias
+ *     is -infinity, or its group is not among the token's topk_group best;
+ *   topk_ids[t] = the k largest c, descending, equal ones by ascending id;
+ *   topk_w[t][j] = s of that expert (without the bias), 0 if it is masked (a
+ *     sigmoid of a logit below -700 counts as 0);
+ *     renorm: divided by the token's sum (all 0 if that is 0);
+ *     then times scale.
+ * c is compared in 64 bits or exactly.  Masked experts rank below all others
+ * and by id, so the ids are always k distinct experts and a valid input of
+ * moe_plan.  A NaN logit or bias, or +infinity under a softmax, makes its
+ * token's weights NaN (the ids stay distinct).
+ *   logits    device [tokens, experts] of dtype, rows ld elements apart (ld >= experts; 0 = experts).
+ *   bias      device float [experts], or NULL: none.
+ *   opts      NULL: softmax, no renorm, no groups, scale 1.
+ *   topk_ids  device int32 [tokens, top_k];  topk_w  device float [tokens, top_k].
+ * experts <= 1024, top_k <= 32 and at most the experts of topk_group groups.
+ */
+int moe_route(int64_t tokens, int32_t experts, int32_t top_k, const void* logits, int32_t dtype, int64_t ld,
+              const float* bias, const moe_route_opts* opts, int32_t* topk_ids, float* topk_w, void* stream);
+
+/*
+ * moe_route_backward — the gradient of moe_route's weights with respect to
+ * the logits.  The choice of experts and the bias take no gradient, and
+ * neither do slots of weight 0.  A slot whose id is outside [0, experts) is
+ * ignored; an expert listed in several slots of a token gets the sum.
+ *   logits, ld, topk_ids, topk_w, opts   as given to and returned by moe_route
+ *             (only score, renorm and scale of opts are read).
+ *   d_topk_w  device float [tokens, top_k], e.g. from moe_scale_backward.
+ *   d_logits  device [tokens, experts] of dtype, rows ld_d elements apart (0 = experts); all written.
+ */
+int moe_route_backward(int64_t tokens, int32_t experts, int32_t top_k, const void* logits, int32_t dtype,
+                       int64_t ld, const int32_t* topk_ids, const float* topk_w, const float* d_topk_w,
+                       const moe_route_opts* opts, void* d_logits, int64_t ld_d, void* stream);
+
+/* Activations of moe_linear.  SWIGLU: silu(gate) * up, where w's rows (and
+ * bias and pre) are the gate's, then the up projection's, as in w_gate_up. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4,
+       MOE_ACT_SWIGLU = 5 };
+
+/* A dense product's sizes and types.  n = 2 * cols under SWIGLU, else cols.
+ * Row pitches are in elements, at least the row's length, at most 2^21;
+ * 0 = packed. */
+typedef struct moe_linear_desc {
+  int64_t rows;          /* of x and out; 0..2^21 */
+  int32_t cols;          /* of out; 1..2^20 */
+  int32_t depth;         /* columns of x and w; a multiple of 8, 8..2^20 */
+  int32_t dtype;         /* MOE_BF16 or MOE_F16: x, w, bias, pre, dx, dw, dbias */
+  int32_t out_dtype;     /* dtype, or MOE_F32: out, residual, d_out */
+  int32_t act;           /* MOE_ACT_* */
+  int32_t pad;           /* zero */
+  int64_t ld_x, ld_w;    /* multiples of 8 */
+  int64_t ld_residual, ld_pre;
+  int64_t ld_out;        /* of out, in the backward pass of d_out */
+  int64_t ld_dx, ld_dw;  /* backward pass only */
+} moe_linear_desc;
+
+/* Workspace bytes of moe_linear (may be 0) and of moe_linear_backward, 256-byte
+ * aligned.  Either pointer may be NULL.  Host only; no HIP call. */
+int moe_linear_sizes(const moe_linear_desc* desc, size_t* forward_bytes, size_t* backward_bytes);
+
+/*
+ * moe_linear — out = act(x w^T + bias) + residual, fp32 inside, rounded once:
+ * a router's logits (out_dtype MOE_F32), a shared expert (SWIGLU, then a
+ * product with moe_scale's output as its residual).
+ *   x         device [rows, depth], 16-byte aligned.    w   device [n, depth], 16-byte aligned.
+ *   bias      device [n] or NULL.
+ *   residual  device [rows, cols] of out_dtype or NULL; may be `out` itself with the same pitch.
+ *   pre       device [rows, n] or NULL: receives x w^T + bias, which moe_linear_backward needs under an
+ *             activation.
+ *   out       device [rows, cols] of out_dtype.
+ *   ws        device workspace, 256-byte aligned, forward_bytes of moe_linear_sizes (NULL if that is 0).  Its
+ *             contents do not matter before or after; calls that overlap on the device need one each.
+ */
+int moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const void* bias, const void* residual,
+               void* pre, void* out, void* ws, void* stream);
+
+/*
+ * moe_linear_backward — with dz = d_out * act'(pre) (SWIGLU: for both halves):
+ *   dx = dz w,  dw = dz^T x,  dbias = column sums of dz.
+ * dz is rounded to dtype before the two products (their operands are 16-bit),
+ * not for dbias; sums are fp32, rounded once.  The residual's gradient is d_out.
+ *   d_out   device [rows, cols] of out_dtype.
+ *   pre     device [rows, n]; not read without an activation (may be NULL then).
+ *   dx      device [rows, depth], dw device [n, depth], dbias device [n]: any may be NULL, not all.
+ *           dx and dw without overlap with the inputs.
+ *   x       may be NULL without dw, w without dx.
+ *   ws      as for moe_linear, backward_bytes.
+ */
+int moe_linear_backward(const moe_linear_desc* desc, const void* x, const void* w, const void* pre,
+                        const void* d_out, void* dx, void* dw, void* dbias, void* ws, void* stream);
 
 /* Synchronises `stream`, then returns the device error word of the plan
  * (MOE_OK, MOE_ETIMEOUT or MOE_EROUTING), or MOE_EHIP. */

@@ -23,6 +23,10 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so"
 MOE_OK, MOE_EINVAL, MOE_ECAPACITY, MOE_EHIP, MOE_ETIMEOUT, MOE_EROUTING, MOE_EUNSUPPORTED = range(7)
 MODE_OVERLAP, MODE_SERIAL, MODE_COPY_ONLY, MODE_COPY_ROWS = 0, 1, 2, 3
 SIGNAL_TILE, SIGNAL_GROUP = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_SWIGLU = range(6)
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 HDR_FIELDS = ["error", "M", "bands", "remote_bands", "segments", "remote_segments",
               "gateup_tiles", "down_tiles", "copy_units", "received_rows", "gateup_row_tiles",
@@ -63,6 +67,19 @@ class moe_combine_opts(ctypes.Structure):
                 ("x_recv", ctypes.c_void_p), ("signal", ctypes.c_int32), ("pad", ctypes.c_int32)]
 
 
+class moe_route_opts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renorm", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("topk_group", ctypes.c_int32), ("group_score", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("depth", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("pad", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+                ("ld_residual", ctypes.c_int64), ("ld_pre", ctypes.c_int64), ("ld_out", ctypes.c_int64),
+                ("ld_dx", ctypes.c_int64), ("ld_dw", ctypes.c_int64)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -85,6 +102,14 @@ def _load():
         "moe_expert_combine_noalloc": (I, [P(moe_shape), V, V, V, V, V, V, V, ctypes.c_uint32,
                                            P(ctypes.c_void_p), P(moe_combine_opts), V]),
         "moe_scale": (I, [P(moe_shape), V, V, V, V, V]),
+        "moe_scale_backward": (I, [P(moe_shape), V, V, V, V, V, V, V]),
+        "moe_route": (I, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, V, ctypes.c_int32, ctypes.c_int64, V,
+                          P(moe_route_opts), V, V, V]),
+        "moe_route_backward": (I, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, V, ctypes.c_int32,
+                                   ctypes.c_int64, V, V, V, P(moe_route_opts), V, ctypes.c_int64, V]),
+        "moe_linear_sizes": (I, [P(moe_linear_desc), P(ctypes.c_size_t), P(ctypes.c_size_t)]),
+        "moe_linear": (I, [P(moe_linear_desc), V, V, V, V, V, V, V, V]),
+        "moe_linear_backward": (I, [P(moe_linear_desc), V, V, V, V, V, V, V, V, V]),
         "moe_device_status": (I, [V, V]),
         "moe_device_cus": (I, []),
     }
@@ -98,7 +123,8 @@ def _load():
 _lib = _load()
 EXPORTED = ["moe_status_string", "moe_query_sizes", "moe_plan_offsets", "moe_plan",
             "moe_expert_combine", "moe_expert_combine_noalloc", "moe_scale", "moe_device_status",
-            "moe_device_cus"]
+            "moe_device_cus", "moe_scale_backward", "moe_route", "moe_route_backward", "moe_linear_sizes",
+            "moe_linear", "moe_linear_backward"]
 
 
 def library_path() -> str:
@@ -196,6 +222,187 @@ def moe_scale(shape: Shape, plan_ws, recv_self, topk_w, out, stream=None) -> Non
                           _stream(stream)), "moe_scale")
 
 
+def moe_scale_backward(shape: Shape, plan_ws, recv_self, topk_w, d_out, d_recv=None, d_topk_w=None,
+                       stream=None) -> None:
+    _check(_lib.moe_scale_backward(shape.ptr, _ptr(plan_ws), _ptr(recv_self), _ptr(topk_w), _ptr(d_out),
+                                   _ptr(d_recv), _ptr(d_topk_w), _stream(stream)), "moe_scale_backward")
+
+
+# --- routing and the dense product -------------------------------------------
+# These take their sizes, types and row pitches from the tensors, so the
+# tensors are checked here; they run on the tensors' device (on its current
+# stream unless one is given).
+
+def _invalid(where: str, what: str):
+    err = MoEError(MOE_EINVAL, where)
+    err.args = (f"{err.args[0]}: {what}",)
+    return err
+
+
+def _matrix(where, name, t, rows, cols, dtype, device) -> int:
+    """Checks a [rows, cols] matrix with unit column stride (None passes);
+    returns its row pitch, 0 (packed) where no second row shows it."""
+    if t is None:
+        return 0
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise _invalid(where, f"{name} is {tuple(t.shape)}, not ({rows}, {cols})")
+    if t.dtype is not dtype:
+        raise _invalid(where, f"{name} is {t.dtype}, not {dtype}")
+    if t.device != device:
+        raise _invalid(where, f"{name} is on {t.device}, not {device}")
+    if rows < 2:
+        if cols > 1 and rows and t.stride(1) != 1:
+            raise _invalid(where, f"{name}'s columns are not contiguous")
+        return 0
+    pitch, step = t.stride()
+    if (cols > 1 and step != 1) or pitch < cols:
+        raise _invalid(where, f"{name} has strides {t.stride()}: rows of contiguous columns are wanted")
+    return pitch
+
+
+def _packed(where, name, t, shape, dtype, device) -> None:
+    if t is None:
+        return
+    if tuple(t.shape) != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise _invalid(where, f"{name} is not a contiguous {dtype} tensor of shape {shape} on {device}")
+
+
+def _on_device(where, t, call, stream):
+    """call(raw stream) with t's device current."""
+    if t.device.type != "cuda":
+        raise _invalid(where, f"the tensors are on {t.device}, not on a GPU")
+    if torch.cuda.current_device() == t.device.index:
+        return call(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+    with torch.cuda.device(t.device):
+        return call(_stream(stream))
+
+
+def _route_opts(score, renorm, n_group, topk_group, group_score, scale):
+    return moe_route_opts(int(score), 1 if renorm else 0, int(n_group), int(topk_group), int(group_score),
+                          float(scale))
+
+
+def _check_logits(where, logits):
+    if logits.dim() != 2 or logits.dtype not in _DTYPES:
+        raise _invalid(where, "logits is a [tokens, experts] tensor of bfloat16, float16 or float32")
+    T, E = logits.shape
+    return T, E, _matrix(where, "logits", logits, T, E, logits.dtype, logits.device)
+
+
+def moe_route(logits, topk_ids, topk_w, bias=None, score: int = SCORE_SOFTMAX, renorm: bool = False,
+              n_group: int = 1, topk_group: int = 0, group_score: int = GROUP_MAX, scale: float = 1.0,
+              stream=None) -> None:
+    """Router logits [T, E] -> topk_ids int32 [T, k] (what moe_plan reads) and
+    topk_w float32 [T, k] (what moe_scale reads); see include/moe.h."""
+    T, E, ld = _check_logits("moe_route", logits)
+    if topk_ids.dim() != 2:
+        raise _invalid("moe_route", "topk_ids is a [tokens, top_k] tensor")
+    k = topk_ids.shape[1]
+    _packed("moe_route", "topk_ids", topk_ids, (T, k), torch.int32, logits.device)
+    _packed("moe_route", "topk_w", topk_w, (T, k), torch.float32, logits.device)
+    _packed("moe_route", "bias", bias, (E,), torch.float32, logits.device)
+    opts = _route_opts(score, renorm, n_group, topk_group, group_score, scale)
+    _check(_on_device("moe_route", logits, lambda s: _lib.moe_route(
+        T, E, k, logits.data_ptr(), _DTYPES[logits.dtype], ld, _ptr(bias), ctypes.byref(opts),
+        topk_ids.data_ptr(), topk_w.data_ptr(), s), stream), "moe_route")
+
+
+def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, score: int = SCORE_SOFTMAX,
+                       renorm: bool = False, scale: float = 1.0, stream=None) -> None:
+    """d_logits [T, E] (the logits' type) from d_topk_w float32 [T, k]; logits,
+    topk_ids, topk_w, score, renorm and scale as in the moe_route call."""
+    where = "moe_route_backward"
+    T, E, ld = _check_logits(where, logits)
+    if topk_ids.dim() != 2:
+        raise _invalid(where, "topk_ids is a [tokens, top_k] tensor")
+    k = topk_ids.shape[1]
+    _packed(where, "topk_ids", topk_ids, (T, k), torch.int32, logits.device)
+    _packed(where, "topk_w", topk_w, (T, k), torch.float32, logits.device)
+    _packed(where, "d_topk_w", d_topk_w, (T, k), torch.float32, logits.device)
+    ld_d = _matrix(where, "d_logits", d_logits, T, E, logits.dtype, logits.device)
+    opts = _route_opts(score, renorm, 1, 1, GROUP_MAX, scale)
+    _check(_on_device(where, logits, lambda s: _lib.moe_route_backward(
+        T, E, k, logits.data_ptr(), _DTYPES[logits.dtype], ld, topk_ids.data_ptr(), topk_w.data_ptr(),
+        d_topk_w.data_ptr(), ctypes.byref(opts), d_logits.data_ptr(), ld_d, s), stream), where)
+
+
+def _linear_desc(where, x, w, out, act, out_name):
+    if x.dim() != 2 or w.dim() != 2 or out.dim() != 2:
+        raise _invalid(where, f"x, w and {out_name} are matrices")
+    if x.dtype not in (torch.bfloat16, torch.float16) or out.dtype not in (x.dtype, torch.float32):
+        raise _invalid(where, f"x is {x.dtype} and {out_name} {out.dtype}: bfloat16 or float16, and the same or "
+                              "float32")
+    (M, K), N = x.shape, out.shape[1]
+    n = 2 * N if act == ACT_SWIGLU else N
+    d = moe_linear_desc(M, N, K, _DTYPES[x.dtype], _DTYPES[out.dtype], int(act), 0)
+    d.ld_x = _matrix(where, "x", x, M, K, x.dtype, x.device)
+    d.ld_w = _matrix(where, "w", w, n, K, x.dtype, x.device)
+    d.ld_out = _matrix(where, out_name, out, M, N, out.dtype, x.device)
+    return d, n
+
+
+def moe_linear_sizes(desc: moe_linear_desc) -> Dict[str, int]:
+    fwd, bwd = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_lib.moe_linear_sizes(ctypes.byref(desc), ctypes.byref(fwd), ctypes.byref(bwd)), "moe_linear_sizes")
+    return {"forward_bytes": fwd.value, "backward_bytes": bwd.value}
+
+
+def _workspace(where, ws, need, x, stream):
+    """The given workspace, checked, or one from torch's allocator on the
+    stream that uses it (freed to that stream, so a later call on it may have
+    the same memory)."""
+    if ws is not None:
+        if ws.device != x.device or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+            raise _invalid(where, f"ws is not a contiguous tensor of {need} bytes on {x.device}")
+        return ws
+    if need == 0:
+        return None
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=x.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=x.device)
+
+
+def moe_linear(x, w, out, bias=None, residual=None, pre=None, act: int = ACT_NONE, ws=None, stream=None) -> None:
+    """out = act(x w^T + bias) + residual: x [M, K], w [N, K] (SWIGLU: [2N, K],
+    gate rows then up rows), out [M, N] of x's type or float32; pre, if given,
+    receives x w^T + bias.  ws: at least moe_linear_sizes' forward_bytes, or
+    None to take it from torch's allocator; see include/moe.h."""
+    where = "moe_linear"
+    d, n = _linear_desc(where, x, w, out, act, "out")
+    M, N = out.shape
+    _packed(where, "bias", bias, (n,), x.dtype, x.device)
+    d.ld_residual = _matrix(where, "residual", residual, M, N, out.dtype, x.device)
+    d.ld_pre = _matrix(where, "pre", pre, M, n, x.dtype, x.device)
+    need = ctypes.c_size_t()
+    _check(_lib.moe_linear_sizes(ctypes.byref(d), ctypes.byref(need), None), where)
+    ws = _workspace(where, ws, need.value, x, stream)
+    _check(_on_device(where, x, lambda s: _lib.moe_linear(
+        ctypes.byref(d), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), _ptr(pre), out.data_ptr(),
+        _ptr(ws), s), stream), where)
+
+
+def moe_linear_backward(x, w, d_out, dx=None, dw=None, dbias=None, pre=None, act: int = ACT_NONE, ws=None,
+                        stream=None) -> None:
+    """The gradients of moe_linear that are given a tensor (dx [M, K], dw like
+    w, dbias [n], all of x's type) from d_out [M, N] and, under an activation,
+    the forward call's pre; see include/moe.h."""
+    where = "moe_linear_backward"
+    d, n = _linear_desc(where, x, w, d_out, act, "d_out")
+    d.ld_pre = _matrix(where, "pre", pre, d_out.shape[0], n, x.dtype, x.device)
+    d.ld_dx = _matrix(where, "dx", dx, x.shape[0], x.shape[1], x.dtype, x.device)
+    d.ld_dw = _matrix(where, "dw", dw, n, x.shape[1], x.dtype, x.device)
+    _packed(where, "dbias", dbias, (n,), x.dtype, x.device)
+    need = ctypes.c_size_t()
+    _check(_lib.moe_linear_sizes(ctypes.byref(d), None, ctypes.byref(need)), where)
+    ws = _workspace(where, ws, need.value, x, stream)
+    _check(_on_device(where, x, lambda s: _lib.moe_linear_backward(
+        ctypes.byref(d), x.data_ptr(), w.data_ptr(), _ptr(pre), d_out.data_ptr(), _ptr(dx), _ptr(dw), _ptr(dbias),
+        _ptr(ws), s), stream), where)
+
+
 def moe_device_status(plan_ws, stream=None) -> int:
     return int(_lib.moe_device_status(_ptr(plan_ws), _stream(stream)))
 
@@ -271,6 +478,11 @@ class RankShare:
 
     def scale(self, topk_w_self, stream=None):
         moe_scale(self.shape, self.plan_ws, self.recv[self.shape.c.rank], topk_w_self, self.out, stream)
+
+    def scale_backward(self, topk_w_self, d_out, d_recv=None, d_topk_w=None, stream=None):
+        """The scale step's gradients: of the rank's receive buffer and of its gate weights."""
+        moe_scale_backward(self.shape, self.plan_ws, self.recv[self.shape.c.rank], topk_w_self, d_out, d_recv,
+                           d_topk_w, stream)
 
     def status(self, stream=None) -> int:
         return moe_device_status(self.plan_ws, stream)

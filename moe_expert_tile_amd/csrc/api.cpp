@@ -208,6 +208,12 @@ void record(void* ev, hipStream_t s) {
 }
 
 }  // namespace
+
+int prepare_device() {
+  int dev;
+  return prepare(&dev);
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -452,6 +458,27 @@ int moe_scale(const moe_shape* s, const void* plan_ws, const uint16_t* recv_self
   rc = prepare(&dev);
   if (rc) return rc;
   return hip_rc(launch_scale(L, (const int32_t*)plan_ws, recv_self, topk_w, out, (hipStream_t)stream));
+}
+
+int moe_scale_backward(const moe_shape* s, const void* plan_ws, const uint16_t* recv_self, const float* topk_w,
+                       const uint16_t* d_out, uint16_t* d_recv, float* d_topk_w, void* stream) {
+  int rc = valid_shape(s);
+  if (rc) return rc;
+  if (!plan_ws || !aligned(plan_ws, 256)) return MOE_EINVAL;
+  if (!d_recv && !d_topk_w) return MOE_EINVAL;
+  if (!aligned(recv_self, 16) || !aligned(topk_w, 4) || !aligned(d_out, 16) || !aligned(d_recv, 16) ||
+      !aligned(d_topk_w, 4))
+    return MOE_EINVAL;
+  if (s->tokens[s->rank] > 0 && (!d_out || (d_topk_w && !recv_self) || (d_recv && !topk_w))) return MOE_EINVAL;
+  PlanLayout L;
+  if (!make_layout(s->world, s->rank, s->experts_per_rank, s->top_k, s->hidden, s->ffn, s->tb_m, s->mgb, s->tokens,
+                   s->recv_rows, &L))
+    return MOE_ECAPACITY;
+  int dev;
+  rc = prepare(&dev);
+  if (rc) return rc;
+  return hip_rc(launch_scale_backward(L, (const int32_t*)plan_ws, recv_self, topk_w, d_out, d_recv, d_topk_w,
+                                      (hipStream_t)stream));
 }
 
 int moe_device_status(const void* plan_ws, void* stream) {

@@ -1,0 +1,909 @@
+// Dense product with its epilogue, out = act(x w^T + bias) + residual
+// (include/moe.h, moe_linear), and its gradients (moe_linear_backward).
+//
+// Every product here is C[m][n] = sum_k A[m][k] B[n][k] with both operands
+// contiguous along k; 16-bit operands, fp32 accumulation in MFMA registers.
+//   * Many rows: v_mfma_f32_32x32x16 over tiles staged through LDS by
+//     direct-to-LDS buffer loads into a two-stage ring (K steps of 64), 16-byte
+//     chunks XOR-swizzled so that operand fetches are free of bank conflicts.
+//     Rows past an operand's end and chunks past K get an offset past the
+//     buffer descriptor's bound, where loads return zeros.  Few tiles are also
+//     split along K: fp32 partial sums in the workspace, summed in order by a
+//     second launch, so results do not depend on timing.
+//   * Few rows (decode): the weights are read once, straight into MFMA
+//     operand registers (v_mfma_f32_16x16x32, 16 weight rows a workgroup), the
+//     workgroup's wavefronts sharing out K and joining their sums in LDS.
+// The first MFMA operand is the weight tile, so a lane ends with 4 consecutive
+// output columns per accumulator quad, and a gated activation's pair of columns
+// sits in one lane.
+//
+// Gradients.  dz = d_out act'(pre) is formed once (rounded to the operand type,
+// which the matrix cores need; its column sums for the bias are taken before
+// the rounding), then dx = dz w and dw = dz^T x are products of the same form
+// over transposed copies in the workspace.
+#include <type_traits>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+typedef unsigned int v4u32 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+constexpr int kBufWord3 = 0x00020000;        // raw buffer access: data format 32, other fields zero
+constexpr uint32_t kPastEnd = 0x80000000u;   // beyond every descriptor's extent (all below 2^31 bytes)
+constexpr int kCus = 256;                    // compute units the work is split for
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)(bytes < 0 ? 0 : bytes), kBufWord3);
+}
+
+// 1 KB of global memory into LDS at `dst` (16 bytes a lane, in lane order)
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rsrc, void* dst, uint32_t off, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)dst, 16, (int)off, soff, 0, 0);
+}
+
+// the 16-bit operand types
+template <bool F16>
+struct Elem {
+  typedef std::conditional_t<F16, f16x8, bf16x8> v8;
+  static __device__ __forceinline__ float to_float(uint16_t b) {
+    if constexpr (F16) return (float)__builtin_bit_cast(_Float16, b);
+    else return __uint_as_float((uint32_t)b << 16);
+  }
+  static __device__ __forceinline__ uint16_t bits(float f) {
+    if constexpr (F16) return __builtin_bit_cast(uint16_t, (_Float16)f);
+    else return __builtin_bit_cast(uint16_t, (__bf16)f);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(v8 a, v8 b, f32x16 c) {
+    if constexpr (F16) return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mfma16(v8 a, v8 b, f32x4 c) {
+    if constexpr (F16) return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+
+// --- activations (fp32) -----------------------------------------------------
+
+__device__ __forceinline__ float logistic(float z) {
+  return 1.0f / (1.0f + __builtin_amdgcn_exp2f(-z * 1.4426950408889634f));
+}
+constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+// gelu_tanh(z) = z (1 + tanh u) / 2 = z logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
+constexpr float kTwoSqrt2OverPi = 1.5957691216057308f, kCubic = 0.044715f;
+
+__device__ __forceinline__ float activate(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);
+    case MOE_ACT_SILU: return z * logistic(z);
+    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    case MOE_ACT_GELU_TANH: return z * logistic(kTwoSqrt2OverPi * (z + kCubic * z * z * z));
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float slope(int act, float z) {
+  // far out the smooth activations' slopes are 0 and 1 to the last bit, and
+  // their terms would be infinity times zero
+  if (act != MOE_ACT_RELU && act != MOE_ACT_NONE && fabsf(z) > 100.f) return z > 0.f ? 1.f : 0.f;
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case MOE_ACT_SILU: {
+      const float p = logistic(z);
+      return p * (1.0f + z * logistic(-z));
+    }
+    case MOE_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z) * kInvSqrt2Pi;
+    case MOE_ACT_GELU_TANH: {
+      const float u = kTwoSqrt2OverPi * (z + kCubic * z * z * z);
+      const float p = logistic(u);
+      return p + z * p * logistic(-u) * kTwoSqrt2OverPi * (1.0f + 3.0f * kCubic * z * z);
+    }
+    default: return 1.f;
+  }
+}
+
+// --- epilogue ---------------------------------------------------------------
+
+struct Epilogue {
+  const uint16_t* bias;
+  const void* res;
+  uint16_t* pre;
+  void* out;
+  int64_t M, ldr, ldp, ldo;
+  int N;         // output columns; a gated product has N gate and N up columns before the activation
+  int act;
+  int out_f32;
+  int vec;       // 4 columns an access: N and the pitches multiples of 4, bases aligned
+};
+
+template <bool F16>
+__device__ __forceinline__ void load4(const uint16_t* p, int n, bool vec, float (&v)[4]) {
+  if (vec) {
+    const uint2 x = *(const uint2*)p;
+    v[0] = Elem<F16>::to_float((uint16_t)x.x); v[1] = Elem<F16>::to_float((uint16_t)(x.x >> 16));
+    v[2] = Elem<F16>::to_float((uint16_t)x.y); v[3] = Elem<F16>::to_float((uint16_t)(x.y >> 16));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = c < n ? Elem<F16>::to_float(p[c]) : 0.f;
+  }
+}
+template <bool F16>
+__device__ __forceinline__ void store4(uint16_t* p, int n, bool vec, const float (&v)[4]) {
+  uint16_t b[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) b[c] = Elem<F16>::bits(v[c]);
+  if (vec) {
+    *(uint2*)p = make_uint2((uint32_t)b[0] | ((uint32_t)b[1] << 16), (uint32_t)b[2] | ((uint32_t)b[3] << 16));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < n) p[c] = b[c];
+  }
+}
+
+// Columns n .. n+3 of row m, of which those below N exist (n < N, m < M): z
+// the sums, u the up columns' sums of a gated product.
+template <bool F16, bool GATED>
+__device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int n, float (&z)[4], float (&u)[4]) {
+  const int left = e.N - n;
+  const bool vec = e.vec;
+  if (e.bias) {
+    float b[4];
+    load4<F16>(e.bias + n, left, vec, b);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) z[c] += b[c];
+    if constexpr (GATED) {
+      load4<F16>(e.bias + e.N + n, left, vec, b);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) u[c] += b[c];
+    }
+  }
+  if (e.pre) {
+    store4<F16>(e.pre + m * e.ldp + n, left, vec, z);
+    if constexpr (GATED) store4<F16>(e.pre + m * e.ldp + e.N + n, left, vec, u);
+  }
+  float y[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if constexpr (GATED) y[c] = z[c] * logistic(z[c]) * u[c];
+    else y[c] = activate(e.act, z[c]);
+  }
+  const int64_t at = m * e.ldo + n;
+  if (e.out_f32) {
+    if (e.res) {
+      const float* r = (const float*)e.res + m * e.ldr + n;
+      if (vec) {
+        const float4 x = *(const float4*)r;
+        y[0] += x.x; y[1] += x.y; y[2] += x.z; y[3] += x.w;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < left) y[c] += r[c];
+      }
+    }
+    float* o = (float*)e.out + at;
+    if (vec) {
+      *(float4*)o = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < left) o[c] = y[c];
+    }
+  } else {
+    if (e.res) {
+      float r[4];
+      load4<F16>((const uint16_t*)e.res + m * e.ldr + n, left, vec, r);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] += r[c];
+    }
+    store4<F16>((uint16_t*)e.out + at, left, vec, y);
+  }
+}
+
+// --- tiled product ----------------------------------------------------------
+
+struct ProdArgs {
+  const uint16_t *a, *b;   // A [M, K], B [N or 2N, K]
+  int64_t lda, ldb;
+  int64_t K;
+  int64_t kper;            // K of one split (a multiple of 64)
+  float* part;             // splits > 1: [splits][M][pitch] partial sums
+  int64_t pitch;
+  int up_col;              // ... where the up columns start in a row of them
+  int n_mt, n_nt, splits;
+  Epilogue e;
+};
+
+constexpr int kBK = 64;    // K step
+
+template <int BM_, int BN_, int WAVES_M, int WAVES_N>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_;
+  static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
+  static constexpr int FM = WM / 32, FN = WN / 32;
+  static constexpr int KK = kBK / 16;             // MFMA steps a stage
+  static constexpr int A_ELEMS = BM * kBK, B_ELEMS = BN * kBK;
+  static constexpr int STAGE = A_ELEMS + B_ELEMS;
+  // the epilogue's staging: a wave's columns (gate, then up) of 32 rows in
+  // fp32, rows 4 floats further apart than they are long, so that the lanes'
+  // 16-byte accesses to different rows fall on different banks
+  template <bool GATED>
+  struct staged {
+    static constexpr int FG = GATED ? FN / 2 : FN;
+    static constexpr int CW = FG * 32;
+    static constexpr int PITCH = FN * 32 + 4;
+  };
+  static constexpr int EPI_ELEMS = NW * 32 * (FN * 32 + 4) * 2;
+  static constexpr int LDS_ELEMS = 2 * STAGE > EPI_ELEMS ? 2 * STAGE : EPI_ELEMS;
+  static constexpr int A_LOADS = BM / 8 / NW;     // 1 KB wave loads a stage (8 rows of 128 bytes)
+  static constexpr int B_LOADS = BN / 8 / NW;
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole wave loads");
+  static_assert(B_LOADS % 2 == 0, "gate and up rows in separate loads");
+  static_assert(LDS_ELEMS * 2 <= 160 * 1024, "LDS");
+};
+typedef Tile<256, 256, 2, 4> Tile256;
+typedef Tile<256, 256, 4, 2> Tile256G;    // gated: each wave's columns hold as many gate as up ones
+typedef Tile<128, 128, 2, 2> Tile128;
+typedef Tile<64, 128, 2, 2> Tile64;
+
+// a workgroup's place in the tile order: workgroup i runs on XCD i mod 8; each
+// XCD gets a contiguous run, in which 8 row tiles x 4 column tiles share their
+// operands in its L2
+__device__ __forceinline__ int xcd_order(int i, int total) {
+  const int q = total / 8, r = total % 8, x = i % 8;
+  return x * q + min(x, r) + i / 8;
+}
+
+template <class C, bool F16, bool GATED, bool PART>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
+void product_kernel(ProdArgs g) {
+  typedef typename Elem<F16>::v8 v8;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[C::LDS_ELEMS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int WAVES_N = C::BN / C::WN;
+  const int wave_m = wave / WAVES_N, wave_n = wave % WAVES_N;
+  constexpr int HB = GATED ? C::BN / 2 : C::BN;    // output columns of a tile
+
+  const int tiles = g.n_mt * g.n_nt;
+  int t = xcd_order(blockIdx.x, tiles * g.splits);
+  const int split = t / tiles;
+  t -= split * tiles;
+  const int grp = t / (8 * g.n_nt), rows8 = min(8, g.n_mt - grp * 8);
+  t -= grp * 8 * g.n_nt;
+  const int mt = grp * 8 + t % rows8, nt = t / rows8;
+
+  const int64_t m0 = (int64_t)mt * C::BM;
+  const int n0 = nt * HB;
+  const int arows = (int)min((int64_t)C::BM, g.e.M - m0);
+  const int brows = min(HB, g.e.N - n0);
+  const int64_t kb = split * g.kper;
+  const int64_t ke = min(g.K, kb + g.kper);
+  const int KT = ke > kb ? (int)((ke - kb + kBK - 1) / kBK) : 0;
+  const int klast = (int)(ke - kb) - (KT - 1) * kBK;   // columns of the last stage
+
+  // lane l of a 1 KB load fills row 8 q + l / 8, chunk l % 8 of the stage, so
+  // it fetches the logical chunk (l % 8) ^ (row / 2) % 8
+  const int ld_row = lane / 8;
+  const int ld_chunk = (lane % 8) ^ ((wave * 4 + ld_row / 2) % 8);
+  static_assert(C::NW % 2 == 0, "a wave's loads are all of one row parity");
+  const __amdgpu_buffer_rsrc_t a_rsrc =
+      make_rsrc(g.a + m0 * g.lda + kb, KT ? ((int64_t)(arows - 1) * g.lda + (ke - kb)) * 2 : 0);
+  const int64_t b_bytes = KT ? ((int64_t)(brows - 1) * g.ldb + (ke - kb)) * 2 : 0;
+  const __amdgpu_buffer_rsrc_t b_rsrc = make_rsrc(g.b + (int64_t)n0 * g.ldb + kb, b_bytes);
+  const __amdgpu_buffer_rsrc_t u_rsrc =
+      GATED ? make_rsrc(g.b + ((int64_t)g.e.N + n0) * g.ldb + kb, b_bytes) : b_rsrc;
+  uint32_t a_off[C::A_LOADS], b_off[C::B_LOADS];
+#pragma unroll
+  for (int i = 0; i < C::A_LOADS; ++i) {
+    const int r = (wave + i * C::NW) * 8 + ld_row;
+    a_off[i] = r < arows ? 2u * ((uint32_t)r * (uint32_t)g.lda + ld_chunk * 8) : kPastEnd;
+  }
+#pragma unroll
+  for (int i = 0; i < C::B_LOADS; ++i) {
+    int r = (wave + i * C::NW) * 8 + ld_row;
+    if (GATED && i >= C::B_LOADS / 2) r -= HB;
+    b_off[i] = r < brows ? 2u * ((uint32_t)r * (uint32_t)g.ldb + ld_chunk * 8) : kPastEnd;
+  }
+  // stage k into half k % 2 of the ring; `last`: chunks past the end of K are
+  // masked (there every operand's chunk is whole or absent, K % 8 == 0)
+  auto issue = [&](int k, auto last_tag) __attribute__((always_inline)) {
+    constexpr bool LAST = decltype(last_tag)::value;
+    char* base = (char*)(lds + (k & 1) * C::STAGE);
+    const int koff = 2 * kBK * k;
+    const bool on = !LAST || ld_chunk * 8 < klast;
+#pragma unroll
+    for (int i = 0; i < C::A_LOADS; ++i)
+      load_lds(a_rsrc, base + (wave + i * C::NW) * 1024, on ? a_off[i] : kPastEnd, koff);
+#pragma unroll
+    for (int i = 0; i < C::B_LOADS; ++i)
+      load_lds(GATED && i >= C::B_LOADS / 2 ? u_rsrc : b_rsrc, base + 2 * C::A_ELEMS + (wave + i * C::NW) * 1024,
+               on ? b_off[i] : kPastEnd, koff);
+  };
+
+  // this wave's weight rows inside the tile (32 a block)
+  int prow[C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FN; ++i) {
+    if constexpr (GATED) {
+      constexpr int HW = C::WN / 2;
+      prow[i] = i < C::FN / 2 ? wave_n * HW + 32 * i : HB + wave_n * HW + 32 * (i - C::FN / 2);
+    } else {
+      prow[i] = wave_n * C::WN + 32 * i;
+    }
+  }
+  const int lrow = lane & 31, lhalf = lane >> 5, rsw = (lrow / 2) % 8;
+
+  f32x16 acc[C::FN][C::FM];
+#pragma unroll
+  for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  using Mid = std::integral_constant<bool, false>;
+  using Last = std::integral_constant<bool, true>;
+  // one stage: wait for its loads and for every wave's reads of the other
+  // half, refill that half (next: 0 nothing, 1 a whole stage, 2 the last one),
+  // multiply with the operand fetches one MFMA step ahead
+  auto step = [&](int k, auto next_tag) __attribute__((always_inline)) {
+    constexpr int NEXT = decltype(next_tag)::value;
+    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    const uint16_t* sa = lds + (k & 1) * C::STAGE;
+    const uint16_t* sb = sa + C::A_ELEMS;
+    v8 pw[2][C::FN], px[2][C::FM];
+    auto fetch = [&](int kk) __attribute__((always_inline)) {
+      const int phys = ((2 * kk + lhalf) ^ rsw) * 8;
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i) pw[kk & 1][i] = *(const v8*)(sb + (prow[i] + lrow) * kBK + phys);
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j) px[kk & 1][j] = *(const v8*)(sa + (wave_m * C::WM + 32 * j + lrow) * kBK + phys);
+    };
+    fetch(0);
+    if constexpr (NEXT == 1) issue(k + 1, Mid{});
+    if constexpr (NEXT == 2) issue(k + 1, Last{});
+#pragma unroll
+    for (int kk = 0; kk < C::KK; ++kk) {
+      if (kk + 1 < C::KK) fetch(kk + 1);
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) acc[i][j] = Elem<F16>::mfma32(pw[kk & 1][i], px[kk & 1][j], acc[i][j]);
+    }
+    // LDS reads of step 0, the refill, then each step's reads before the
+    // previous step's MFMAs
+    __builtin_amdgcn_sched_group_barrier(0x100, C::FN + C::FM, 0);
+    if constexpr (NEXT != 0) __builtin_amdgcn_sched_group_barrier(0x10, C::A_LOADS + C::B_LOADS, 0);
+#pragma unroll
+    for (int kk = 0; kk < C::KK; ++kk) {
+      if (kk + 1 < C::KK) __builtin_amdgcn_sched_group_barrier(0x100, C::FN + C::FM, 0);
+      __builtin_amdgcn_sched_group_barrier(0x8, C::FN * C::FM, 0);
+    }
+  };
+  if (KT > 0) {
+    if (KT > 1) issue(0, Mid{});
+    else issue(0, Last{});
+    int k = 0;
+    for (; k + 2 < KT; ++k) step(k, std::integral_constant<int, 1>{});
+    if (k + 1 < KT) step(k++, std::integral_constant<int, 2>{});
+    step(k, std::integral_constant<int, 0>{});
+  }
+
+  // Epilogue: 32 rows of a wave's columns at a time go through LDS (each wave
+  // has its own part of it), so that lanes hold neighbouring columns and every
+  // global access covers whole lines.
+  __builtin_amdgcn_s_waitcnt(0x70);
+  __builtin_amdgcn_s_barrier();   // every wave is done with the operands
+  constexpr int FG = C::template staged<GATED>::FG, CW = C::template staged<GATED>::CW;
+  constexpr int PITCH = C::template staged<GATED>::PITCH;
+  float* stage = (float*)lds + wave * 32 * PITCH;
+  const int ncol = n0 + (GATED ? wave_n * (C::WN / 2) : wave_n * C::WN);
+  constexpr int LPR = CW / 4, RPP = 64 / LPR;   // lanes a row, rows a pass
+  const int er = lane / LPR, ec = (lane % LPR) * 4;
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j) {
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(float4*)(stage + lrow * PITCH + 32 * i + 8 * q + 4 * lhalf) =
+            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+    __builtin_amdgcn_wave_barrier();
+    const int64_t mj = m0 + wave_m * C::WM + 32 * j;
+#pragma unroll 1
+    for (int r = er; r < 32; r += RPP) {
+      const int64_t m = mj + r;
+      const int n = ncol + ec;
+      if (m < g.e.M && n < g.e.N) {
+        const float4 x = *(const float4*)(stage + r * PITCH + ec);
+        float z[4] = {x.x, x.y, x.z, x.w}, u[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (GATED) {
+          const float4 y = *(const float4*)(stage + r * PITCH + CW + ec);
+          u[0] = y.x; u[1] = y.y; u[2] = y.z; u[3] = y.w;
+        }
+        if constexpr (PART) {
+          float* p = g.part + (split * g.e.M + m) * g.pitch + n;
+          *(float4*)p = make_float4(z[0], z[1], z[2], z[3]);
+          if constexpr (GATED) *(float4*)(p + g.up_col) = make_float4(u[0], u[1], u[2], u[3]);
+        } else {
+          finish4<F16, GATED>(g.e, m, n, z, u);
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// sums of a split product's partial sums, in split order, and the epilogue
+template <bool F16, bool GATED>
+__global__ __launch_bounds__(256) void join_kernel(ProdArgs g) {
+  const int quads = (g.e.N + 3) / 4;
+  const int64_t total = g.e.M * quads;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / quads;
+    const int n = (int)(i - m * quads) * 4;
+    float z[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < g.splits; ++s) {
+      const float* p = g.part + (s * g.e.M + m) * g.pitch + n;
+      const float4 x = *(const float4*)p;
+      z[0] += x.x; z[1] += x.y; z[2] += x.z; z[3] += x.w;
+      if constexpr (GATED) {
+        const float4 y = *(const float4*)(p + g.up_col);
+        u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+      }
+    }
+    finish4<F16, GATED>(g.e, m, n, z, u);
+  }
+}
+
+// --- few rows ---------------------------------------------------------------
+//
+// A workgroup owns 16 output columns; its wavefronts take K in steps of 32 in
+// turn.  Operand lane layout of v_mfma_f32_16x16x32: row (or column) lane % 16,
+// k = 8 (lane / 16) .. + 7, so a lane's operand is one 16-byte load; result
+// lane: column (token) lane % 16, rows (weight rows) 4 (lane / 16) .. + 3.
+constexpr int kFewWaves = 8;
+
+template <int TT, bool F16, bool GATED>
+__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
+  typedef typename Elem<F16>::v8 v8;
+  constexpr int NB = GATED ? 2 : 1;
+  __shared__ float4 part[kFewWaves][NB][TT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int n0 = blockIdx.x * 16;
+  const int r = lane & 15, kc = (lane >> 4) * 8;
+  const int M = (int)g.e.M, K = (int)g.K;
+  const int brows = min(16, g.e.N - n0);
+  const int64_t b_bytes = ((int64_t)(brows - 1) * g.ldb + K) * 2;
+  __amdgpu_buffer_rsrc_t b_rsrc[NB];
+  b_rsrc[0] = make_rsrc(g.b + (int64_t)n0 * g.ldb, b_bytes);
+  if constexpr (GATED) b_rsrc[1] = make_rsrc(g.b + ((int64_t)g.e.N + n0) * g.ldb, b_bytes);
+  const __amdgpu_buffer_rsrc_t a_rsrc = make_rsrc(g.a, ((int64_t)(M - 1) * g.lda + K) * 2);
+  const uint32_t b_off = r < brows ? 2u * ((uint32_t)r * (uint32_t)g.ldb + kc) : kPastEnd;
+  uint32_t a_off[TT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i) a_off[i] = 16 * i + r < M ? 2u * ((uint32_t)(16 * i + r) * (uint32_t)g.lda + kc) : kPastEnd;
+  f32x4 acc[NB][TT];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < TT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int U = TT >= 4 ? 2 : 4;   // K steps with their loads in flight together
+  for (int k0 = wave * 32; k0 < K; k0 += kFewWaves * 32 * U) {
+    v4u32 wv[U][NB], xv[U][TT];
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+      const int k = k0 + s * kFewWaves * 32;
+      const bool on = k + kc < K;      // a lane's 8 columns are whole or absent
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        wv[s][b] = __builtin_amdgcn_raw_buffer_load_b128(b_rsrc[b], (int)(on ? b_off + 2u * k : kPastEnd), 0, 0);
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+        xv[s][i] = __builtin_amdgcn_raw_buffer_load_b128(a_rsrc, (int)(on && a_off[i] != kPastEnd ? a_off[i] + 2u * k : kPastEnd), 0, 0);
+    }
+#pragma unroll
+    for (int s = 0; s < U; ++s)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+          acc[b][i] = Elem<F16>::mfma16(__builtin_bit_cast(v8, wv[s][b]), __builtin_bit_cast(v8, xv[s][i]), acc[b][i]);
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < TT; ++i) part[wave][b][i][lane] = make_float4(acc[b][i][0], acc[b][i][1], acc[b][i][2], acc[b][i][3]);
+  __syncthreads();
+  for (int i = wave; i < TT; i += kFewWaves) {
+    float z[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+      const float4 x = part[w][0][i][lane];
+      z[0] += x.x; z[1] += x.y; z[2] += x.z; z[3] += x.w;
+      if constexpr (GATED) {
+        const float4 y = part[w][NB - 1][i][lane];
+        u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+      }
+    }
+    const int m = 16 * i + r, n = n0 + (lane >> 4) * 4;
+    if (m < M && n < g.e.N) finish4<F16, GATED>(g.e, m, n, z, u);
+  }
+}
+
+// --- gradients: dz and transposed copies ---------------------------------------
+
+struct DzArgs {
+  const void* d_out;      // [M, N]
+  const uint16_t* pre;    // [M, N or 2N]
+  uint16_t* dz;           // [M, ldz] or null
+  uint16_t* dzt;          // [N or 2N, mp] or null
+  float* sums;            // [mp / 64][N or 2N] column sums of 64 rows each, or null
+  int64_t M, ldd, ldp, ldz, mp;
+  int N, act, d_f32, vec;
+};
+
+// 64 rows x 64 columns a workgroup: thread t forms row t / 4, columns 16 (t % 4)
+// .. + 15.  Rows past M and columns past N (up to ldz, a multiple of 8) are
+// zeros in both copies.
+template <bool F16>
+__global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
+  __shared__ float tile[64][65];
+  const int tid = threadIdx.x;
+  const int64_t m0 = (int64_t)blockIdx.y * 64;
+  const int n0 = blockIdx.x * 64;
+  const int r = tid / 4, c0 = (tid % 4) * 16;
+  const int64_t m = m0 + r;
+  const bool gated = a.act == MOE_ACT_SWIGLU;
+  const int halves = gated ? 2 : 1;
+  float g[16], p[16], u[16];
+#pragma unroll
+  for (int c = 0; c < 16; c += 4) {
+    const int n = n0 + c0 + c;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+    if (m < a.M && n < a.N) {
+      const int left = a.N - n;
+      if (a.d_f32) {
+        const float* s = (const float*)a.d_out + m * a.ldd + n;
+        if (a.vec) {
+          const float4 q = *(const float4*)s;
+          v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < left) v[i] = s[i];
+        }
+      } else {
+        load4<F16>((const uint16_t*)a.d_out + m * a.ldd + n, left, a.vec, v);
+      }
+      if (a.act != MOE_ACT_NONE) load4<F16>(a.pre + m * a.ldp + n, left, a.vec, x);
+      if (gated) load4<F16>(a.pre + m * a.ldp + a.N + n, left, a.vec, y);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { g[c + i] = v[i]; p[c + i] = x[i]; u[c + i] = y[i]; }
+  }
+  for (int h = 0; h < halves; ++h) {
+    if (h) __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      float d;
+      if (gated) d = h == 0 ? g[c] * u[c] * slope(MOE_ACT_SILU, p[c]) : g[c] * (p[c] * logistic(p[c]));
+      else d = a.act == MOE_ACT_NONE ? g[c] : g[c] * slope(a.act, p[c]);
+      // outside the matrix there is no gradient, whatever the slope at 0
+      tile[r][c0 + c] = m < a.M && n0 + c0 + c < a.N ? d : 0.f;
+    }
+    __syncthreads();
+    const int64_t first = (int64_t)h * a.N;   // column of the half's start
+    if (a.sums && tid < 64 && n0 + tid < a.N) {
+      float s = 0.f;
+      for (int i = 0; i < 64; ++i) s += tile[i][tid];
+      a.sums[blockIdx.y * (int64_t)halves * a.N + first + n0 + tid] = s;
+    }
+    // 8 values of one row (dz) or column (its transpose) a store, 64 x 8 stores
+    for (int i = tid; i < 512; i += 256) {
+      const int row = i / 8, part8 = (i % 8) * 8;
+      if (a.dz && m0 + row < a.M) {
+        uint16_t* d = a.dz + (m0 + row) * a.ldz + first + n0 + part8;
+        uint16_t b[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) b[c] = Elem<F16>::bits(tile[row][part8 + c]);
+        const int64_t end = h + 1 < halves ? (int64_t)a.N - n0 - part8 : a.ldz - first - n0 - part8;   // columns that are this half's
+        if (end >= 8 && (first & 7) == 0) {
+          *(uint4*)d = make_uint4(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16, b[4] | (uint32_t)b[5] << 16, b[6] | (uint32_t)b[7] << 16);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < end) d[c] = b[c];
+        }
+      }
+      if (a.dzt && n0 + row < a.N) {
+        uint16_t b[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) b[c] = Elem<F16>::bits(tile[part8 + c][row]);
+        *(uint4*)(a.dzt + (first + n0 + row) * a.mp + m0 + part8) =
+            make_uint4(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16, b[4] | (uint32_t)b[5] << 16, b[6] | (uint32_t)b[7] << 16);
+      }
+    }
+  }
+}
+
+// bias gradient: the column sums' rows added in order
+template <bool F16>
+__global__ __launch_bounds__(256) void bias_grad_kernel(const float* sums, int rows, int64_t cols, uint16_t* out) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= cols) return;
+  float s = 0.f;
+  for (int i = 0; i < rows; ++i) s += sums[i * cols + n];
+  out[n] = Elem<F16>::bits(s);
+}
+
+// out[c][r] = in[r][c], 16-bit values, cols a multiple of 8; rows from R up to
+// the output's pitch (a multiple of 64) are zeros
+__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* in, int64_t ld, int64_t R, int cols,
+                                                        uint16_t* out, int64_t pitch) {
+  __shared__ uint16_t tile[64][66];
+  const int tid = threadIdx.x;
+  const int64_t r0 = (int64_t)blockIdx.y * 64;
+  const int c0 = blockIdx.x * 64;
+  for (int i = tid; i < 512; i += 256) {
+    const int row = i / 8, c = (i % 8) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r0 + row < R && c0 + c < cols) v = *(const uint4*)(in + (r0 + row) * ld + c0 + c);
+    uint32_t* d = (uint32_t*)&tile[row][c];
+    d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+  }
+  __syncthreads();
+  for (int i = tid; i < 512; i += 256) {
+    const int col = i / 8, r = (i % 8) * 8;
+    if (c0 + col >= cols) continue;
+    uint16_t b[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) b[c] = tile[r + c][col];
+    *(uint4*)(out + (int64_t)(c0 + col) * pitch + r0 + r) =
+        make_uint4(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16, b[4] | (uint32_t)b[5] << 16, b[6] | (uint32_t)b[7] << 16);
+  }
+}
+
+// --- host -------------------------------------------------------------------
+
+int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// How a product is cut: tile 0 = few rows, 1 = 64 x 128, 2 = 128 x 128,
+// 3 = 256 x 256 (a gated product's columns count twice), and the splits of K.
+struct Cut {
+  int tile, splits;
+  int64_t kper;
+};
+
+Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated) {
+  const int64_t NZ = gated ? 2 * N : N;
+  if (M <= 64) return {0, 1, round_up(K, kBK)};
+  // time of each choice from the rates one CU reaches with each tile and the
+  // cost of the partial sums' round trip; the smallest wins
+  static const int bm[4] = {0, 64, 128, 256}, bn[4] = {0, 128, 128, 256}, per_cu[4] = {0, 3, 2, 1};
+  static const double rate[4] = {0, 2.2e6, 3.4e6, 4.7e6};   // flop per us and CU
+  const int64_t steps = (K + kBK - 1) / kBK;
+  Cut best = {1, 1, round_up(K, kBK)};
+  double best_us = 1e30;
+  for (int t = 1; t <= 3; ++t) {
+    const int64_t tiles = ((M + bm[t] - 1) / bm[t]) * ((NZ + bn[t] - 1) / bn[t]);
+    for (int s = 1; s <= 32; s *= 2) {
+      if (s > 1 && steps < 4 * s) break;
+      const int64_t per = (steps + s - 1) / s;
+      const int64_t blocks = tiles * s, slots = (int64_t)kCus * per_cu[t];
+      const int64_t conc = blocks >= slots ? per_cu[t] : (blocks + kCus - 1) / kCus;
+      const double step_us = conc * 2.0 * bm[t] * bn[t] * kBK / rate[t];
+      double us = (double)((blocks + kCus * conc - 1) / (kCus * conc)) * (per * (step_us > 0.5 ? step_us : 0.5) + 2.0);
+      if (s > 1) us += 4.0 + (double)s * M * NZ * 8 / 3.5e6;
+      if (us < best_us) {
+        best_us = us;
+        best = {t, s, per * kBK};
+      }
+    }
+  }
+  best.splits = K > 0 ? (int)((K + best.kper - 1) / best.kper) : 1;
+  return best;
+}
+
+size_t part_bytes(const Cut& c, int64_t M, int64_t N, bool gated) {
+  return c.splits > 1 ? (size_t)c.splits * M * round_up(N, 4) * (gated ? 2 : 1) * 4 : 0;
+}
+
+template <class C, bool F16, bool GATED>
+void launch_tiles(ProdArgs& g, hipStream_t s) {
+  constexpr int HB = GATED ? C::BN / 2 : C::BN;
+  g.n_mt = (int)((g.e.M + C::BM - 1) / C::BM);
+  g.n_nt = (g.e.N + HB - 1) / HB;
+  const unsigned grid = (unsigned)((int64_t)g.n_mt * g.n_nt * g.splits);
+  if (g.splits == 1) {
+    hipLaunchKernelGGL((product_kernel<C, F16, GATED, false>), dim3(grid), dim3(C::NT), 0, s, g);
+    return;
+  }
+  hipLaunchKernelGGL((product_kernel<C, F16, GATED, true>), dim3(grid), dim3(C::NT), 0, s, g);
+  const int64_t blocks = (g.e.M * ((g.e.N + 3) / 4) + 255) / 256;
+  hipLaunchKernelGGL((join_kernel<F16, GATED>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, g);
+}
+
+template <bool F16, bool GATED>
+hipError_t launch_product(ProdArgs& g, const Cut& c, void* ws, hipStream_t s) {
+  if (g.e.M == 0) return hipSuccess;
+  g.kper = c.kper;
+  g.splits = c.splits;
+  g.part = (float*)ws;
+  g.up_col = (int)round_up(g.e.N, 4);
+  g.pitch = (int64_t)g.up_col * (GATED ? 2 : 1);
+  if (c.tile == 0) {
+    const dim3 grid((unsigned)((g.e.N + 15) / 16)), block(kFewWaves * 64);
+    if (g.e.M <= 16) hipLaunchKernelGGL((few_rows_kernel<1, F16, GATED>), grid, block, 0, s, g);
+    else if (g.e.M <= 32) hipLaunchKernelGGL((few_rows_kernel<2, F16, GATED>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((few_rows_kernel<4, F16, GATED>), grid, block, 0, s, g);
+  } else if (c.tile == 1) {
+    launch_tiles<Tile64, F16, GATED>(g, s);
+  } else if (c.tile == 2) {
+    launch_tiles<Tile128, F16, GATED>(g, s);
+  } else {
+    launch_tiles<std::conditional_t<GATED, Tile256G, Tile256>, F16, GATED>(g, s);
+  }
+  return hipGetLastError();
+}
+
+bool gated(const moe_linear_desc& d) { return d.act == MOE_ACT_SWIGLU; }
+
+hipError_t run_product(ProdArgs& g, bool f16, bool gate, const Cut& c, void* ws, hipStream_t s) {
+  if (f16) return gate ? launch_product<true, true>(g, c, ws, s) : launch_product<true, false>(g, c, ws, s);
+  return gate ? launch_product<false, true>(g, c, ws, s) : launch_product<false, false>(g, c, ws, s);
+}
+
+// Workspace of the backward pass, in bytes (pieces 256-byte aligned).
+struct BackLayout {
+  int64_t NZ, ldz, mp, np;
+  Cut dx, dw;
+  size_t dz, dzt, xt, wt, sums, part, total;
+};
+BackLayout back_layout(const moe_linear_desc& d) {
+  BackLayout L;
+  L.NZ = (int64_t)d.cols * (gated(d) ? 2 : 1);
+  L.ldz = round_up(L.NZ, 8);
+  L.np = round_up(L.NZ, 64);
+  L.mp = round_up(d.rows, 64);
+  L.dx = choose_cut(d.rows, d.depth, L.ldz, false);
+  L.dw = choose_cut(L.NZ, d.depth, L.mp, false);
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off += (size_t)round_up((int64_t)n, 256);
+    return at;
+  };
+  L.dz = take((size_t)d.rows * L.ldz * 2);
+  L.dzt = take((size_t)L.NZ * L.mp * 2);
+  L.xt = take((size_t)d.depth * L.mp * 2);
+  L.wt = take((size_t)d.depth * L.np * 2);
+  L.sums = take((size_t)(L.mp / 64) * L.NZ * 4);
+  const size_t p1 = part_bytes(L.dx, d.rows, d.depth, false), p2 = part_bytes(L.dw, L.NZ, d.depth, false);
+  L.part = take(p1 > p2 ? p1 : p2);
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+
+size_t linear_ws_bytes(const moe_linear_desc& d) {
+  return part_bytes(choose_cut(d.rows, d.cols, d.depth, gated(d)), d.rows, d.cols, gated(d));
+}
+
+size_t linear_back_ws_bytes(const moe_linear_desc& d) { return back_layout(d).total; }
+
+hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void* ws, hipStream_t s) {
+  ProdArgs g;
+  g.a = (const uint16_t*)b.x;
+  g.b = (const uint16_t*)b.w;
+  g.lda = d.ld_x;
+  g.ldb = d.ld_w;
+  g.K = d.depth;
+  Epilogue& e = g.e;
+  e.bias = (const uint16_t*)b.bias;
+  e.res = b.residual;
+  e.pre = (uint16_t*)b.pre;
+  e.out = b.out;
+  e.M = d.rows; e.N = d.cols;
+  e.ldr = d.ld_residual; e.ldp = d.ld_pre; e.ldo = d.ld_out;
+  e.act = d.act;
+  e.out_f32 = d.out_dtype == MOE_F32;
+  const size_t o = e.out_f32 ? 16 : 8;
+  e.vec = d.cols % 4 == 0 && e.ldo % 4 == 0 && aligned_to(b.out, o) && aligned_to(b.bias, 8) &&
+          (!b.residual || (e.ldr % 4 == 0 && aligned_to(b.residual, o))) &&
+          (!b.pre || (e.ldp % 4 == 0 && aligned_to(b.pre, 8)));
+  return run_product(g, d.dtype == MOE_F16, gated(d), choose_cut(d.rows, d.cols, d.depth, gated(d)), ws, s);
+}
+
+hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b, void* ws, hipStream_t s) {
+  const BackLayout L = back_layout(d);
+  char* base = (char*)ws;
+  const bool f16 = d.dtype == MOE_F16, f32 = d.out_dtype == MOE_F32;
+  uint16_t* dz = (uint16_t*)(base + L.dz);
+  uint16_t* dzt = (uint16_t*)(base + L.dzt);
+  // without an activation the incoming gradient can be the operand itself
+  const bool direct = d.act == MOE_ACT_NONE && !f32 && d.cols % 8 == 0 && d.ld_out % 8 == 0 && aligned_to(b.d_out, 16);
+  const bool want_dz = b.dx && !direct;
+  if (d.rows > 0 && (want_dz || b.dw || b.dbias)) {
+    DzArgs a;
+    a.d_out = b.d_out;
+    a.pre = (const uint16_t*)b.pre;
+    a.dz = want_dz ? dz : nullptr;
+    a.dzt = b.dw ? dzt : nullptr;
+    a.sums = b.dbias ? (float*)(base + L.sums) : nullptr;
+    a.M = d.rows; a.N = d.cols;
+    a.ldd = d.ld_out; a.ldp = d.ld_pre; a.ldz = L.ldz; a.mp = L.mp;
+    a.act = d.act;
+    a.d_f32 = f32;
+    a.vec = d.cols % 4 == 0 && a.ldd % 4 == 0 && aligned_to(b.d_out, f32 ? 16 : 8) &&
+            (d.act == MOE_ACT_NONE || (a.ldp % 4 == 0 && aligned_to(b.pre, 8)));
+    // the up half's columns may start anywhere, and so end up to 7 past N
+    const dim3 grid((unsigned)((d.cols + (gated(d) ? 7 : 0) + 63) / 64), (unsigned)(L.mp / 64));
+    if (f16) hipLaunchKernelGGL((dz_kernel<true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((dz_kernel<false>), grid, dim3(256), 0, s, a);
+  }
+  if (b.dbias) {
+    const dim3 grid((unsigned)((L.NZ + 255) / 256));
+    const int rows = (int)(L.mp / 64);
+    if (f16) hipLaunchKernelGGL((bias_grad_kernel<true>), grid, dim3(256), 0, s, (const float*)(base + L.sums), rows, L.NZ, (uint16_t*)b.dbias);
+    else hipLaunchKernelGGL((bias_grad_kernel<false>), grid, dim3(256), 0, s, (const float*)(base + L.sums), rows, L.NZ, (uint16_t*)b.dbias);
+  }
+  hipError_t rc = hipGetLastError();
+  if (rc != hipSuccess) return rc;
+  ProdArgs g;
+  Epilogue& e = g.e;
+  e.bias = nullptr; e.res = nullptr; e.pre = nullptr;
+  e.ldr = e.ldp = 0;
+  e.act = MOE_ACT_NONE;
+  e.out_f32 = 0;
+  e.N = d.depth;
+  if (b.dx && d.rows > 0) {
+    uint16_t* wt = (uint16_t*)(base + L.wt);
+    const dim3 grid((unsigned)((d.depth + 63) / 64), (unsigned)(L.np / 64));
+    hipLaunchKernelGGL(transpose_kernel, grid, dim3(256), 0, s, (const uint16_t*)b.w, d.ld_w, L.NZ, d.depth, wt, L.np);
+    g.a = direct ? (const uint16_t*)b.d_out : dz;
+    g.lda = direct ? d.ld_out : L.ldz;
+    g.b = wt;
+    g.ldb = L.np;
+    g.K = L.ldz;
+    e.M = d.rows;
+    e.out = b.dx;
+    e.ldo = d.ld_dx;
+    e.vec = e.ldo % 4 == 0 && aligned_to(b.dx, 8);
+    rc = run_product(g, f16, false, L.dx, base + L.part, s);
+    if (rc != hipSuccess) return rc;
+  }
+  if (b.dw) {
+    uint16_t* xt = (uint16_t*)(base + L.xt);
+    if (d.rows > 0) {
+      const dim3 grid((unsigned)((d.depth + 63) / 64), (unsigned)(L.mp / 64));
+      hipLaunchKernelGGL(transpose_kernel, grid, dim3(256), 0, s, (const uint16_t*)b.x, d.ld_x, d.rows, d.depth, xt, L.mp);
+    }
+    g.a = dzt;
+    g.lda = L.mp;
+    g.b = xt;
+    g.ldb = L.mp;
+    g.K = L.mp;
+    e.M = L.NZ;
+    e.out = b.dw;
+    e.ldo = d.ld_dw;
+    e.vec = e.ldo % 4 == 0 && aligned_to(b.dw, 8);
+    rc = run_product(g, f16, false, L.dw, base + L.part, s);
+  }
+  return rc;
+}
+
+}  // namespace moe

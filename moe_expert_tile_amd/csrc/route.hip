@@ -1,0 +1,670 @@
+// Routing: router logits -> the top-k expert ids and gate weights that the
+// plan and the scale step take (include/moe.h, moe_route), and the gradient
+// of the weights with respect to the logits (moe_route_backward).
+//
+// Forward.  A row of logits is held by LPR lanes of a wavefront, VPL values
+// each, so 64 / LPR tokens go through a wavefront at once.  The lanes of a row
+// are divided among its expert groups (each group has the same number of
+// lanes), which makes a group's best scores a reduction over neighbouring
+// lanes.  Every value becomes a 64-bit key that orders by (value descending,
+// expert ascending) as a double: a float has 24 significant bits, so a double
+// leaves 29 below them for the expert's index.  Each lane sorts its keys with
+// a fixed network of v_max_f64 / v_min_f64; then every pick is the largest
+// head over the row's lanes, and the lane that held it moves its list up.
+//
+// Which values are ranked.  Without a bias the scores are an increasing
+// function of the logits, so the logits themselves are ranked, exactly.  With
+// a bias (or where groups are ranked by sums of scores) c = s + b is ranked in
+// 32 bits; where two values that decide something lie closer than the error of
+// that, the row is ranked again in 64 bits (exact_row), one row at a time by
+// the whole wavefront.
+#include <type_traits>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRouteThreads = 256;
+// a sigmoid below this logit counts as 0 (its value would be below 2^-1009),
+// so that masking with a type's lowest value leaves renormalised weights of 0
+constexpr float kSigmoidZero = -700.0f;
+
+__device__ __forceinline__ float load_as_float(const void* p, int dtype, int64_t i) {
+  if (dtype == MOE_F32) return ((const float*)p)[i];
+  if (dtype == MOE_BF16) return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
+  return (float)((const _Float16*)p)[i];
+}
+
+__device__ __forceinline__ void load4_as_float(const void* p, int dtype, int64_t i, float (&v)[4]) {
+  if (dtype == MOE_F32) {
+    const float4 x = *(const float4*)((const float*)p + i);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else if (dtype == MOE_BF16) {
+    const uint2 x = *(const uint2*)((const uint16_t*)p + i);
+    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+  } else {
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    const f16x4 x = *(const f16x4*)((const _Float16*)p + i);
+    v[0] = (float)x[0]; v[1] = (float)x[1]; v[2] = (float)x[2]; v[3] = (float)x[3];
+  }
+}
+
+// 32-bit lane exchange across the lanes of a row, step S of an all-reduce:
+// after steps 1, 2, 4, ... the operands are uniform over ever larger blocks,
+// so any exchange between the two halves of a block will do (mirrors here)
+template <int S>
+__device__ __forceinline__ uint32_t swap_step(uint32_t v) {
+  if constexpr (S == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);        // quad_perm 1 0 3 2
+  else if constexpr (S == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);   // quad_perm 2 3 0 1
+  else if constexpr (S == 4) return __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);  // row_half_mirror
+  else if constexpr (S == 8) return __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);  // row_mirror
+  else return (uint32_t)__shfl_xor((int)v, S);
+}
+template <int S>
+__device__ __forceinline__ float swap_step(float v) {
+  return __uint_as_float(swap_step<S>(__float_as_uint(v)));
+}
+template <int S>
+__device__ __forceinline__ double swap_step(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = swap_step<S>((uint32_t)b), hi = swap_step<S>((uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (hi << 32) | lo);
+}
+
+// keys are never NaN, so the bare instructions do (the compiler's fmax first
+// quiets both operands, two more instructions)
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
+template <int N, int S = 1, class F, class V>
+__device__ __forceinline__ V reduce_lanes(V v, F f) {
+  if constexpr (S < N) return reduce_lanes<N, 2 * S>(f(v, swap_step<S>(v)), f);
+  else return v;
+}
+template <int N> __device__ __forceinline__ float max_lanes(float v) {
+  return reduce_lanes<N>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int N> __device__ __forceinline__ float sum_lanes(float v) {
+  return reduce_lanes<N>(v, [](float a, float b) { return a + b; });
+}
+// the same over a block of `n` lanes of the row, n a power of two at most N
+template <int N, int S = 1, class F, class V>
+__device__ __forceinline__ V reduce_block(V v, int n, F f) {
+  if constexpr (S < N) {
+    if (S < n) v = f(v, swap_step<S>(v));
+    return reduce_block<N, 2 * S>(v, n, f);
+  } else {
+    return v;
+  }
+}
+
+// keys: a float's 24 bits, then the expert index so that among equal values
+// the lower one is larger; infinities become finite so that their low bits
+// hold an index too.  A masked expert has the value -inf, a lane's place
+// without an expert lies below all of them.
+constexpr double kKeyInf = 0x1p1000, kKeyAbsent = -0x1p1010;
+__device__ __forceinline__ double make_key(float v, int idx) {
+  v += 0.0f;   // -0 as +0
+  double d = (double)v;
+  if (v == __builtin_inff()) d = kKeyInf;
+  if (v == -__builtin_inff()) d = -kKeyInf;
+  uint64_t b = __builtin_bit_cast(uint64_t, d);
+  b |= (uint32_t)(v >= 0.0f ? 1023 - idx : idx);
+  return __builtin_bit_cast(double, b);
+}
+__device__ __forceinline__ int key_index(double k) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, k);
+  const int low = (int)(b & 1023);
+  return (b >> 63) ? low : 1023 - low;
+}
+__device__ __forceinline__ float key_value(double k) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, k) & ~(uint64_t)1023;
+  return (float)__builtin_bit_cast(double, b);   // +-kKeyInf round to infinities
+}
+
+// descending sort of N = 2^n values in registers (Batcher's odd-even merges)
+template <int N>
+__device__ __forceinline__ void sort_desc(double (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2) {
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2) {
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q) {
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const double a = v[i + j], b = v[i + j + q];
+            v[i + j] = max64(a, b);
+            v[i + j + q] = min64(a, b);
+          }
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  int32_t* ids;
+  float* w;
+  int64_t T, ld;
+  int E, k, dtype, score, renorm, groups, gsize, keep, top2;
+  float scale;
+  int lpg;       // lanes per group (a power of two)
+  int vec;       // four values a load: group size and row pitch multiples of 4, the base aligned
+};
+
+// One row ranked in 64 bits by the whole wavefront, c in LDS (E doubles, then
+// groups doubles): the picks go to `pick` (expert, or expert | 1 << 16 for a
+// masked one).  Slow and rare; it holds few registers.
+__device__ __forceinline__ void exact_row(const RouteArgs& a, int64_t t, double* c, double* gs, int* pick) {
+  const int lane = threadIdx.x & 63;
+  const int64_t base = t * a.ld;
+  double m = -__builtin_inf();
+  double sum = 1.0;
+  if (a.score == MOE_SCORE_SOFTMAX) {
+    for (int e = lane; e < a.E; e += 64) m = fmax(m, (double)load_as_float(a.logits, a.dtype, base + e));
+    for (int s = 32; s; s >>= 1) m = fmax(m, __shfl_xor(m, s));
+    sum = 0.0;
+    for (int e = lane; e < a.E; e += 64) sum += exp((double)load_as_float(a.logits, a.dtype, base + e) - m);
+    for (int s = 32; s; s >>= 1) sum += __shfl_xor(sum, s);
+  }
+  for (int e = lane; e < a.E; e += 64) {
+    const double z = (double)load_as_float(a.logits, a.dtype, base + e);
+    const double s = a.score == MOE_SCORE_SOFTMAX ? exp(z - m) / sum : 1.0 / (1.0 + exp(-z));
+    double v = a.bias ? s + (double)a.bias[e] : s;
+    if (z == -__builtin_inf() || !(v == v)) v = -__builtin_inf();
+    c[e] = v;
+  }
+  __builtin_amdgcn_wave_barrier();
+  __threadfence_block();
+  if (a.groups > 1) {
+    for (int g = lane; g < a.groups; g += 64) {
+      double b1 = -__builtin_inf(), b2 = -__builtin_inf();
+      for (int i = 0; i < a.gsize; ++i) {
+        const double v = c[g * a.gsize + i];
+        if (v > b1) { b2 = b1; b1 = v; } else if (v > b2) { b2 = v; }
+      }
+      gs[g] = a.top2 ? b1 + b2 : b1;
+    }
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+    for (int e = lane; e < a.E; e += 64) {
+      const int g = e / a.gsize;
+      int better = 0;
+      for (int o = 0; o < a.groups; ++o) better += (gs[o] > gs[g] || (gs[o] == gs[g] && o < g)) ? 1 : 0;
+      if (better >= a.keep) c[e] = -__builtin_inf();
+    }
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+  }
+  // picks: largest c, ties to the lower expert; a taken expert becomes NaN,
+  // which no comparison prefers
+  for (int j = 0; j < a.k; ++j) {
+    double bv = 0.0;
+    int be = 1 << 20;   // none yet
+    for (int e = lane; e < a.E; e += 64) {
+      const double v = c[e];
+      if (v == v && (be == (1 << 20) || v > bv)) { bv = v; be = e; }
+    }
+    for (int s = 32; s; s >>= 1) {
+      const double ov = __shfl_xor(bv, s);
+      const int oe = __shfl_xor(be, s);
+      const bool take = oe != (1 << 20) && (be == (1 << 20) || ov > bv || (ov == bv && oe < be));
+      if (take) { bv = ov; be = oe; }
+    }
+    if (lane == 0) {
+      pick[j] = be | (bv == -__builtin_inf() ? 1 << 16 : 0);
+      c[be] = __builtin_nan("");
+    }
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+  }
+}
+
+// LPR lanes a row, VPL values a lane, at most KMAX picks; BYC: c = s + b is
+// ranked (else the logits)
+template <int LPR, int VPL, int KMAX, bool BYC>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  constexpr int RPW = 64 / LPR;                       // rows a wavefront
+  constexpr int LOOK = KMAX + (BYC ? 1 : 0);          // picks looked at: with BYC the first one left out too
+  constexpr int NS = (LOOK + LPR - 1) / LPR;          // picks a lane keeps
+  constexpr int DEPTH = VPL < LOOK ? VPL : LOOK;      // places of the sorted list they can come from
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l = lane % LPR;                           // lane within the row
+  const int g = l / a.lpg, sub = l % a.lpg;
+  constexpr float kInf = __builtin_inff();
+  const int64_t waves = (int64_t)gridDim.x * (kRouteThreads / 64);
+  for (int64_t t0 = ((int64_t)blockIdx.x * (kRouteThreads / 64) + wave) * RPW; t0 < a.T; t0 += waves * RPW) {
+    const int64_t t = t0 + lane / LPR;
+    const bool live = t < a.T;
+    // place i of this lane: expert g * gsize + p(i)
+    auto place = [&](int i) { return (i / 4) * 4 * a.lpg + sub * 4 + (i & 3); };
+    float z[VPL];
+    const bool lane_on = live && g < a.groups;
+    const int64_t base = t * a.ld + (int64_t)g * a.gsize;
+    if (a.vec) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += 4) {
+        float v[4] = {-kInf, -kInf, -kInf, -kInf};
+        if (lane_on && place(i) < a.gsize) load4_as_float(a.logits, a.dtype, base + place(i), v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) z[i + c] = v[c];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        z[i] = lane_on && place(i) < a.gsize ? load_as_float(a.logits, a.dtype, base + place(i)) : -kInf;
+    }
+    // a NaN logit (or bias), or +inf under a softmax, has no weights: the
+    // row's are NaN, its ids still k distinct experts
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      bad |= !(z[i] == z[i]) || (a.score == MOE_SCORE_SOFTMAX && z[i] == kInf);
+      if (!(z[i] == z[i])) z[i] = -kInf;
+    }
+    // the softmax's maximum and sum, where full scores are wanted
+    float zmax = 0.f, zsum = 1.f;
+    const bool full = a.score == MOE_SCORE_SOFTMAX && (BYC || !a.renorm);
+    if (full) {
+      float m = z[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, z[i]);
+      m = max_lanes<LPR>(m);
+      zmax = m == -kInf ? 0.f : m;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s += exp_fast(z[i] - zmax);
+      zsum = fmaxf(sum_lanes<LPR>(s), 1e-30f);   // every expert masked: zero scores
+    }
+    // what is ranked: the logits, or c
+    float v[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if constexpr (BYC) {
+        const float s = a.score == MOE_SCORE_SOFTMAX ? exp_fast(z[i] - zmax) / zsum : 1.0f / (1.0f + exp_fast(-z[i]));
+        float c = s;
+        if (a.bias && lane_on && place(i) < a.gsize) c += a.bias[g * a.gsize + place(i)];
+        bad |= z[i] != -kInf && !(c == c);
+        v[i] = (z[i] == -kInf || !(c == c)) ? -kInf : c;
+      } else {
+        v[i] = z[i];
+      }
+    }
+    bool near = false;   // BYC: a decision closer than the error of 32 bits
+    auto close = [](float hi, float lo) { return hi - lo <= 0x1p-18f * fmaxf(1.0f, fabsf(hi)); };
+    bool kept = true;
+    if (a.groups > 1) {
+      float b1 = -kInf, b2 = -kInf;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float x = place(i) < a.gsize ? v[i] : -kInf;
+        b2 = fmaxf(b2, fminf(b1, x));
+        b1 = fmaxf(b1, x);
+      }
+      auto merge = [&](auto tag) {
+        constexpr int S = decltype(tag)::value;
+        if (S < a.lpg) {
+          const float o1 = swap_step<S>(b1), o2 = swap_step<S>(b2);
+          b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+          b1 = fmaxf(b1, o1);
+        }
+      };
+      merge(std::integral_constant<int, 1>{});
+      if constexpr (LPR > 2) merge(std::integral_constant<int, 2>{});
+      if constexpr (LPR > 4) merge(std::integral_constant<int, 4>{});
+      if constexpr (LPR > 8) merge(std::integral_constant<int, 8>{});
+      if constexpr (LPR > 16) merge(std::integral_constant<int, 16>{});
+      if constexpr (LPR > 32) merge(std::integral_constant<int, 32>{});
+      const float sc = a.top2 ? b1 + b2 : b1;
+      int better = 0;
+      for (int o = 0; o < a.groups; ++o) {
+        const float os = __shfl(sc, (lane - l) + o * a.lpg);
+        better += (os > sc || (os == sc && o < g)) ? 1 : 0;
+      }
+      kept = g < a.groups && better < a.keep;
+      if constexpr (BYC) {
+        // lowest kept and highest dropped group; infinities differ by NaN or
+        // by infinity and so are never close
+        const float lo = -max_lanes<LPR>(kept ? -sc : -kInf);
+        const float hi = max_lanes<LPR>(!kept && g < a.groups ? sc : -kInf);
+        near |= close(lo, hi);
+      }
+    }
+    double key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      key[i] = g < a.groups && place(i) < a.gsize ? make_key(kept ? v[i] : -kInf, g * a.gsize + place(i)) : kKeyAbsent;
+    sort_desc<VPL>(key);
+
+    double slot[NS];
+#pragma unroll
+    for (int r = 0; r < NS; ++r) slot[r] = kKeyAbsent;
+    const int picks = BYC && a.k < a.E ? a.k + 1 : a.k;   // one more to see how near the first one left out lies
+    for (int j = 0; j < picks; ++j) {
+      const double best = reduce_lanes<LPR>(key[0], [](double x, double y) { return max64(x, y); });
+#pragma unroll
+      for (int r = 0; r < NS; ++r)
+        if (j == r * LPR + l) slot[r] = best;
+      const bool mine = key[0] == best;
+#pragma unroll
+      for (int i = 0; i + 1 < DEPTH; ++i) key[i] = mine ? key[i + 1] : key[i];
+      // the list's last place: once it has been picked nothing is left in it
+      if constexpr (DEPTH == VPL) key[DEPTH - 1] = mine ? kKeyAbsent : key[DEPTH - 1];
+    }
+    int pick[NS];
+#pragma unroll
+    for (int r = 0; r < NS; ++r)
+      pick[r] = key_index(slot[r]) | (key_value(slot[r]) == -kInf ? 1 << 16 : 0);
+    if constexpr (BYC) {
+      // neighbours in the order that are close, unless their logits and
+      // biases are the same and the index decides (zero biases over 16-bit
+      // logits are full of those)
+      float pc = kInf, pz = 0.f, pb = 0.f;   // the last lane's pick of the previous round
+#pragma unroll
+      for (int r = 0; r < NS; ++r) {
+        const int j = r * LPR + l;
+        const bool on = live && j < picks;
+        const float c = key_value(slot[r]);
+        const float zj = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : 0.f;
+        const float bj = on && a.bias ? a.bias[pick[r] & 0xffff] : 0.f;
+        float qc = __shfl_up(c, 1, LPR), qz = __shfl_up(zj, 1, LPR), qb = __shfl_up(bj, 1, LPR);
+        if (l == 0) { qc = pc; qz = pz; qb = pb; }
+        near |= on && j > 0 && close(qc, c) && !(qz == zj && qb == bj);
+        if constexpr (NS > 1) {
+          pc = __shfl(c, LPR - 1, LPR);
+          pz = __shfl(zj, LPR - 1, LPR);
+          pb = __shfl(bj, LPR - 1, LPR);
+        }
+      }
+      near = max_lanes<LPR>(near ? 1.f : 0.f) > 0.f;
+      double* cbuf = (double*)smem + (size_t)wave * (a.E + a.groups + 16 + 1);
+      double* gbuf = cbuf + a.E;
+      int* pbuf = (int*)(gbuf + a.groups);
+      uint64_t todo = __ballot(near && live && l == 0);
+      while (todo) {
+        const int at = __ffsll((unsigned long long)todo) - 1;
+        todo &= todo - 1;
+        exact_row(a, t0 + at / LPR, cbuf, gbuf, pbuf);
+        if (lane / LPR == at / LPR) {
+#pragma unroll
+          for (int r = 0; r < NS; ++r)
+            if (r * LPR + l < a.k) pick[r] = pbuf[r * LPR + l];
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+    // weights of the picks
+    float p[NS], zs[NS];
+    bool nan_row = max_lanes<LPR>(bad ? 1.f : 0.f) > 0.f;
+    float top = -kInf;
+#pragma unroll
+    for (int r = 0; r < NS; ++r) {
+      const bool on = live && r * LPR + l < a.k && !(pick[r] >> 16);
+      if constexpr (BYC) zs[r] = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : -kInf;
+      else zs[r] = on ? key_value(slot[r]) : -kInf;
+      top = fmaxf(top, zs[r]);
+    }
+    float total = 0.f;
+    if (a.renorm) {
+      // the weights' ratios need no common factor: the softmax's maximum is
+      // taken over the picks, and sigmoids of far negative logits are scaled
+      // up by e^-top, so that the sum does not vanish in 32 bits
+      top = max_lanes<LPR>(top);
+      const float shift = a.score == MOE_SCORE_SOFTMAX ? (top == -kInf ? 0.f : top) : fminf(0.f, top == -kInf ? 0.f : top);
+#pragma unroll
+      for (int r = 0; r < NS; ++r) {
+        float q;
+        if (zs[r] == -kInf) q = 0.f;
+        else if (a.score == MOE_SCORE_SOFTMAX) q = expf(zs[r] - shift);
+        else if (zs[r] < kSigmoidZero) q = 0.f;
+        else q = zs[r] > 0.f ? 1.0f / (1.0f + expf(-zs[r])) : expf(zs[r] - shift) / (1.0f + expf(zs[r]));
+        p[r] = q;
+        total += q;
+      }
+      total = sum_lanes<LPR>(total);
+    } else {
+#pragma unroll
+      for (int r = 0; r < NS; ++r) {
+        if (zs[r] == -kInf) p[r] = 0.f;
+        else if (a.score == MOE_SCORE_SOFTMAX) p[r] = expf(zs[r] - zmax) / zsum;
+        else p[r] = 1.0f / (1.0f + expf(-zs[r]));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NS; ++r) {
+      const int j = r * LPR + l;
+      if (live && j < a.k) {
+        float wj = a.renorm ? (total > 0.f ? p[r] / total : 0.f) : p[r];
+        wj *= a.scale;
+        a.ids[t * a.k + j] = pick[r] & 0xffff;
+        a.w[t * a.k + j] = nan_row ? __builtin_nanf("") : wj;
+      }
+    }
+  }
+}
+
+// --- backward ---------------------------------------------------------------
+//
+// ids, a bias and slots of weight 0 are constants.  With p the weights before
+// the factor, S their sum and g the gradient of the weights:
+//   softmax, renormalised:  dz_j = w_j (g_j - D / scale),      D = sum_i g_i w_i
+//   softmax:                dz_e = [e = id_j] w_j g_j - s_e D
+//   sigmoid, renormalised:  dz_j = w_j (1 - s_j) (g_j - D / scale)
+//   sigmoid:                dz_j = w_j (1 - s_j) g_j
+// (a sigmoid's slope is s (1 - s), and 1 - s_j = 1 / (1 + e^z_j)).  So only
+// the full softmax reads whole rows of logits; the others read k of them.
+// A wavefront builds its rows in LDS (zeros, then the k values, summed in slot
+// order where an expert is listed twice) and writes them out whole.
+struct RouteBackArgs {
+  const void* logits;
+  const int32_t* ids;
+  const float* w;
+  const float* dw;
+  void* dz;
+  int64_t T, ld, ldd;
+  int E, k, dtype, score, renorm;
+  float scale;
+  int rows;   // rows a wavefront builds at once, at most 64 / SL
+  int pitch;  // floats between them in LDS
+  int vec;    // four values a store (E, ld, ldd multiples of 4, bases aligned)
+};
+
+__device__ __forceinline__ void store_as(void* p, int dtype, int64_t i, float v) {
+  if (dtype == MOE_F32) ((float*)p)[i] = v;
+  else if (dtype == MOE_BF16) ((__bf16*)p)[i] = (__bf16)v;
+  else ((_Float16*)p)[i] = (_Float16)v;
+}
+__device__ __forceinline__ void store4_as(void* p, int dtype, int64_t i, const float4& v) {
+  if (dtype == MOE_F32) {
+    *(float4*)((float*)p + i) = v;
+  } else if (dtype == MOE_BF16) {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    *(bf16x4*)((__bf16*)p + i) = bf16x4{(__bf16)v.x, (__bf16)v.y, (__bf16)v.z, (__bf16)v.w};
+  } else {
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    *(f16x4*)((_Float16*)p + i) = f16x4{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
+  }
+}
+
+// SL lanes hold the slots of a row (k <= SL)
+template <int SL>
+__global__ __launch_bounds__(kRouteThreads) void route_back_kernel(RouteBackArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float* tile = (float*)smem + (size_t)wave * a.rows * a.pitch;
+  const int64_t waves = (int64_t)gridDim.x * (kRouteThreads / 64);
+  const int row = lane / SL, j = lane % SL;
+  constexpr float kInf = __builtin_inff();
+  for (int64_t t0 = ((int64_t)blockIdx.x * (kRouteThreads / 64) + wave) * a.rows; t0 < a.T; t0 += waves * a.rows) {
+    const int64_t t = t0 + row;
+    const int n = (int)min((int64_t)a.rows, a.T - t0);
+    const bool on = row < n && j < a.k;
+    int id = -1;
+    float w = 0.f, g = 0.f, z = 0.f;
+    if (on) {
+      id = a.ids[t * a.k + j];
+      w = a.w[t * a.k + j];
+      if (id < 0 || id >= a.E || w == 0.f) id = -1;   // constants, or no expert at all
+      if (id >= 0) {
+        g = a.dw[t * a.k + j];
+        if (a.score == MOE_SCORE_SIGMOID) z = load_as_float(a.logits, a.dtype, t * a.ld + id);
+      } else {
+        w = 0.f;
+      }
+    }
+    for (int i = lane * 4; i < n * a.pitch; i += 256) *(float4*)(tile + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+    float dot = id >= 0 ? g * w : 0.f;
+    dot = sum_lanes<SL>(dot);
+    float v = 0.f;
+    if (id >= 0) {
+      v = a.renorm ? w * (g - dot / a.scale) : w * g;
+      if (a.score == MOE_SCORE_SIGMOID) v *= 1.0f / (1.0f + expf(z));
+    }
+    // an expert listed in several slots: the first of them adds all up
+    float total = 0.f;
+    bool first = true;
+    for (int i = 0; i < a.k; ++i) {
+      const int oid = __shfl(id, row * SL + i);
+      const float ov = __shfl(v, row * SL + i);
+      if (oid == id) {
+        total += ov;
+        if (i < j) first = false;
+      }
+    }
+    if (id >= 0 && first) tile[row * a.pitch + id] = total;
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+    if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) {
+      // the other part of the full softmax, - s_e D, a row at a time
+      for (int r = 0; r < n; ++r) {
+        const int64_t base = (t0 + r) * a.ld;
+        float m = -kInf;
+        for (int e = lane; e < a.E; e += 64) m = fmaxf(m, load_as_float(a.logits, a.dtype, base + e));
+        m = max_lanes<64>(m);
+        if (m == -kInf) m = 0.f;
+        float s = 0.f;
+        for (int e = lane; e < a.E; e += 64) s += exp_fast(load_as_float(a.logits, a.dtype, base + e) - m);
+        s = sum_lanes<64>(s);
+        const float f = __shfl(dot, r * SL) / (s > 0.f ? s : 1.f);
+        for (int e = lane; e < a.E; e += 64) {
+          const float q = exp_fast(load_as_float(a.logits, a.dtype, base + e) - m);
+          tile[r * a.pitch + e] -= q * f;
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+      __threadfence_block();
+    }
+    if (a.vec) {
+      const int per = a.E / 4;
+      for (int i = lane; i < n * per; i += 64) {
+        const int r = i / per, e = (i - r * per) * 4;
+        store4_as(a.dz, a.dtype, (t0 + r) * a.ldd + e, *(const float4*)(tile + r * a.pitch + e));
+      }
+    } else {
+      for (int i = lane; i < n * a.E; i += 64) {
+        const int r = i / a.E, e = i - r * a.E;
+        store_as(a.dz, a.dtype, (t0 + r) * a.ldd + e, tile[r * a.pitch + e]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+  }
+}
+
+bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+template <int LPR, int VPL>
+void launch_route_k(const RouteArgs& a, bool byc, hipStream_t s) {
+  constexpr int RPW = 64 / LPR, WPB = kRouteThreads / 64;
+  const int64_t blocks = (a.T + RPW * WPB - 1) / (RPW * WPB);
+  const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192);
+  const size_t lds = byc ? (size_t)WPB * (a.E + a.groups + 16 + 1) * 8 : 0;
+  if (a.k <= 8) {
+    if (byc) hipLaunchKernelGGL((route_kernel<LPR, VPL, 8, true>), dim3(grid), dim3(kRouteThreads), lds, s, a);
+    else hipLaunchKernelGGL((route_kernel<LPR, VPL, 8, false>), dim3(grid), dim3(kRouteThreads), 0, s, a);
+  } else {
+    if (byc) hipLaunchKernelGGL((route_kernel<LPR, VPL, 32, true>), dim3(grid), dim3(kRouteThreads), lds, s, a);
+    else hipLaunchKernelGGL((route_kernel<LPR, VPL, 32, false>), dim3(grid), dim3(kRouteThreads), 0, s, a);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_route(int64_t T, int E, int k, const void* logits, int dtype, int64_t ld, const float* bias,
+                        const moe_route_opts& o, int32_t* ids, float* w, hipStream_t s) {
+  RouteArgs a;
+  a.logits = logits; a.bias = bias; a.ids = ids; a.w = w;
+  a.T = T; a.ld = ld; a.E = E; a.k = k; a.dtype = dtype;
+  a.score = o.score; a.renorm = o.renorm;
+  a.groups = o.n_group; a.gsize = E / o.n_group; a.keep = o.topk_group;
+  a.top2 = o.n_group > 1 && o.group_score == MOE_GROUP_TOP2;
+  a.scale = o.scale;
+  const size_t item = dtype == MOE_F32 ? 4 : 2;
+  a.vec = a.gsize % 4 == 0 && ld % 4 == 0 && aligned_to(logits, 4 * item);
+  const bool byc = bias != nullptr || a.top2;
+  int gp = 1;
+  while (gp < a.groups) gp *= 2;
+  // the fewest lanes that hold a row with at most 16 values each (a row over
+  // more lanes sorts less but shares a pick's exchanges among fewer rows)
+  auto places = [&](int lpr) { return (a.gsize + 4 * (lpr / gp) - 1) / (4 * (lpr / gp)) * 4; };
+  int lpr = gp < 4 ? 4 : gp;
+  if (E > 16 && lpr < 8) lpr = 8;
+  if (E > 64 && lpr < 16) lpr = 16;
+  while (lpr < 64 && places(lpr) > (lpr == 4 ? 4 : 16)) lpr *= 2;
+  const int vpl = places(lpr);
+  a.lpg = lpr / gp;
+  if (lpr == 4) launch_route_k<4, 4>(a, byc, s);
+  else if (lpr == 8 && vpl <= 8) launch_route_k<8, 8>(a, byc, s);
+  else if (lpr == 8) launch_route_k<8, 16>(a, byc, s);
+  else if (lpr == 16 && vpl <= 8) launch_route_k<16, 8>(a, byc, s);
+  else if (lpr == 16) launch_route_k<16, 16>(a, byc, s);
+  else if (lpr == 32) launch_route_k<32, 16>(a, byc, s);
+  else if (vpl <= 16) launch_route_k<64, 16>(a, byc, s);
+  else launch_route_k<64, 32>(a, byc, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_route_backward(int64_t T, int E, int k, const void* logits, int dtype, int64_t ld,
+                                 const int32_t* ids, const float* w, const float* dw, const moe_route_opts& o,
+                                 void* dz, int64_t ldd, hipStream_t s) {
+  RouteBackArgs a;
+  a.logits = logits; a.ids = ids; a.w = w; a.dw = dw; a.dz = dz;
+  a.T = T; a.ld = ld; a.ldd = ldd; a.E = E; a.k = k; a.dtype = dtype;
+  a.score = o.score; a.renorm = o.renorm; a.scale = o.scale;
+  const size_t item = dtype == MOE_F32 ? 4 : 2;
+  a.vec = E % 4 == 0 && ldd % 4 == 0 && aligned_to(dz, 4 * item);
+  a.pitch = (E + 3) / 4 * 4;
+  const int sl = k <= 8 ? 8 : 32;
+  // up to 8 KB of rows a wavefront
+  int rows = 2048 / a.pitch;
+  rows = rows < 1 ? 1 : rows;
+  a.rows = rows < 64 / sl ? rows : 64 / sl;
+  constexpr int WPB = kRouteThreads / 64;
+  const size_t lds = (size_t)WPB * a.rows * a.pitch * 4;
+  const int64_t blocks = (T + (int64_t)a.rows * WPB - 1) / ((int64_t)a.rows * WPB);
+  const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192);
+  if (sl == 8) hipLaunchKernelGGL((route_back_kernel<8>), dim3(grid), dim3(kRouteThreads), lds, s, a);
+  else hipLaunchKernelGGL((route_back_kernel<32>), dim3(grid), dim3(kRouteThreads), lds, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -112,7 +112,78 @@ __global__ __launch_bounds__(256) void scale_kernel(PlanLayout L, const int32_t*
   }
 }
 
+// Gradient of the scale step (moe_scale_backward):
+//   d_recv[pos[t][j]] = bf16(w[t][j] d_out[t]),  d_w[t][j] = <d_out[t], recv[pos[t][j]]>.
+// One wavefront per (token, slot): it reads the returned row and the token's
+// gradient once, 4 16-byte vectors of each in flight a lane, writes the row's
+// gradient and reduces the product in fp32 across its lanes.  A token's slots
+// are neighbouring wavefronts, so its gradient comes from the caches after the
+// first of them.
+template <bool DRECV, bool DW>
+__global__ __launch_bounds__(256) void scale_back_kernel(PlanLayout L, const int32_t* __restrict__ ws,
+                                                         const uint4* __restrict__ recv,
+                                                         const float* __restrict__ w,
+                                                         const uint4* __restrict__ dout, uint4* __restrict__ drecv,
+                                                         float* __restrict__ dw) {
+  if (ws[L.o_hdr + H_ERROR] != 0) return;
+  const int32_t* pos = ws + L.o_pos;
+  const int k = L.k, vec = L.d / 8, lane = threadIdx.x & 63;
+  const int wpb = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t total = (int64_t)L.T_r * k;
+  for (int64_t wv = (int64_t)blockIdx.x * wpb + wave; wv < total; wv += (int64_t)gridDim.x * wpb) {
+    const int64_t t = wv / k;
+    const float wt = w[wv];
+    const int64_t p = pos[wv];
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc((void*)(recv + p * vec), (short)0, DW ? vec * 16 : 0, kBufWord3);
+    const __amdgpu_buffer_rsrc_t gr = __builtin_amdgcn_make_buffer_rsrc((void*)(dout + t * vec), (short)0, vec * 16, kBufWord3);
+    const __amdgpu_buffer_rsrc_t dr = __builtin_amdgcn_make_buffer_rsrc((void*)(drecv + p * vec), (short)0, DRECV ? vec * 16 : 0, kBufWord3);
+    float sum = 0.f;
+    constexpr int U = 4;
+    // loads past the row's end read zeros and stores there are dropped
+    for (int v0 = lane; v0 < vec; v0 += 64 * U) {
+      v4u32 x[U], g[U];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        g[q] = __builtin_amdgcn_raw_buffer_load_b128(gr, (v0 + 64 * q) * 16, 0, 0);
+        if constexpr (DW) x[q] = __builtin_amdgcn_raw_buffer_load_b128(xr, (v0 + 64 * q) * 16, 0, kNontemporal);
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        v4u32 o;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float g0 = bf_lo(g[q][c]), g1 = bf_hi(g[q][c]);
+          if constexpr (DW) sum = fmaf(g1, bf_hi(x[q][c]), fmaf(g0, bf_lo(x[q][c]), sum));
+          if constexpr (DRECV) o[c] = pack2(wt * g0, wt * g1);
+        }
+        if constexpr (DRECV) __builtin_amdgcn_raw_buffer_store_b128(o, dr, (v0 + 64 * q) * 16, 0, kNontemporal);
+      }
+    }
+    if constexpr (DW) {
+#pragma unroll
+      for (int s = 32; s; s >>= 1) sum += __shfl_xor(sum, s);
+      if (lane == 0) dw[wv] = sum;
+    }
+  }
+}
+
 }  // namespace
+
+hipError_t launch_scale_backward(const PlanLayout& L, const int32_t* ws, const uint16_t* recv_self,
+                                 const float* topk_w, const uint16_t* d_out, uint16_t* d_recv, float* d_topk_w,
+                                 hipStream_t s) {
+  const int64_t waves = (int64_t)L.T_r * L.k;
+  if (waves == 0) return hipSuccess;
+  const int64_t blocks = (waves + 3) / 4;
+  const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536)), block(256);
+  const uint4 *r = (const uint4*)recv_self, *g = (const uint4*)d_out;
+  uint4* dr = (uint4*)d_recv;
+  if (d_recv && d_topk_w) hipLaunchKernelGGL((scale_back_kernel<true, true>), grid, block, 0, s, L, ws, r, topk_w, g, dr, d_topk_w);
+  else if (d_recv) hipLaunchKernelGGL((scale_back_kernel<true, false>), grid, block, 0, s, L, ws, r, topk_w, g, dr, d_topk_w);
+  else hipLaunchKernelGGL((scale_back_kernel<false, true>), grid, block, 0, s, L, ws, r, topk_w, g, dr, d_topk_w);
+  return hipGetLastError();
+}
 
 hipError_t launch_scale(const PlanLayout& L, const int32_t* ws, const uint16_t* recv_self, const float* topk_w,
                         uint16_t* out, hipStream_t s) {

@@ -24,6 +24,8 @@ Modules
              the hidden activation and of the expert output.
 ``combine``  applying the combine plan to the expert output.
 ``scale``    gate-weighted top-k reduction at the owner.
+``route``    the gate: top-k experts and weights from logits, and their gradient.
+``linear``   dense product with bias, activation and residual, and its gradients.
 ``brute``    definition-level MoE output and a sort-based layout, for tiny
              inputs (independent of the histogram/scan route of ``plan``).
 ``invariants`` the properties the pages fix for layout, schedule and plan.
@@ -32,6 +34,6 @@ Pins: ``tests/test_oracle_*.py`` (marked ``not gpu``).  Every function here has
 at least one pin that does not re-derive it with the same formula; see the
 test module docstrings.
 """
-from . import bf16, plan, ffn, combine, scale, brute, invariants  # noqa: F401
+from . import bf16, plan, ffn, combine, scale, route, linear, brute, invariants  # noqa: F401
 
-__all__ = ["bf16", "plan", "ffn", "combine", "scale", "brute", "invariants"]
+__all__ = ["bf16", "plan", "ffn", "combine", "scale", "route", "linear", "brute", "invariants"]

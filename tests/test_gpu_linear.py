@@ -1,0 +1,299 @@
+"""The dense product and its gradients on the GPU against the float64 oracle.
+
+Tolerances are bounds, not fits.  With u = 2^-24 and S = |x| |w|^T + |b|, an
+fp32 sum of depth exact products is off by at most (depth + 2) u S whatever its
+order.  An activation passes an error on with its largest slope (1.13 for the
+smooth ones here) and adds a few u of its value (8 u, and 64 u |z| where exp
+takes a rounded argument); a gated one multiplies the two halves' errors by the
+other half.  Every 16-bit result adds half a step, eps / 2 of its value.  In
+the gradients each dz is rounded to 16 bits, eps / 2 |dz|, which a product sums
+as eps / 2 |dz| |w|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import say
+from oracle import linear as OL
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh", "swiglu"]
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def _m():
+    import moe_expert_tile_amd as m
+    return m
+
+
+def _act(name):
+    return getattr(_m(), "ACT_" + name.upper())
+
+
+def _np(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def _half(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def _tiny(dtype):
+    return 2.0 ** -25 if dtype is torch.float16 else 2.0 ** -140
+
+
+def _inputs(M, N, K, act, dtype, seed, bias=True, residual=True, out="same"):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def randn(*shape, std=1.0, dtype=DT[dtype]):
+        return (torch.randn(*shape, generator=gen, device="cuda") * std).to(dtype)
+
+    n = 2 * N if act == "swiglu" else N
+    o = DT[dtype] if out == "same" else torch.float32
+    return dict(x=randn(M, K), w=randn(n, K, std=K ** -0.5), bias=randn(n, std=0.5) if bias else None,
+                residual=randn(M, N, dtype=o) if residual else None, d_out=randn(M, N, dtype=o),
+                out=torch.full((M, N), float("nan"), dtype=o, device="cuda"),
+                pre=torch.full((M, n), float("nan"), dtype=DT[dtype], device="cuda"))
+
+
+def _forward_error(x, w, b, act, z):
+    """(bound on z's error, bound on the activation's error)"""
+    S = np.abs(x) @ np.abs(w).T + (0 if b is None else np.abs(b))
+    ez = (x.shape[1] + 2) * U * S
+    if act == "swiglu":
+        n = z.shape[1] // 2
+        g, u = z[:, :n], z[:, n:]
+        sg = np.abs(OL.activation("silu", g))
+        own = (16 * U + 64 * U * np.abs(g)) * sg * np.abs(u)
+        return ez, 1.13 * ez[:, :n] * np.abs(u) + sg * ez[:, n:] + 1.13 * ez[:, :n] * ez[:, n:] + own
+    y = np.abs(OL.activation(act, z))
+    if act in ("none", "relu"):
+        return ez, ez
+    return ez, 1.13 * ez + 16 * U * np.abs(z) + 64 * U * np.abs(z) * y
+
+
+def _check_forward(a, act, ws=None):
+    m = _m()
+    res = None if a["residual"] is None else a["residual"].clone()
+    m.moe_linear(a["x"], a["w"], a["out"], bias=a["bias"], residual=a["residual"], pre=a["pre"], act=_act(act), ws=ws)
+    torch.cuda.synchronize()
+    x, w, b = _np(a["x"]), _np(a["w"]), _np(a["bias"])
+    z = OL.product(x, w, b)
+    ez, ey = _forward_error(x, w, b, act, z)
+    r = 0 if res is None else _np(res)
+    y = OL.apply(act, z) + r
+    half = _half(a["out"].dtype)
+    err = np.abs(_np(a["out"]) - y)
+    bound = (ey + U * (np.abs(y) + np.abs(r))) * (1 + half) + half * np.abs(y) + _tiny(a["out"].dtype)
+    assert np.all(err <= bound), (err - bound).max()
+    if a["pre"] is not None:
+        half = _half(a["pre"].dtype)
+        err = np.abs(_np(a["pre"]) - z)
+        assert np.all(err <= ez * (1 + half) + half * np.abs(z) + _tiny(a["pre"].dtype))
+
+
+# every tile, edges of each, sums from one chunk to several splits
+SIZES = [(1, 1, 8), (1, 7168, 2048), (2, 16, 64), (7, 33, 40), (16, 100, 512), (17, 60, 256), (31, 48, 1000),
+         (33, 130, 72), (64, 64, 64), (65, 60, 512), (65, 1, 8), (100, 256, 4096), (128, 128, 128), (129, 513, 264),
+         (200, 60, 2056), (257, 255, 192), (300, 1000, 8), (512, 256, 1024), (1000, 130, 136), (2049, 516, 328),
+         (4100, 2052, 72)]
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu", "gelu"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_forward(M, N, K, act):
+    if M * N > 1 << 22 and act != "none":
+        N //= 4
+    for dtype, out in (("bf16", "same"), ("f16", "f32")):
+        say(f"[linear] {M}x{N}x{K} {act} {dtype} {out}")
+        _check_forward(_inputs(M, N, K, act, dtype, M + N, out=out), act)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f16", "same")])
+def test_activations_and_options(act, dtype, out):
+    for M, N, K in ((5, 44, 96), (150, 90, 136)):
+        for bias in (False, True):
+            for residual in (False, True):
+                a = _inputs(M, N, K, act, dtype, 3, bias=bias, residual=residual, out=out)
+                a["w"] *= 3        # sums out where the activations bend
+                _check_forward(a, act)
+                a["pre"] = None
+                _check_forward(a, act)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 520, 200), (1100, 264, 2056), (520, 512, 520)])
+def test_large_tiles_of_every_kind(M, N, K):
+    """Sizes below one 256-row tile's worth of work choose small tiles; these
+    are repeated on a batch large enough for the others."""
+    for act in ("none", "swiglu", "silu"):
+        for scale in (1, 6):
+            a = _inputs(M * scale, N, K, act, "bf16", 5)
+            _check_forward(a, act)
+
+
+def _strided(t, pad, fill=float("nan")):
+    if t is None:
+        return None
+    big = torch.full((t.shape[0] * 2, t.shape[1] + pad), fill, dtype=t.dtype, device="cuda")
+    view = big[::2, :t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 37, 72), (140, 61, 136), (600, 300, 520)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_strides(M, N, K, act):
+    """Row pitches beyond the rows' length: what lies between is not read into
+    the sums and not written."""
+    a = _inputs(M, N, K, act, "bf16", 9)
+    packed = dict(a, out=a["out"].clone(), pre=a["pre"].clone())
+    _check_forward(packed, act)
+    s = {k: _strided(v, 8 if k in ("x", "w") else 3) if v is not None and v.dim() == 2 else v for k, v in a.items()}
+    s["bias"] = a["bias"]
+    keep_out, keep_pre = s["out"]._base.clone(), s["pre"]._base.clone()
+    _check_forward(s, act)
+    assert torch.equal(s["out"], packed["out"]) and torch.equal(s["pre"], packed["pre"])
+    for view, was in ((s["out"], keep_out), (s["pre"], keep_pre)):
+        now = view._base.clone()
+        now[::2, :view.shape[1]] = was[::2, :view.shape[1]]
+        assert torch.equal(now.isnan(), was.isnan())
+
+
+def test_residual_in_place_and_workspace():
+    m = _m()
+    for M, N, K in ((3, 256, 512), (128, 64, 8192), (512, 512, 256)):
+        a = _inputs(M, N, K, "none", "bf16", 21)
+        a["pre"] = None
+        m.moe_linear(a["x"], a["w"], a["out"], bias=a["bias"], residual=a["residual"])
+        d = m.moe_linear_desc(M, N, K, 0, 0, 0, 0)
+        need = m.moe_linear_sizes(d)["forward_bytes"]
+        ws = torch.full((need + 512,), 255, dtype=torch.uint8, device="cuda")   # NaNs: its contents do not matter
+        run = a["residual"].clone()
+        m.moe_linear(a["x"], a["w"], run, bias=a["bias"], residual=run, ws=ws)
+        assert torch.equal(run, a["out"])
+        assert bool((ws[need:] == 255).all())
+        if need:
+            with pytest.raises(m.MoEError):
+                m.moe_linear(a["x"], a["w"], run, ws=ws[:need - 1])
+
+
+def test_infinities_stay_in_their_rows():
+    m = _m()
+    for M in (5, 200):
+        a = _inputs(M, 96, 136, "none", "bf16", 2)
+        a["x"][3, 7] = float("inf")
+        a["x"][4, 8] = float("nan")
+        m.moe_linear(a["x"], a["w"], a["out"])
+        bad = (~torch.isfinite(a["out"])).any(1)
+        assert bad.nonzero().flatten().tolist() == [3, 4]
+
+
+def test_no_rows():
+    m = _m()
+    x, w = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.randn(32, 64, device="cuda").to(torch.bfloat16)
+    m.moe_linear(x, w, torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"))
+    dw, db = torch.full_like(w, 5.0), torch.full((32,), 5.0, dtype=torch.bfloat16, device="cuda")
+    m.moe_linear_backward(x, w, torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"), dx=torch.empty_like(x), dw=dw,
+                          dbias=db)
+    torch.cuda.synchronize()
+    assert not dw.any() and not db.any()
+
+
+# --- gradients -------------------------------------------------------------------
+
+def _check_backward(a, act, want=("dx", "dw", "dbias"), place=None):
+    m = _m()
+    x, w, g = _np(a["x"]), _np(a["w"]), _np(a["d_out"])
+    n = a["w"].shape[0]
+    dtype = a["x"].dtype
+    got = {"dx": torch.full_like(a["x"], 9.0), "dw": torch.full_like(a["w"], 9.0),
+           "dbias": torch.full((n,), 9.0, dtype=dtype, device="cuda")}
+    got = {k: v for k, v in got.items() if k in want}
+    if place:
+        got.update(place)
+    m.moe_linear_backward(a["x"], a["w"], a["d_out"], pre=a["pre"], act=_act(act), **got)
+    torch.cuda.synchronize()
+    pre = None if act == "none" else _np(a["pre"])
+    dz = OL.dz(act, g, pre)
+    half = _half(dtype)
+    # dz's own error: slopes (and silu's values) to a few u, exp's argument rounded
+    if act == "none":
+        e32 = 0 * np.abs(dz)
+    elif act == "swiglu":
+        z = np.abs(pre)
+        gu = np.concatenate([np.abs(g * pre[:, g.shape[1]:]), np.abs(g * pre[:, :g.shape[1]])], 1)
+        e32 = (16 + 64 * np.concatenate([z[:, :g.shape[1]]] * 2, 1)) * U * gu
+    else:
+        e32 = (16 + 64 * np.abs(pre) * (1 + pre ** 2)) * U * np.abs(g)
+    edz = half * np.abs(dz) + (1 + half) * e32 + _tiny(dtype)
+    for name, ref, err in (("dx", dz @ w, edz @ np.abs(w) + (n + 8) * U * (np.abs(dz) + edz) @ np.abs(w)),
+                           ("dw", dz.T @ x, edz.T @ np.abs(x) + (len(x) + 64) * U * (np.abs(dz) + edz).T @ np.abs(x)),
+                           ("dbias", dz.sum(0), (e32 + (len(x) + 2) * U * np.abs(dz)).sum(0))):
+        if name in got:
+            d = np.abs(_np(got[name]) - ref)
+            bound = err * (1 + half) + half * np.abs(ref) + _tiny(dtype)
+            assert np.all(d <= bound), (name, (d - bound).max())
+    return got
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 8), (1, 64, 128), (3, 31, 40), (64, 60, 512), (65, 63, 72), (100, 65, 200),
+                                   (130, 128, 264), (257, 100, 1000), (512, 60, 2048), (1025, 520, 328),
+                                   (4097, 257, 136)])
+@pytest.mark.parametrize("act", ["none", "swiglu", "silu"])
+def test_backward(M, N, K, act):
+    for dtype, out in (("bf16", "same"), ("f16", "f32")):
+        say(f"[linear back] {M}x{N}x{K} {act} {dtype} {out}")
+        a = _inputs(M, N, K, act, dtype, M + N, out=out)
+        a["pre"].normal_(generator=torch.Generator(device="cuda").manual_seed(4))
+        if act == "none":
+            a["pre"] = None
+        _check_backward(a, act)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_backward_of_every_activation_and_part(act):
+    a = _inputs(150, 72, 136, act, "bf16", 6)
+    a["pre"].normal_(std=2.0)
+    a["pre"][0, :6] = torch.tensor([0.0, -0.0, 30.0, -30.0, 120.0, -120.0])
+    whole = _check_backward(a, act)
+    for want in (("dx",), ("dw",), ("dbias",), ("dx", "dw")):
+        part = _check_backward(a, act, want)
+        for k in want:
+            assert torch.equal(part[k], whole[k]), (want, k)
+
+
+def test_backward_strides():
+    a = _inputs(140, 61, 136, "swiglu", "bf16", 8)
+    a["pre"].normal_()
+    whole = _check_backward(a, "swiglu")
+    s = {k: _strided(v, 8 if k in ("x", "w") else 3) if v is not None and v.dim() == 2 else v for k, v in a.items()}
+    place = {"dx": _strided(whole["dx"] * 0, 5), "dw": _strided(whole["dw"] * 0, 7)}
+    got = _check_backward(s, "swiglu", place=place)
+    for k in whole:
+        assert torch.equal(got[k], whole[k])
+    for k in ("dx", "dw"):
+        rest = got[k]._base.clone()
+        rest[::2, :got[k].shape[1]] = float("nan")
+        assert bool(rest.isnan().all())
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_backward_without_x_or_w(act):
+    """What a gradient does not need may be missing (through the C entry point)."""
+    import ctypes
+    m = _m()
+    a = _inputs(70, 40, 64, act, "bf16", 10)
+    a["pre"].normal_()
+    whole = _check_backward(dict(a, pre=a["pre"] if act != "none" else None), act)
+    d = m.moe_linear_desc(70, 40, 64, 0, 0, _act(act), 0)
+    ws = torch.empty(m.moe_linear_sizes(d)["backward_bytes"], dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    dx, dw = torch.zeros_like(a["x"]), torch.zeros_like(a["w"])
+    p = lambda t: t.data_ptr()  # noqa: E731
+    assert m._lib.moe_linear_backward(ctypes.byref(d), None, p(a["w"]), p(a["pre"]), p(a["d_out"]), p(dx), None, None, p(ws), s) == 0
+    assert m._lib.moe_linear_backward(ctypes.byref(d), p(a["x"]), None, p(a["pre"]), p(a["d_out"]), None, p(dw), None, p(ws), s) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(dx, whole["dx"]) and torch.equal(dw, whole["dw"])
