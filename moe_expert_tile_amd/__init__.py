@@ -166,9 +166,17 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# torch's raw current stream of a device: building the Stream object that
+# current_stream() returns takes 2.7 us, as long as a kernel launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -239,54 +247,64 @@ def _invalid(where: str, what: str):
     return err
 
 
-def _matrix(where, name, t, rows, cols, dtype, device) -> int:
-    """Checks a [rows, cols] matrix with unit column stride (None passes);
+def _matrix(where, name, t, shape, dtype, device) -> int:
+    """Checks a matrix of that shape with unit column stride (None passes);
     returns its row pitch, 0 (packed) where no second row shows it."""
     if t is None:
         return 0
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise _invalid(where, f"{name} is {tuple(t.shape)}, not ({rows}, {cols})")
+    if t.shape != shape:
+        raise _invalid(where, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype is not dtype:
         raise _invalid(where, f"{name} is {t.dtype}, not {dtype}")
     if t.device != device:
         raise _invalid(where, f"{name} is on {t.device}, not {device}")
-    if rows < 2:
-        if cols > 1 and rows and t.stride(1) != 1:
-            raise _invalid(where, f"{name}'s columns are not contiguous")
-        return 0
+    rows, cols = shape
     pitch, step = t.stride()
-    if (cols > 1 and step != 1) or pitch < cols:
-        raise _invalid(where, f"{name} has strides {t.stride()}: rows of contiguous columns are wanted")
+    if step != 1 and cols > 1 and rows > 0:
+        raise _invalid(where, f"{name}'s columns are not contiguous (strides {t.stride()})")
+    if rows < 2:
+        return 0
+    if pitch < cols:
+        raise _invalid(where, f"{name}'s rows overlap (strides {t.stride()})")
     return pitch
 
 
-def _packed(where, name, t, shape, dtype, device) -> None:
+def _packed(where, name, t, shape, dtype, device) -> Optional[int]:
+    """Checks a contiguous tensor (None passes); returns its address."""
     if t is None:
-        return
-    if tuple(t.shape) != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise _invalid(where, f"{name} is not a contiguous {dtype} tensor of shape {shape} on {device}")
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise _invalid(where, f"{name} is not a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
 
 
-def _on_device(where, t, call, stream):
-    """call(raw stream) with t's device current."""
-    if t.device.type != "cuda":
-        raise _invalid(where, f"the tensors are on {t.device}, not on a GPU")
-    if torch.cuda.current_device() == t.device.index:
-        return call(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
-    with torch.cuda.device(t.device):
-        return call(_stream(stream))
+def _launch(where, device, stream, fn, *args) -> None:
+    """fn(*args, raw stream) with `device` current; raises its errors."""
+    index = device.index
+    if device.type != "cuda":
+        raise _invalid(where, f"the tensors are on {device}, not on a GPU")
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, where)
 
 
-def _route_opts(score, renorm, n_group, topk_group, group_score, scale):
-    return moe_route_opts(int(score), 1 if renorm else 0, int(n_group), int(topk_group), int(group_score),
-                          float(scale))
-
-
-def _check_logits(where, logits):
+def _route_tensors(where, logits, topk_ids, topk_w):
+    """(sizes, type, row pitch) of the logits, and the addresses of the others."""
     if logits.dim() != 2 or logits.dtype not in _DTYPES:
         raise _invalid(where, "logits is a [tokens, experts] tensor of bfloat16, float16 or float32")
-    T, E = logits.shape
-    return T, E, _matrix(where, "logits", logits, T, E, logits.dtype, logits.device)
+    if topk_ids.dim() != 2:
+        raise _invalid(where, "topk_ids is a [tokens, top_k] tensor")
+    dtype, device = logits.dtype, logits.device
+    T, E = shape = logits.shape
+    k = topk_ids.shape[1]
+    ld = _matrix(where, "logits", logits, shape, dtype, device)
+    return (T, E, k, logits.data_ptr(), _DTYPES[dtype], ld), (
+        _packed(where, "topk_ids", topk_ids, (T, k), torch.int32, device),
+        _packed(where, "topk_w", topk_w, (T, k), torch.float32, device))
 
 
 def moe_route(logits, topk_ids, topk_w, bias=None, score: int = SCORE_SOFTMAX, renorm: bool = False,
@@ -294,17 +312,11 @@ def moe_route(logits, topk_ids, topk_w, bias=None, score: int = SCORE_SOFTMAX, r
               stream=None) -> None:
     """Router logits [T, E] -> topk_ids int32 [T, k] (what moe_plan reads) and
     topk_w float32 [T, k] (what moe_scale reads); see include/moe.h."""
-    T, E, ld = _check_logits("moe_route", logits)
-    if topk_ids.dim() != 2:
-        raise _invalid("moe_route", "topk_ids is a [tokens, top_k] tensor")
-    k = topk_ids.shape[1]
-    _packed("moe_route", "topk_ids", topk_ids, (T, k), torch.int32, logits.device)
-    _packed("moe_route", "topk_w", topk_w, (T, k), torch.float32, logits.device)
-    _packed("moe_route", "bias", bias, (E,), torch.float32, logits.device)
-    opts = _route_opts(score, renorm, n_group, topk_group, group_score, scale)
-    _check(_on_device("moe_route", logits, lambda s: _lib.moe_route(
-        T, E, k, logits.data_ptr(), _DTYPES[logits.dtype], ld, _ptr(bias), ctypes.byref(opts),
-        topk_ids.data_ptr(), topk_w.data_ptr(), s), stream), "moe_route")
+    sizes, outs = _route_tensors("moe_route", logits, topk_ids, topk_w)
+    device = logits.device
+    b = _packed("moe_route", "bias", bias, (sizes[1],), torch.float32, device)
+    opts = moe_route_opts(score, 1 if renorm else 0, n_group, topk_group, group_score, scale)
+    _launch("moe_route", device, stream, _lib.moe_route, *sizes, b, opts, *outs)
 
 
 def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, score: int = SCORE_SOFTMAX,
@@ -312,33 +324,26 @@ def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, score: int 
     """d_logits [T, E] (the logits' type) from d_topk_w float32 [T, k]; logits,
     topk_ids, topk_w, score, renorm and scale as in the moe_route call."""
     where = "moe_route_backward"
-    T, E, ld = _check_logits(where, logits)
-    if topk_ids.dim() != 2:
-        raise _invalid(where, "topk_ids is a [tokens, top_k] tensor")
-    k = topk_ids.shape[1]
-    _packed(where, "topk_ids", topk_ids, (T, k), torch.int32, logits.device)
-    _packed(where, "topk_w", topk_w, (T, k), torch.float32, logits.device)
-    _packed(where, "d_topk_w", d_topk_w, (T, k), torch.float32, logits.device)
-    ld_d = _matrix(where, "d_logits", d_logits, T, E, logits.dtype, logits.device)
-    opts = _route_opts(score, renorm, 1, 1, GROUP_MAX, scale)
-    _check(_on_device(where, logits, lambda s: _lib.moe_route_backward(
-        T, E, k, logits.data_ptr(), _DTYPES[logits.dtype], ld, topk_ids.data_ptr(), topk_w.data_ptr(),
-        d_topk_w.data_ptr(), ctypes.byref(opts), d_logits.data_ptr(), ld_d, s), stream), where)
+    sizes, ins = _route_tensors(where, logits, topk_ids, topk_w)
+    device = logits.device
+    g = _packed(where, "d_topk_w", d_topk_w, (sizes[0], sizes[2]), torch.float32, device)
+    ld_d = _matrix(where, "d_logits", d_logits, logits.shape, logits.dtype, device)
+    opts = moe_route_opts(score, 1 if renorm else 0, 1, 1, GROUP_MAX, scale)
+    _launch(where, device, stream, _lib.moe_route_backward, *sizes, *ins, g, opts, d_logits.data_ptr(), ld_d)
 
 
 def _linear_desc(where, x, w, out, act, out_name):
     if x.dim() != 2 or w.dim() != 2 or out.dim() != 2:
         raise _invalid(where, f"x, w and {out_name} are matrices")
-    if x.dtype not in (torch.bfloat16, torch.float16) or out.dtype not in (x.dtype, torch.float32):
-        raise _invalid(where, f"x is {x.dtype} and {out_name} {out.dtype}: bfloat16 or float16, and the same or "
-                              "float32")
-    (M, K), N = x.shape, out.shape[1]
+    dtype, out_dtype, device = x.dtype, out.dtype, x.device
+    if dtype not in _DTYPES or dtype is torch.float32 or (out_dtype is not dtype and out_dtype is not torch.float32):
+        raise _invalid(where, f"x is {dtype} and {out_name} {out_dtype}: bfloat16 or float16, and the same or float32")
+    M, K = xs = x.shape
+    N = out.shape[1]
     n = 2 * N if act == ACT_SWIGLU else N
-    d = moe_linear_desc(M, N, K, _DTYPES[x.dtype], _DTYPES[out.dtype], int(act), 0)
-    d.ld_x = _matrix(where, "x", x, M, K, x.dtype, x.device)
-    d.ld_w = _matrix(where, "w", w, n, K, x.dtype, x.device)
-    d.ld_out = _matrix(where, out_name, out, M, N, out.dtype, x.device)
-    return d, n
+    return moe_linear_desc(M, N, K, _DTYPES[dtype], _DTYPES[out_dtype], act, 0, _matrix(where, "x", x, xs, dtype, device),
+                           _matrix(where, "w", w, (n, K), dtype, device), 0, 0,
+                           _matrix(where, out_name, out, (M, N), out_dtype, device), 0, 0), n
 
 
 def moe_linear_sizes(desc: moe_linear_desc) -> Dict[str, int]:
@@ -372,16 +377,20 @@ def moe_linear(x, w, out, bias=None, residual=None, pre=None, act: int = ACT_NON
     None to take it from torch's allocator; see include/moe.h."""
     where = "moe_linear"
     d, n = _linear_desc(where, x, w, out, act, "out")
-    M, N = out.shape
-    _packed(where, "bias", bias, (n,), x.dtype, x.device)
-    d.ld_residual = _matrix(where, "residual", residual, M, N, out.dtype, x.device)
-    d.ld_pre = _matrix(where, "pre", pre, M, n, x.dtype, x.device)
+    device = x.device
+    if residual is not None:
+        d.ld_residual = _matrix(where, "residual", residual, out.shape, out.dtype, device)
+    if pre is not None:
+        d.ld_pre = _matrix(where, "pre", pre, (x.shape[0], n), x.dtype, device)
+    b = _packed(where, "bias", bias, (n,), x.dtype, device)
     need = ctypes.c_size_t()
-    _check(_lib.moe_linear_sizes(ctypes.byref(d), ctypes.byref(need), None), where)
-    ws = _workspace(where, ws, need.value, x, stream)
-    _check(_on_device(where, x, lambda s: _lib.moe_linear(
-        ctypes.byref(d), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), _ptr(pre), out.data_ptr(),
-        _ptr(ws), s), stream), where)
+    rc = _lib.moe_linear_sizes(d, need, None)
+    if rc != MOE_OK:
+        raise MoEError(rc, where)
+    if ws is not None or need.value:
+        ws = _workspace(where, ws, need.value, x, stream)
+    _launch(where, device, stream, _lib.moe_linear, d, x.data_ptr(), w.data_ptr(), b, _ptr(residual), _ptr(pre),
+            out.data_ptr(), _ptr(ws))
 
 
 def moe_linear_backward(x, w, d_out, dx=None, dw=None, dbias=None, pre=None, act: int = ACT_NONE, ws=None,
@@ -391,16 +400,18 @@ def moe_linear_backward(x, w, d_out, dx=None, dw=None, dbias=None, pre=None, act
     the forward call's pre; see include/moe.h."""
     where = "moe_linear_backward"
     d, n = _linear_desc(where, x, w, d_out, act, "d_out")
-    d.ld_pre = _matrix(where, "pre", pre, d_out.shape[0], n, x.dtype, x.device)
-    d.ld_dx = _matrix(where, "dx", dx, x.shape[0], x.shape[1], x.dtype, x.device)
-    d.ld_dw = _matrix(where, "dw", dw, n, x.shape[1], x.dtype, x.device)
-    _packed(where, "dbias", dbias, (n,), x.dtype, x.device)
+    dtype, device = x.dtype, x.device
+    d.ld_pre = _matrix(where, "pre", pre, (x.shape[0], n), dtype, device)
+    d.ld_dx = _matrix(where, "dx", dx, x.shape, dtype, device)
+    d.ld_dw = _matrix(where, "dw", dw, w.shape, dtype, device)
+    db = _packed(where, "dbias", dbias, (n,), dtype, device)
     need = ctypes.c_size_t()
-    _check(_lib.moe_linear_sizes(ctypes.byref(d), None, ctypes.byref(need)), where)
+    rc = _lib.moe_linear_sizes(d, None, need)
+    if rc != MOE_OK:
+        raise MoEError(rc, where)
     ws = _workspace(where, ws, need.value, x, stream)
-    _check(_on_device(where, x, lambda s: _lib.moe_linear_backward(
-        ctypes.byref(d), x.data_ptr(), w.data_ptr(), _ptr(pre), d_out.data_ptr(), _ptr(dx), _ptr(dw), _ptr(dbias),
-        _ptr(ws), s), stream), where)
+    _launch(where, device, stream, _lib.moe_linear_backward, d, x.data_ptr(), w.data_ptr(), _ptr(pre),
+            d_out.data_ptr(), _ptr(dx), _ptr(dw), db, _ptr(ws))
 
 
 def moe_device_status(plan_ws, stream=None) -> int:

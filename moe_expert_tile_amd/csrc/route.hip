@@ -7,8 +7,10 @@
 // are divided among its expert groups (each group has the same number of
 // lanes), which makes a group's best scores a reduction over neighbouring
 // lanes.  Every value becomes a 64-bit key that orders by (value descending,
-// expert ascending) as a double: a float has 24 significant bits, so a double
-// leaves 29 below them for the expert's index.  Each lane sorts its keys with
+// expert ascending): the float's bits, remapped so that they order as an
+// integer, above 10 bits of the expert's index, all in the fraction of a
+// double in [1, 2), so that one v_max_f64 compares two keys.  Each lane sorts
+// its keys with
 // a fixed network of v_max_f64 / v_min_f64; then every pick is the largest
 // head over the row's lanes, and the lane that held it moves its list up.
 //
@@ -36,41 +38,93 @@ __device__ __forceinline__ float load_as_float(const void* p, int dtype, int64_t
   return (float)((const _Float16*)p)[i];
 }
 
-__device__ __forceinline__ void load4_as_float(const void* p, int dtype, int64_t i, float (&v)[4]) {
-  if (dtype == MOE_F32) {
-    const float4 x = *(const float4*)((const float*)p + i);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-  } else if (dtype == MOE_BF16) {
-    const uint2 x = *(const uint2*)((const uint16_t*)p + i);
-    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
-    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+constexpr int kBufWord3 = 0x00020000;        // raw buffer access: data format 32, other fields zero
+constexpr uint32_t kPastEnd = 0x80000000u;   // past every descriptor's extent: loads there return zeros
+
+// VPL values of a row into z: place i at byte offset row_off + item * (chunk
+// i / 4 of this lane, `step` values apart); places from cnt on are -inf.  All
+// loads are issued before the first use: bounds are left to the descriptor.
+template <int DT, int VPL>
+__device__ __forceinline__ void load_places(__amdgpu_buffer_rsrc_t r, uint32_t row_off, int step, int cnt, bool vec,
+                                            float (&z)[VPL]) {
+  constexpr int ITEM = DT == MOE_F32 ? 4 : 2;
+  if (vec) {
+    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+    uint32_t raw[VPL / 4][ITEM];
+#pragma unroll
+    for (int c = 0; c < VPL / 4; ++c) {
+      const uint32_t off = 4 * c < cnt ? row_off + ITEM * c * step : kPastEnd;
+      if constexpr (DT == MOE_F32) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[c][i] = v[i];
+      } else {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+        raw[c][0] = v[0];
+        raw[c][1] = v[1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      float f;
+      if constexpr (DT == MOE_F32) f = __uint_as_float(raw[i / 4][i % 4]);
+      else {
+        const uint32_t w = raw[i / 4][(i % 4) / 2];
+        if constexpr (DT == MOE_BF16) f = __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
+        else f = (float)__builtin_bit_cast(_Float16, (uint16_t)(i % 2 ? w >> 16 : w));
+      }
+      z[i] = i < cnt ? f : -__builtin_inff();
+    }
   } else {
-    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-    const f16x4 x = *(const f16x4*)((const _Float16*)p + i);
-    v[0] = (float)x[0]; v[1] = (float)x[1]; v[2] = (float)x[2]; v[3] = (float)x[3];
+    uint32_t raw[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const uint32_t off = i < cnt ? row_off + ITEM * ((i / 4) * step + i % 4) : kPastEnd;
+      if constexpr (DT == MOE_F32) raw[i] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
+      else raw[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      float f;
+      if constexpr (DT == MOE_F32) f = __uint_as_float(raw[i]);
+      else if constexpr (DT == MOE_BF16) f = __uint_as_float(raw[i] << 16);
+      else f = (float)__builtin_bit_cast(_Float16, (uint16_t)raw[i]);
+      z[i] = i < cnt ? f : -__builtin_inff();
+    }
   }
 }
 
-// 32-bit lane exchange across the lanes of a row, step S of an all-reduce:
-// after steps 1, 2, 4, ... the operands are uniform over ever larger blocks,
-// so any exchange between the two halves of a block will do (mirrors here)
+// One step of an all-reduce over 2 S lanes whose halves are uniform already:
+// f of the two halves' values.  Within 16 lanes any exchange between the halves
+// will do (mirrors); across them the swap instructions give both halves at once.
 template <int S>
-__device__ __forceinline__ uint32_t swap_step(uint32_t v) {
-  if constexpr (S == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);        // quad_perm 1 0 3 2
-  else if constexpr (S == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);   // quad_perm 2 3 0 1
-  else if constexpr (S == 4) return __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);  // row_half_mirror
-  else if constexpr (S == 8) return __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);  // row_mirror
-  else return (uint32_t)__shfl_xor((int)v, S);
+__device__ __forceinline__ void halves(uint32_t v, uint32_t& a, uint32_t& b) {
+  a = v;
+  if constexpr (S == 1) b = __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);        // quad_perm 1 0 3 2
+  else if constexpr (S == 2) b = __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);   // quad_perm 2 3 0 1
+  else if constexpr (S == 4) b = __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);  // row_half_mirror
+  else if constexpr (S == 8) b = __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true);  // row_mirror
+  else {
+    const auto r = S == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+  }
 }
-template <int S>
-__device__ __forceinline__ float swap_step(float v) {
-  return __uint_as_float(swap_step<S>(__float_as_uint(v)));
+template <int S, class F>
+__device__ __forceinline__ float reduce_step(float v, F f) {
+  uint32_t a, b;
+  halves<S>(__float_as_uint(v), a, b);
+  return f(__uint_as_float(a), __uint_as_float(b));
 }
-template <int S>
-__device__ __forceinline__ double swap_step(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint64_t lo = swap_step<S>((uint32_t)b), hi = swap_step<S>((uint32_t)(b >> 32));
-  return __builtin_bit_cast(double, (hi << 32) | lo);
+template <int S, class F>
+__device__ __forceinline__ double reduce_step(double v, F f) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, v);
+  uint32_t al, bl, ah, bh;
+  halves<S>((uint32_t)w, al, bl);
+  halves<S>((uint32_t)(w >> 32), ah, bh);
+  return f(__builtin_bit_cast(double, ((uint64_t)ah << 32) | al), __builtin_bit_cast(double, ((uint64_t)bh << 32) | bl));
 }
 
 // keys are never NaN, so the bare instructions do (the compiler's fmax first
@@ -88,7 +142,7 @@ __device__ __forceinline__ double min64(double a, double b) {
 
 template <int N, int S = 1, class F, class V>
 __device__ __forceinline__ V reduce_lanes(V v, F f) {
-  if constexpr (S < N) return reduce_lanes<N, 2 * S>(f(v, swap_step<S>(v)), f);
+  if constexpr (S < N) return reduce_lanes<N, 2 * S>(reduce_step<S>(v, f), f);
   else return v;
 }
 template <int N> __device__ __forceinline__ float max_lanes(float v) {
@@ -97,39 +151,23 @@ template <int N> __device__ __forceinline__ float max_lanes(float v) {
 template <int N> __device__ __forceinline__ float sum_lanes(float v) {
   return reduce_lanes<N>(v, [](float a, float b) { return a + b; });
 }
-// the same over a block of `n` lanes of the row, n a power of two at most N
-template <int N, int S = 1, class F, class V>
-__device__ __forceinline__ V reduce_block(V v, int n, F f) {
-  if constexpr (S < N) {
-    if (S < n) v = f(v, swap_step<S>(v));
-    return reduce_block<N, 2 * S>(v, n, f);
-  } else {
-    return v;
-  }
+// Keys.  `ord` maps a float's bits to an integer of the same order (not for
+// NaN); low = 1023 - expert.  A lane's place without an expert holds kKeyAbsent,
+// below every value.
+__device__ __forceinline__ uint32_t ord(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);   // -0 as +0
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
-
-// keys: a float's 24 bits, then the expert index so that among equal values
-// the lower one is larger; infinities become finite so that their low bits
-// hold an index too.  A masked expert has the value -inf, a lane's place
-// without an expert lies below all of them.
-constexpr double kKeyInf = 0x1p1000, kKeyAbsent = -0x1p1010;
-__device__ __forceinline__ double make_key(float v, int idx) {
-  v += 0.0f;   // -0 as +0
-  double d = (double)v;
-  if (v == __builtin_inff()) d = kKeyInf;
-  if (v == -__builtin_inff()) d = -kKeyInf;
-  uint64_t b = __builtin_bit_cast(uint64_t, d);
-  b |= (uint32_t)(v >= 0.0f ? 1023 - idx : idx);
-  return __builtin_bit_cast(double, b);
+__device__ __forceinline__ double make_key(float v, uint32_t low, bool there) {
+  const uint32_t o = ord(v);
+  const uint32_t hi = there ? (o >> 12) | 0x3ff00000u : 0x3ff00000u;   // -inf, the lowest value, has 0x7ff below the exponent
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | ((o << 20) | low));
 }
-__device__ __forceinline__ int key_index(double k) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, k);
-  const int low = (int)(b & 1023);
-  return (b >> 63) ? low : 1023 - low;
-}
+constexpr double kKeyAbsent = 1.0;
+__device__ __forceinline__ int key_index(double k) { return 1023 - (int)(__builtin_bit_cast(uint64_t, k) & 1023); }
 __device__ __forceinline__ float key_value(double k) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, k) & ~(uint64_t)1023;
-  return (float)__builtin_bit_cast(double, b);   // +-kKeyInf round to infinities
+  const uint32_t o = (uint32_t)(__builtin_bit_cast(uint64_t, k) >> 20);
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
 // descending sort of N = 2^n values in registers (Batcher's odd-even merges)
@@ -170,70 +208,116 @@ struct RouteArgs {
 
 // One row ranked in 64 bits by the whole wavefront, c in LDS (E doubles, then
 // groups doubles): the picks go to `pick` (expert, or expert | 1 << 16 for a
-// masked one).  Slow and rare; it holds few registers.
-__device__ __forceinline__ void exact_row(const RouteArgs& a, int64_t t, double* c, double* gs, int* pick) {
-  const int lane = threadIdx.x & 63;
-  const int64_t base = t * a.ld;
-  double m = -__builtin_inf();
-  double sum = 1.0;
-  if (a.score == MOE_SCORE_SOFTMAX) {
-    for (int e = lane; e < a.E; e += 64) m = fmax(m, (double)load_as_float(a.logits, a.dtype, base + e));
-    for (int s = 32; s; s >>= 1) m = fmax(m, __shfl_xor(m, s));
-    sum = 0.0;
-    for (int e = lane; e < a.E; e += 64) sum += exp((double)load_as_float(a.logits, a.dtype, base + e) - m);
-    for (int s = 32; s; s >>= 1) sum += __shfl_xor(sum, s);
-  }
-  for (int e = lane; e < a.E; e += 64) {
-    const double z = (double)load_as_float(a.logits, a.dtype, base + e);
-    const double s = a.score == MOE_SCORE_SOFTMAX ? exp(z - m) / sum : 1.0 / (1.0 + exp(-z));
-    double v = a.bias ? s + (double)a.bias[e] : s;
-    if (z == -__builtin_inf() || !(v == v)) v = -__builtin_inf();
-    c[e] = v;
-  }
+// masked one).  Rare, but a late one holds up the launch, so each lane keeps
+// the best of its own values and only the lane that gave a pick looks again.
+// Masked values are kMasked, taken ones -inf.
+constexpr double kMasked = -0x1p1000;
+__device__ __forceinline__ void lds_wait() {   // this wavefront's LDS accesses so far, before those that follow
   __builtin_amdgcn_wave_barrier();
   __threadfence_block();
-  if (a.groups > 1) {
-    for (int g = lane; g < a.groups; g += 64) {
-      double b1 = -__builtin_inf(), b2 = -__builtin_inf();
-      for (int i = 0; i < a.gsize; ++i) {
-        const double v = c[g * a.gsize + i];
-        if (v > b1) { b2 = b1; b1 = v; } else if (v > b2) { b2 = v; }
-      }
-      gs[g] = a.top2 ? b1 + b2 : b1;
+}
+__device__ __forceinline__ void exact_row(const RouteArgs& a, int64_t t, double* c, double* gs, int* pick) {
+  const int lane = threadIdx.x & 63;
+  constexpr double kInf = __builtin_inf();
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  const int item = a.dtype == MOE_F32 ? 4 : 2;
+  const __amdgpu_buffer_rsrc_t zr = __builtin_amdgcn_make_buffer_rsrc(
+      (char*)const_cast<void*>(a.logits) + t * a.ld * item, (short)0, a.E * item, kBufWord3);
+  const __amdgpu_buffer_rsrc_t br =
+      __builtin_amdgcn_make_buffer_rsrc((void*)a.bias, (short)0, a.bias ? a.E * 4 : 0, kBufWord3);
+  // four values a lane at a time, so that their exponentials overlap
+  auto load4 = [&](int e0, float (&z)[4]) {   // experts e0 + 64 i; past the end: zeros
+    uint32_t raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      raw[i] = item == 4 ? __builtin_amdgcn_raw_buffer_load_b32(zr, (e0 + 64 * i) * 4, 0, 0)
+                         : (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(zr, (e0 + 64 * i) * 2, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      z[i] = a.dtype == MOE_F32 ? __uint_as_float(raw[i])
+             : a.dtype == MOE_BF16 ? __uint_as_float(raw[i] << 16)
+                                   : (float)__builtin_bit_cast(_Float16, (uint16_t)raw[i]);
+  };
+  double m = 0.0, sum = 0.0;
+  if (softmax) {
+    float mf = -__builtin_inff();
+#pragma unroll 1
+    for (int e0 = lane; e0 < a.E; e0 += 256) {
+      float z[4];
+      load4(e0, z);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e0 + 64 * i < a.E) mf = fmaxf(mf, z[i]);
     }
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
-    for (int e = lane; e < a.E; e += 64) {
-      const int g = e / a.gsize;
-      int better = 0;
-      for (int o = 0; o < a.groups; ++o) better += (gs[o] > gs[g] || (gs[o] == gs[g] && o < g)) ? 1 : 0;
-      if (better >= a.keep) c[e] = -__builtin_inf();
-    }
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
+    m = (double)max_lanes<64>(mf);
   }
-  // picks: largest c, ties to the lower expert; a taken expert becomes NaN,
-  // which no comparison prefers
-  for (int j = 0; j < a.k; ++j) {
-    double bv = 0.0;
-    int be = 1 << 20;   // none yet
+#pragma unroll 1
+  for (int e0 = lane; e0 < a.E; e0 += 256) {
+    float z[4];
+    double x[4];
+    load4(e0, z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = exp(softmax ? (double)z[i] - m : -(double)z[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e0 + 64 * i < a.E) {
+        sum += x[i];
+        c[e0 + 64 * i] = z[i] > -__builtin_inff() ? x[i] : -1.0;   // -1 for masked and NaN
+      }
+    }
+  }
+  if (softmax) sum = reduce_lanes<64>(sum, [](double x, double y) { return x + y; });
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) {
+    const double x = c[e];
+    const double b = (double)__uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(br, e * 4, 0, 0));
+    const double v = (softmax ? x : 1.0) / (softmax ? sum : 1.0 + x) + b;
+    c[e] = x >= 0.0 && v > -kInf ? v : kMasked;   // (a NaN compares false)
+  }
+  lds_wait();
+  if (a.groups > 1) {
+    if (lane < a.groups) {   // at most 64
+      double b1 = kMasked, b2 = kMasked;
+#pragma unroll 8
+      for (int i = 0; i < a.gsize; ++i) {
+        const double v = c[lane * a.gsize + i];
+        b2 = max64(b2, min64(b1, v));
+        b1 = max64(b1, v);
+      }
+      gs[lane] = a.top2 ? (b2 == kMasked ? kMasked : b1 + b2) : b1;
+    }
+    lds_wait();
+    if (lane < a.groups) {
+      const double mine = gs[lane];
+      int better = 0;
+#pragma unroll 8
+      for (int o = 0; o < a.groups; ++o) better += (gs[o] > mine || (gs[o] == mine && o < lane)) ? 1 : 0;
+      if (better >= a.keep)
+        for (int i = 0; i < a.gsize; ++i) c[lane * a.gsize + i] = kMasked;
+    }
+    lds_wait();
+  }
+  double bv = -kInf;
+  int be = 0;
+  auto best_of_mine = [&]() {
+    bv = -kInf;
+#pragma unroll 4
     for (int e = lane; e < a.E; e += 64) {
       const double v = c[e];
-      if (v == v && (be == (1 << 20) || v > bv)) { bv = v; be = e; }
+      if (v > bv) { bv = v; be = e; }   // ascending: equal ones keep the lower expert
     }
-    for (int s = 32; s; s >>= 1) {
-      const double ov = __shfl_xor(bv, s);
-      const int oe = __shfl_xor(be, s);
-      const bool take = oe != (1 << 20) && (be == (1 << 20) || ov > bv || (ov == bv && oe < be));
-      if (take) { bv = ov; be = oe; }
+  };
+  best_of_mine();
+  for (int j = 0; j < a.k; ++j) {
+    const double top = reduce_lanes<64>(bv, [](double x, double y) { return max64(x, y); });
+    const int e = -(int)reduce_lanes<64>(bv == top ? (float)-be : -1e9f, [](float x, float y) { return fmaxf(x, y); });
+    if (lane == 0) pick[j] = e | (top == kMasked ? 1 << 16 : 0);
+    if ((e & 63) == lane) {
+      c[e] = -kInf;
+      best_of_mine();
     }
-    if (lane == 0) {
-      pick[j] = be | (bv == -__builtin_inf() ? 1 << 16 : 0);
-      c[be] = __builtin_nan("");
-    }
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
   }
+  lds_wait();
 }
 
 // LPR lanes a row, VPL values a lane, at most KMAX picks; BYC: c = s + b is
@@ -245,217 +329,247 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
   constexpr int LOOK = KMAX + (BYC ? 1 : 0);          // picks looked at: with BYC the first one left out too
   constexpr int NS = (LOOK + LPR - 1) / LPR;          // picks a lane keeps
   constexpr int DEPTH = VPL < LOOK ? VPL : LOOK;      // places of the sorted list they can come from
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l = lane % LPR;                           // lane within the row
-  const int g = l / a.lpg, sub = l % a.lpg;
+  const int g = l / a.lpg, sub = l % a.lpg;           // its group, and place among the group's lanes
   constexpr float kInf = __builtin_inff();
-  const int64_t waves = (int64_t)gridDim.x * (kRouteThreads / 64);
-  for (int64_t t0 = ((int64_t)blockIdx.x * (kRouteThreads / 64) + wave) * RPW; t0 < a.T; t0 += waves * RPW) {
-    const int64_t t = t0 + lane / LPR;
-    const bool live = t < a.T;
-    // place i of this lane: expert g * gsize + p(i)
-    auto place = [&](int i) { return (i / 4) * 4 * a.lpg + sub * 4 + (i & 3); };
-    float z[VPL];
-    const bool lane_on = live && g < a.groups;
-    const int64_t base = t * a.ld + (int64_t)g * a.gsize;
-    if (a.vec) {
+  // place i of this lane is value (i / 4) * step + sub * 4 + i % 4 of its
+  // group; the first cnt places exist
+  const int step = 4 * a.lpg;
+  const int rem = a.gsize - sub * 4;
+  const int cnt = g < a.groups && rem > 0 ? rem / step * 4 + min(rem % step, 4) : 0;
+  const int e0 = g * a.gsize + sub * 4;               // its first expert
+  const int64_t t0 = ((int64_t)blockIdx.x * (kRouteThreads / 64) + wave) * RPW;
+  if (t0 >= a.T) return;
+  const int64_t t = t0 + lane / LPR;
+  const bool live = t < a.T;
+  const int nrows = (int)min((int64_t)RPW, a.T - t0);
+  const int item = a.dtype == MOE_F32 ? 4 : 2;
+  const __amdgpu_buffer_rsrc_t zr = __builtin_amdgcn_make_buffer_rsrc(
+      (char*)const_cast<void*>(a.logits) + t0 * a.ld * item, (short)0,
+      (int)(((nrows - 1) * a.ld + a.E) * item), kBufWord3);
+  const uint32_t zoff = (uint32_t)((lane / LPR) * (uint32_t)a.ld + e0) * item;
+  const int zcnt = live ? cnt : 0;
+  float z[VPL];
+  if (a.dtype == MOE_F32) load_places<MOE_F32, VPL>(zr, zoff, step, zcnt, a.vec, z);
+  else if (a.dtype == MOE_BF16) load_places<MOE_BF16, VPL>(zr, zoff, step, zcnt, a.vec, z);
+  else load_places<MOE_F16, VPL>(zr, zoff, step, zcnt, a.vec, z);
+  float bv[BYC ? VPL : 1];
+  if constexpr (BYC) {
+    // a.vec says the group size is a multiple of 4; four-byte alignment is all a buffer load needs
+    const __amdgpu_buffer_rsrc_t br =
+        __builtin_amdgcn_make_buffer_rsrc((void*)a.bias, (short)0, a.bias ? a.E * 4 : 0, kBufWord3);
+    load_places<MOE_F32, VPL>(br, 4 * e0, step, cnt, a.gsize % 4 == 0, bv);
+  }
+  // a NaN logit (or bias), or +inf under a softmax, has no weights: the
+  // row's are NaN, its ids still k distinct experts
+  bool bad = false;
 #pragma unroll
-      for (int i = 0; i < VPL; i += 4) {
-        float v[4] = {-kInf, -kInf, -kInf, -kInf};
-        if (lane_on && place(i) < a.gsize) load4_as_float(a.logits, a.dtype, base + place(i), v);
+  for (int i = 0; i < VPL; i += 2) bad |= __builtin_isunordered(z[i], z[i + 1]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) z[i + c] = v[c];
-      }
+  for (int i = 0; i < VPL; ++i) z[i] = fmaxf(z[i], -kInf);   // a NaN ranks as masked
+  // the softmax's maximum and sum, where full scores are wanted
+  float zmax = 0.f, zsum = 1.f;
+  const bool full = a.score == MOE_SCORE_SOFTMAX && (BYC || !a.renorm);
+  if (full) {
+    float m = z[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, z[i]);
+    m = max_lanes<LPR>(m);
+    zmax = m == -kInf ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s += exp_fast(z[i] - zmax);
+    zsum = fmaxf(sum_lanes<LPR>(s), 1e-30f);   // every expert masked: zero scores
+  }
+  // what is ranked: the logits, or c
+  const float zinv = 1.0f / zsum;
+  float v[VPL];
+  if constexpr (BYC) {
+    if (a.score == MOE_SCORE_SOFTMAX) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[i] = exp_fast(z[i] - zmax) * zinv;
     } else {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        z[i] = lane_on && place(i) < a.gsize ? load_as_float(a.logits, a.dtype, base + place(i)) : -kInf;
+      for (int i = 0; i < VPL; ++i) v[i] = __builtin_amdgcn_rcpf(1.0f + exp_fast(-z[i]));
     }
-    // a NaN logit (or bias), or +inf under a softmax, has no weights: the
-    // row's are NaN, its ids still k distinct experts
-    bool bad = false;
+    // without a bias its buffer reads zeros, and places past cnt -inf
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      bad |= !(z[i] == z[i]) || (a.score == MOE_SCORE_SOFTMAX && z[i] == kInf);
-      if (!(z[i] == z[i])) z[i] = -kInf;
+      const float c = v[i] + bv[i];
+      bad |= z[i] != -kInf && !(c == c);
+      v[i] = fmaxf(z[i] == -kInf ? -kInf : c, -kInf);
     }
-    // the softmax's maximum and sum, where full scores are wanted
-    float zmax = 0.f, zsum = 1.f;
-    const bool full = a.score == MOE_SCORE_SOFTMAX && (BYC || !a.renorm);
-    if (full) {
-      float m = z[0];
+  } else {
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) m = fmaxf(m, z[i]);
-      m = max_lanes<LPR>(m);
-      zmax = m == -kInf ? 0.f : m;
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) s += exp_fast(z[i] - zmax);
-      zsum = fmaxf(sum_lanes<LPR>(s), 1e-30f);   // every expert masked: zero scores
-    }
-    // what is ranked: the logits, or c
-    float v[VPL];
+    for (int i = 0; i < VPL; ++i) v[i] = z[i];
+  }
+  bool near = false;   // BYC: a decision closer than the error of 32 bits
+  // Error of c in 32 bits, u = 2^-24: the sum's rounding, u |c|; a sigmoid's
+  // below 4 u (its exponent's rounding times s (1 - s) |z| < 1/4, exp, 1 + e
+  // and the reciprocal); a softmax's below 64 u s + u (the terms' and the
+  // sum's roundings).  Two of them, with s at most smax:
+  auto error2 = [&](float cmax, float smax) {
+    return fmaf(0x1p-22f, cmax, a.score == MOE_SCORE_SOFTMAX ? fmaf(0x1p-17f, smax, 0x1p-22f) : 0x1p-21f);
+  };
+  bool kept = true;
+  if (a.groups > 1) {
+    float b1 = -kInf, b2 = -kInf;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      if constexpr (BYC) {
-        const float s = a.score == MOE_SCORE_SOFTMAX ? exp_fast(z[i] - zmax) / zsum : 1.0f / (1.0f + exp_fast(-z[i]));
-        float c = s;
-        if (a.bias && lane_on && place(i) < a.gsize) c += a.bias[g * a.gsize + place(i)];
-        bad |= z[i] != -kInf && !(c == c);
-        v[i] = (z[i] == -kInf || !(c == c)) ? -kInf : c;
-      } else {
-        v[i] = z[i];
-      }
+      b2 = fmaxf(b2, fminf(b1, v[i]));
+      b1 = fmaxf(b1, v[i]);
     }
-    bool near = false;   // BYC: a decision closer than the error of 32 bits
-    auto close = [](float hi, float lo) { return hi - lo <= 0x1p-18f * fmaxf(1.0f, fabsf(hi)); };
-    bool kept = true;
-    if (a.groups > 1) {
-      float b1 = -kInf, b2 = -kInf;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const float x = place(i) < a.gsize ? v[i] : -kInf;
-        b2 = fmaxf(b2, fminf(b1, x));
-        b1 = fmaxf(b1, x);
+    auto merge = [&](auto tag) {
+      constexpr int S = decltype(tag)::value;
+      if (S < a.lpg) {
+        uint32_t x1, y1, x2, y2;
+        halves<S>(__float_as_uint(b1), x1, y1);
+        halves<S>(__float_as_uint(b2), x2, y2);
+        b1 = fmaxf(__uint_as_float(x1), __uint_as_float(y1));
+        b2 = fmaxf(fmaxf(__uint_as_float(x2), __uint_as_float(y2)), fminf(__uint_as_float(x1), __uint_as_float(y1)));
       }
-      auto merge = [&](auto tag) {
-        constexpr int S = decltype(tag)::value;
-        if (S < a.lpg) {
-          const float o1 = swap_step<S>(b1), o2 = swap_step<S>(b2);
-          b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
-          b1 = fmaxf(b1, o1);
-        }
-      };
-      merge(std::integral_constant<int, 1>{});
-      if constexpr (LPR > 2) merge(std::integral_constant<int, 2>{});
-      if constexpr (LPR > 4) merge(std::integral_constant<int, 4>{});
-      if constexpr (LPR > 8) merge(std::integral_constant<int, 8>{});
-      if constexpr (LPR > 16) merge(std::integral_constant<int, 16>{});
-      if constexpr (LPR > 32) merge(std::integral_constant<int, 32>{});
-      const float sc = a.top2 ? b1 + b2 : b1;
-      int better = 0;
-      for (int o = 0; o < a.groups; ++o) {
-        const float os = __shfl(sc, (lane - l) + o * a.lpg);
-        better += (os > sc || (os == sc && o < g)) ? 1 : 0;
-      }
-      kept = g < a.groups && better < a.keep;
-      if constexpr (BYC) {
-        // lowest kept and highest dropped group; infinities differ by NaN or
-        // by infinity and so are never close
-        const float lo = -max_lanes<LPR>(kept ? -sc : -kInf);
-        const float hi = max_lanes<LPR>(!kept && g < a.groups ? sc : -kInf);
-        near |= close(lo, hi);
-      }
+    };
+    merge(std::integral_constant<int, 1>{});
+    if constexpr (LPR > 2) merge(std::integral_constant<int, 2>{});
+    if constexpr (LPR > 4) merge(std::integral_constant<int, 4>{});
+    if constexpr (LPR > 8) merge(std::integral_constant<int, 8>{});
+    if constexpr (LPR > 16) merge(std::integral_constant<int, 16>{});
+    if constexpr (LPR > 32) merge(std::integral_constant<int, 32>{});
+    const float sc = a.top2 ? b1 + b2 : b1;
+    int better = 0;
+    for (int o = 0; o < a.groups; ++o) {
+      const float os = __shfl(sc, (lane - l) + o * a.lpg);
+      better += (os > sc || (os == sc && o < g)) ? 1 : 0;
     }
-    double key[VPL];
+    kept = g < a.groups && better < a.keep;
+    if constexpr (BYC) {
+      // lowest kept and highest dropped group; infinities differ by NaN or
+      // by infinity and so are never close
+      const float lo = -max_lanes<LPR>(kept ? -sc : -kInf);
+      const float hi = max_lanes<LPR>(!kept && g < a.groups ? sc : -kInf);
+      // (twice the scores' error for sums of two; no score exceeds the best one's, zinv)
+      const float size = fabsf(b1) + (a.top2 ? fabsf(b2) : 0.f);
+      const float cmax = max_lanes<LPR>(size < kInf ? size : 0.f);
+      near |= lo - hi <= 2.0f * error2(cmax, zinv);
+    }
+  }
+  double key[VPL];
+  const uint32_t low = 1023 - e0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      key[i] = g < a.groups && place(i) < a.gsize ? make_key(kept ? v[i] : -kInf, g * a.gsize + place(i)) : kKeyAbsent;
-    sort_desc<VPL>(key);
+  for (int i = 0; i < VPL; ++i)
+    key[i] = make_key(kept ? v[i] : -kInf, low - ((i / 4) * step + i % 4), i < cnt);
+  sort_desc<VPL>(key);
 
-    double slot[NS];
+  double slot[NS];
 #pragma unroll
-    for (int r = 0; r < NS; ++r) slot[r] = kKeyAbsent;
-    const int picks = BYC && a.k < a.E ? a.k + 1 : a.k;   // one more to see how near the first one left out lies
-    for (int j = 0; j < picks; ++j) {
-      const double best = reduce_lanes<LPR>(key[0], [](double x, double y) { return max64(x, y); });
-#pragma unroll
-      for (int r = 0; r < NS; ++r)
-        if (j == r * LPR + l) slot[r] = best;
-      const bool mine = key[0] == best;
-#pragma unroll
-      for (int i = 0; i + 1 < DEPTH; ++i) key[i] = mine ? key[i + 1] : key[i];
-      // the list's last place: once it has been picked nothing is left in it
-      if constexpr (DEPTH == VPL) key[DEPTH - 1] = mine ? kKeyAbsent : key[DEPTH - 1];
-    }
-    int pick[NS];
+  for (int r = 0; r < NS; ++r) slot[r] = kKeyAbsent;
+  const int picks = BYC && a.k < a.E ? a.k + 1 : a.k;   // one more to see how near the first one left out lies
+  for (int j = 0; j < picks; ++j) {
+    const double best = reduce_lanes<LPR>(key[0], [](double x, double y) { return max64(x, y); });
 #pragma unroll
     for (int r = 0; r < NS; ++r)
-      pick[r] = key_index(slot[r]) | (key_value(slot[r]) == -kInf ? 1 << 16 : 0);
-    if constexpr (BYC) {
-      // neighbours in the order that are close, unless their logits and
-      // biases are the same and the index decides (zero biases over 16-bit
-      // logits are full of those)
-      float pc = kInf, pz = 0.f, pb = 0.f;   // the last lane's pick of the previous round
+      if (j == r * LPR + l) slot[r] = best;
+    // (a branch, not a select an element: that became indexed reads of the list)
+    if (key[0] == best) {
 #pragma unroll
-      for (int r = 0; r < NS; ++r) {
-        const int j = r * LPR + l;
-        const bool on = live && j < picks;
-        const float c = key_value(slot[r]);
-        const float zj = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : 0.f;
-        const float bj = on && a.bias ? a.bias[pick[r] & 0xffff] : 0.f;
-        float qc = __shfl_up(c, 1, LPR), qz = __shfl_up(zj, 1, LPR), qb = __shfl_up(bj, 1, LPR);
-        if (l == 0) { qc = pc; qz = pz; qb = pb; }
-        near |= on && j > 0 && close(qc, c) && !(qz == zj && qb == bj);
-        if constexpr (NS > 1) {
-          pc = __shfl(c, LPR - 1, LPR);
-          pz = __shfl(zj, LPR - 1, LPR);
-          pb = __shfl(bj, LPR - 1, LPR);
-        }
-      }
-      near = max_lanes<LPR>(near ? 1.f : 0.f) > 0.f;
-      double* cbuf = (double*)smem + (size_t)wave * (a.E + a.groups + 16 + 1);
-      double* gbuf = cbuf + a.E;
-      int* pbuf = (int*)(gbuf + a.groups);
-      uint64_t todo = __ballot(near && live && l == 0);
-      while (todo) {
-        const int at = __ffsll((unsigned long long)todo) - 1;
-        todo &= todo - 1;
-        exact_row(a, t0 + at / LPR, cbuf, gbuf, pbuf);
-        if (lane / LPR == at / LPR) {
-#pragma unroll
-          for (int r = 0; r < NS; ++r)
-            if (r * LPR + l < a.k) pick[r] = pbuf[r * LPR + l];
-        }
-        __builtin_amdgcn_wave_barrier();
-      }
+      for (int i = 0; i + 1 < DEPTH; ++i) key[i] = key[i + 1];
+      // the list's last place: once it has been picked nothing is left in it
+      if constexpr (DEPTH == VPL) key[DEPTH - 1] = kKeyAbsent;
     }
-    // weights of the picks
-    float p[NS], zs[NS];
-    bool nan_row = max_lanes<LPR>(bad ? 1.f : 0.f) > 0.f;
-    float top = -kInf;
+  }
+  int pick[NS];
 #pragma unroll
-    for (int r = 0; r < NS; ++r) {
-      const bool on = live && r * LPR + l < a.k && !(pick[r] >> 16);
-      if constexpr (BYC) zs[r] = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : -kInf;
-      else zs[r] = on ? key_value(slot[r]) : -kInf;
-      top = fmaxf(top, zs[r]);
-    }
-    float total = 0.f;
-    if (a.renorm) {
-      // the weights' ratios need no common factor: the softmax's maximum is
-      // taken over the picks, and sigmoids of far negative logits are scaled
-      // up by e^-top, so that the sum does not vanish in 32 bits
-      top = max_lanes<LPR>(top);
-      const float shift = a.score == MOE_SCORE_SOFTMAX ? (top == -kInf ? 0.f : top) : fminf(0.f, top == -kInf ? 0.f : top);
-#pragma unroll
-      for (int r = 0; r < NS; ++r) {
-        float q;
-        if (zs[r] == -kInf) q = 0.f;
-        else if (a.score == MOE_SCORE_SOFTMAX) q = expf(zs[r] - shift);
-        else if (zs[r] < kSigmoidZero) q = 0.f;
-        else q = zs[r] > 0.f ? 1.0f / (1.0f + expf(-zs[r])) : expf(zs[r] - shift) / (1.0f + expf(zs[r]));
-        p[r] = q;
-        total += q;
-      }
-      total = sum_lanes<LPR>(total);
-    } else {
-#pragma unroll
-      for (int r = 0; r < NS; ++r) {
-        if (zs[r] == -kInf) p[r] = 0.f;
-        else if (a.score == MOE_SCORE_SOFTMAX) p[r] = expf(zs[r] - zmax) / zsum;
-        else p[r] = 1.0f / (1.0f + expf(-zs[r]));
-      }
-    }
+  for (int r = 0; r < NS; ++r)
+    pick[r] = key_index(slot[r]) | (key_value(slot[r]) == -kInf ? 1 << 16 : 0);
+  if constexpr (BYC) {
+    // neighbours in the order that are close, unless their logits and
+    // biases are the same and the index decides (zero biases over 16-bit
+    // logits are full of those)
+    float pc = kInf, pz = 0.f, pb = 0.f, ps = 0.f;   // the last lane's pick of the previous round
 #pragma unroll
     for (int r = 0; r < NS; ++r) {
       const int j = r * LPR + l;
-      if (live && j < a.k) {
-        float wj = a.renorm ? (total > 0.f ? p[r] / total : 0.f) : p[r];
-        wj *= a.scale;
-        a.ids[t * a.k + j] = pick[r] & 0xffff;
-        a.w[t * a.k + j] = nan_row ? __builtin_nanf("") : wj;
+      const bool on = live && j < picks;
+      const float c = key_value(slot[r]);
+      const float zj = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : 0.f;
+      const float bj = on && a.bias ? a.bias[pick[r] & 0xffff] : 0.f;
+      const float sj = exp_fast(zj - zmax) * zinv;   // of a softmax
+      float qc = __shfl_up(c, 1, LPR), qz = __shfl_up(zj, 1, LPR), qb = __shfl_up(bj, 1, LPR);
+      float qs = __shfl_up(sj, 1, LPR);
+      if (l == 0) { qc = pc; qz = pz; qb = pb; qs = ps; }
+      near |= on && j > 0 && qc - c <= error2(fabsf(qc), fmaxf(qs, sj)) && !(qz == zj && qb == bj);
+      if constexpr (NS > 1) {
+        pc = __shfl(c, LPR - 1, LPR);
+        pz = __shfl(zj, LPR - 1, LPR);
+        pb = __shfl(bj, LPR - 1, LPR);
+        ps = __shfl(sj, LPR - 1, LPR);
       }
+    }
+    near = max_lanes<LPR>(near ? 1.f : 0.f) > 0.f;
+    double* cbuf = (double*)smem + (size_t)wave * (a.E + a.groups + 16 + 1);
+    double* gbuf = cbuf + a.E;
+    int* pbuf = (int*)(gbuf + a.groups);
+    uint64_t todo = __ballot(near && live && l == 0);
+    while (todo) {
+      const int at = __ffsll((unsigned long long)todo) - 1;
+      todo &= todo - 1;
+      exact_row(a, t0 + at / LPR, cbuf, gbuf, pbuf);
+      if (lane / LPR == at / LPR) {
+#pragma unroll
+        for (int r = 0; r < NS; ++r)
+          if (r * LPR + l < a.k) pick[r] = pbuf[r * LPR + l];
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  // weights of the picks
+  float p[NS], zs[NS];
+  float top = -kInf;
+#pragma unroll
+  for (int r = 0; r < NS; ++r) {
+    const bool on = live && r * LPR + l < a.k && !(pick[r] >> 16);
+    if constexpr (BYC) zs[r] = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : -kInf;
+    else zs[r] = on ? key_value(slot[r]) : -kInf;
+    top = fmaxf(top, zs[r]);
+  }
+  if (a.score == MOE_SCORE_SOFTMAX) bad |= top == kInf;
+  const bool nan_row = max_lanes<LPR>(bad ? 1.f : 0.f) > 0.f;
+  float total = 0.f;
+  if (a.renorm) {
+    // the weights' ratios need no common factor: the softmax's maximum is
+    // taken over the picks, and sigmoids of far negative logits are scaled
+    // up by e^-top, so that the sum does not vanish in 32 bits
+    top = max_lanes<LPR>(top);
+    const float shift = a.score == MOE_SCORE_SOFTMAX ? (top == -kInf ? 0.f : top) : fminf(0.f, top == -kInf ? 0.f : top);
+#pragma unroll
+    for (int r = 0; r < NS; ++r) {
+      float q;
+      if (zs[r] == -kInf) q = 0.f;
+      else if (a.score == MOE_SCORE_SOFTMAX) q = expf(zs[r] - shift);
+      else if (zs[r] < kSigmoidZero) q = 0.f;
+      else q = zs[r] > 0.f ? 1.0f / (1.0f + expf(-zs[r])) : expf(zs[r] - shift) / (1.0f + expf(zs[r]));
+      p[r] = q;
+      total += q;
+    }
+    total = sum_lanes<LPR>(total);
+  } else {
+#pragma unroll
+    for (int r = 0; r < NS; ++r) {
+      if (zs[r] == -kInf) p[r] = 0.f;
+      else if (a.score == MOE_SCORE_SOFTMAX) p[r] = expf(zs[r] - zmax) / zsum;
+      else p[r] = 1.0f / (1.0f + expf(-zs[r]));
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < NS; ++r) {
+    const int j = r * LPR + l;
+    if (live && j < a.k) {
+      float wj = a.renorm ? (total > 0.f ? p[r] / total : 0.f) : p[r];
+      wj *= a.scale;
+      a.ids[t * a.k + j] = pick[r] & 0xffff;
+      a.w[t * a.k + j] = nan_row ? __builtin_nanf("") : wj;
     }
   }
 }
@@ -595,8 +709,7 @@ bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 template <int LPR, int VPL>
 void launch_route_k(const RouteArgs& a, bool byc, hipStream_t s) {
   constexpr int RPW = 64 / LPR, WPB = kRouteThreads / 64;
-  const int64_t blocks = (a.T + RPW * WPB - 1) / (RPW * WPB);
-  const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192);
+  const unsigned grid = (unsigned)((a.T + RPW * WPB - 1) / (RPW * WPB));
   const size_t lds = byc ? (size_t)WPB * (a.E + a.groups + 16 + 1) * 8 : 0;
   if (a.k <= 8) {
     if (byc) hipLaunchKernelGGL((route_kernel<LPR, VPL, 8, true>), dim3(grid), dim3(kRouteThreads), lds, s, a);
