@@ -1,11 +1,14 @@
 // Dense product with its epilogue, out = act(x w^T + bias) + residual
 // (include/moe.h, moe_linear), and its gradients (moe_linear_backward).
 //
-// Every product here is C[m][n] = sum_k A[m][k] B[n][k] with both operands
-// contiguous along k; 16-bit operands, fp32 accumulation in MFMA registers.
+// Every product here is C[m][n] = sum_k A(m, k) B(n, k); 16-bit operands, fp32
+// accumulation in MFMA registers.
 //   * Many rows: v_mfma_f32_32x32x16 over tiles staged through LDS by
 //     direct-to-LDS buffer loads into a two-stage ring (K steps of 64), 16-byte
 //     chunks XOR-swizzled so that operand fetches are free of bank conflicts.
+//     An operand is contiguous along k (x and w in the forward product) or
+//     across it (w in dx = dz w, both in dw = dz^T x); the latter is staged as
+//     it lies and transposed on the way out of LDS (ds_read_b64_tr_b16).
 //     Rows past an operand's end and chunks past K get an offset past the
 //     buffer descriptor's bound, where loads return zeros.  Few tiles are also
 //     split along K: fp32 partial sums in the workspace, summed in order by a
@@ -19,8 +22,8 @@
 //
 // Gradients.  dz = d_out act'(pre) is formed once (rounded to the operand type,
 // which the matrix cores need; its column sums for the bias are taken before
-// the rounding), then dx = dz w and dw = dz^T x are products of the same form
-// over transposed copies in the workspace.
+// the rounding), then dx = dz w and dw = dz^T x are products of the same form.
+// Without an activation dz is d_out itself where its type and layout allow.
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -211,7 +214,7 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int n, flo
 // --- tiled product ----------------------------------------------------------
 
 struct ProdArgs {
-  const uint16_t *a, *b;   // A [M, K], B [N or 2N, K]
+  const uint16_t *a, *b;   // A [M, K] or, across k, [K, M]; B [N or 2N, K] or [K, N]
   int64_t lda, ldb;
   int64_t K;
   int64_t kper;            // K of one split (a multiple of 64)
@@ -263,9 +266,60 @@ __device__ __forceinline__ int xcd_order(int i, int total) {
   return x * q + min(x, r) + i / 8;
 }
 
-template <class C, bool F16, bool GATED, bool PART>
+// An operand's tile in LDS.  Along k: ROWS rows of 64 k, row r's 16-byte chunk c
+// at c ^ (r / 2) % 8.  Across k: 64 rows (k) of ROWS values, row r's chunk c at
+// c ^ across_swizzle(r): a transposing read takes 4 rows x 32 values a half
+// wavefront, 64 bytes of each row, which so fall on different banks (rows of
+// 128 bytes are half a bank line apart already).  Either way a
+// wavefront fills 1 KB at a time in LDS order, and the lane picks the chunk of
+// global memory that belongs there.
+template <int ROWS>
+__device__ __forceinline__ int across_swizzle(int r) {
+  return ROWS >= 128 ? 4 * (r % 4) : 4 * ((r / 2) % 2);
+}
+template <int ROWS, int NW, bool ACROSS>
+struct Staged {
+  static constexpr int LOADS = ROWS / 8 / NW;        // 1 KB loads a stage and wave
+  static constexpr int LPR = ACROSS ? ROWS / 8 : 8;  // lanes (chunks) a row
+  static constexpr int RPL = 64 / LPR;               // rows a load
+  uint32_t off[LOADS];
+  int chunk;   // along k: this lane's logical chunk of a row (the same in all of its loads)
+
+  // r0: the operand's rows (or, across k, columns) from the tile's first one on
+  __device__ __forceinline__ void init(int wave, int lane, int rows, int64_t ld) {
+    chunk = (lane % 8) ^ ((wave * 4 + lane / 16) % 8);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int r = (wave + i * NW) * RPL + lane / LPR;
+      if constexpr (ACROSS) {
+        const int c = (lane % LPR) ^ across_swizzle<ROWS>(r);
+        off[i] = c * 8 < rows ? 2u * ((uint32_t)r * (uint32_t)ld + c * 8) : kPastEnd;
+      } else {
+        off[i] = r < rows ? 2u * ((uint32_t)r * (uint32_t)ld + chunk * 8) : kPastEnd;
+      }
+    }
+  }
+};
+
+// the transposing LDS read of a 32-row MFMA operand block: lane l gets row
+// l % 32, k = 8 (l / 32) .. + 7, as two reads of 4 k each.  (`restrict` gives
+// the reads an alias scope; without one the compiler lets them wait for every
+// load to LDS in flight, the next stage's among them: dx of 8192 x 4096 x 7168
+// 546 us, with it 470 us.)
+template <class V8>
+__device__ __forceinline__ V8 read_across(const uint16_t* __restrict p, int pitch) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  struct { s16x4 lo, hi; } v;
+  v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * pitch));
+  return __builtin_bit_cast(V8, v);
+}
+
+template <class C, bool F16, bool GATED, bool PART, bool AX, bool BX>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
 void product_kernel(ProdArgs g) {
+  static_assert(!GATED || !BX, "gated weights lie along k");
   typedef typename Elem<F16>::v8 v8;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[C::LDS_ELEMS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -291,43 +345,46 @@ void product_kernel(ProdArgs g) {
   const int KT = ke > kb ? (int)((ke - kb + kBK - 1) / kBK) : 0;
   const int klast = (int)(ke - kb) - (KT - 1) * kBK;   // columns of the last stage
 
-  // lane l of a 1 KB load fills row 8 q + l / 8, chunk l % 8 of the stage, so
-  // it fetches the logical chunk (l % 8) ^ (row / 2) % 8
-  const int ld_row = lane / 8;
-  const int ld_chunk = (lane % 8) ^ ((wave * 4 + ld_row / 2) % 8);
   static_assert(C::NW % 2 == 0, "a wave's loads are all of one row parity");
-  const __amdgpu_buffer_rsrc_t a_rsrc =
-      make_rsrc(g.a + m0 * g.lda + kb, KT ? ((int64_t)(arows - 1) * g.lda + (ke - kb)) * 2 : 0);
-  const int64_t b_bytes = KT ? ((int64_t)(brows - 1) * g.ldb + (ke - kb)) * 2 : 0;
-  const __amdgpu_buffer_rsrc_t b_rsrc = make_rsrc(g.b + (int64_t)n0 * g.ldb + kb, b_bytes);
-  const __amdgpu_buffer_rsrc_t u_rsrc =
-      GATED ? make_rsrc(g.b + ((int64_t)g.e.N + n0) * g.ldb + kb, b_bytes) : b_rsrc;
-  uint32_t a_off[C::A_LOADS], b_off[C::B_LOADS];
+  Staged<C::BM, C::NW, AX> sta;
+  Staged<C::BN, C::NW, BX> stb;
+  sta.init(wave, lane, arows, g.lda);
+  stb.init(wave, lane, brows, g.ldb);
+  if constexpr (GATED) {
+    // the second half of the tile holds the up rows
 #pragma unroll
-  for (int i = 0; i < C::A_LOADS; ++i) {
-    const int r = (wave + i * C::NW) * 8 + ld_row;
-    a_off[i] = r < arows ? 2u * ((uint32_t)r * (uint32_t)g.lda + ld_chunk * 8) : kPastEnd;
+    for (int i = C::B_LOADS / 2; i < C::B_LOADS; ++i) stb.off[i] = stb.off[i - C::B_LOADS / 2];
   }
-#pragma unroll
-  for (int i = 0; i < C::B_LOADS; ++i) {
-    int r = (wave + i * C::NW) * 8 + ld_row;
-    if (GATED && i >= C::B_LOADS / 2) r -= HB;
-    b_off[i] = r < brows ? 2u * ((uint32_t)r * (uint32_t)g.ldb + ld_chunk * 8) : kPastEnd;
-  }
-  // stage k into half k % 2 of the ring; `last`: chunks past the end of K are
-  // masked (there every operand's chunk is whole or absent, K % 8 == 0)
+  // (descriptors end with a whole 16-byte chunk: a length that is no multiple
+  // of 8 is dz's, whose rows have zeros up to one)
+  const int64_t along_a = KT ? ((int64_t)(arows - 1) * g.lda + (ke - kb + 7) / 8 * 8) * 2 : 0;
+  const int64_t along_b = KT ? ((int64_t)(brows - 1) * g.ldb + (ke - kb)) * 2 : 0;
+  const int arows8 = (arows + 7) / 8 * 8;
+  const uint16_t* a_base = AX ? g.a + kb * g.lda + m0 : g.a + m0 * g.lda + kb;
+  const uint16_t* b_base = BX ? g.b + kb * g.ldb + n0 : g.b + (int64_t)n0 * g.ldb + kb;
+  const __amdgpu_buffer_rsrc_t a_all = make_rsrc(a_base, AX ? 0 : along_a);
+  const __amdgpu_buffer_rsrc_t b_all = make_rsrc(b_base, BX ? 0 : along_b);
+  const __amdgpu_buffer_rsrc_t u_all = GATED ? make_rsrc(b_base + (int64_t)g.e.N * g.ldb, along_b) : b_all;
+  // stage k into half k % 2 of the ring.  Along k, `last` masks the chunks past
+  // the end of K (each is whole or absent, or dz's with its zeros);
+  // across k, a stage has a descriptor of its own that ends with its last row.
   auto issue = [&](int k, auto last_tag) __attribute__((always_inline)) {
     constexpr bool LAST = decltype(last_tag)::value;
     char* base = (char*)(lds + (k & 1) * C::STAGE);
     const int koff = 2 * kBK * k;
-    const bool on = !LAST || ld_chunk * 8 < klast;
+    const int64_t rows = LAST ? klast : kBK;
+    const __amdgpu_buffer_rsrc_t ar =
+        AX ? make_rsrc(a_base + (int64_t)k * kBK * g.lda, ((rows - 1) * g.lda + arows8) * 2) : a_all;
+    const __amdgpu_buffer_rsrc_t br =
+        BX ? make_rsrc(b_base + (int64_t)k * kBK * g.ldb, ((rows - 1) * g.ldb + brows) * 2) : b_all;
 #pragma unroll
     for (int i = 0; i < C::A_LOADS; ++i)
-      load_lds(a_rsrc, base + (wave + i * C::NW) * 1024, on ? a_off[i] : kPastEnd, koff);
+      load_lds(ar, base + (wave + i * C::NW) * 1024,
+               !LAST || AX || sta.chunk * 8 < klast ? sta.off[i] : kPastEnd, AX ? 0 : koff);
 #pragma unroll
     for (int i = 0; i < C::B_LOADS; ++i)
-      load_lds(GATED && i >= C::B_LOADS / 2 ? u_rsrc : b_rsrc, base + 2 * C::A_ELEMS + (wave + i * C::NW) * 1024,
-               on ? b_off[i] : kPastEnd, koff);
+      load_lds(GATED && i >= C::B_LOADS / 2 ? u_all : br, base + 2 * C::A_ELEMS + (wave + i * C::NW) * 1024,
+               !LAST || BX || stb.chunk * 8 < klast ? stb.off[i] : kPastEnd, BX ? 0 : koff);
   };
 
   // this wave's weight rows inside the tile (32 a block)
@@ -342,6 +399,13 @@ void product_kernel(ProdArgs g) {
     }
   }
   const int lrow = lane & 31, lhalf = lane >> 5, rsw = (lrow / 2) % 8;
+  // transposing reads: this lane's row (k) among 16, its place among 32 values
+  const int xrow = 8 * lhalf + (lane & 15) / 4;
+  const int xcol = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), xsub = (lane & 1) * 4;
+  auto across = [&](int block, auto pitch) __attribute__((always_inline)) {
+    constexpr int P = decltype(pitch)::value;
+    return xrow * P + (((block / 8) ^ across_swizzle<P>(xrow)) + xcol) * 8 + xsub;
+  };
 
   f32x16 acc[C::FN][C::FM];
 #pragma unroll
@@ -366,9 +430,16 @@ void product_kernel(ProdArgs g) {
     auto fetch = [&](int kk) __attribute__((always_inline)) {
       const int phys = ((2 * kk + lhalf) ^ rsw) * 8;
 #pragma unroll
-      for (int i = 0; i < C::FN; ++i) pw[kk & 1][i] = *(const v8*)(sb + (prow[i] + lrow) * kBK + phys);
+      for (int i = 0; i < C::FN; ++i) {
+        if constexpr (BX) pw[kk & 1][i] = read_across<v8>(sb + 16 * kk * C::BN + across(prow[i], std::integral_constant<int, C::BN>{}), C::BN);
+        else pw[kk & 1][i] = *(const v8*)(sb + (prow[i] + lrow) * kBK + phys);
+      }
 #pragma unroll
-      for (int j = 0; j < C::FM; ++j) px[kk & 1][j] = *(const v8*)(sa + (wave_m * C::WM + 32 * j + lrow) * kBK + phys);
+      for (int j = 0; j < C::FM; ++j) {
+        const int at = wave_m * C::WM + 32 * j;
+        if constexpr (AX) px[kk & 1][j] = read_across<v8>(sa + 16 * kk * C::BM + across(at, std::integral_constant<int, C::BM>{}), C::BM);
+        else px[kk & 1][j] = *(const v8*)(sa + (at + lrow) * kBK + phys);
+      }
     };
     fetch(0);
     if constexpr (NEXT == 1) issue(k + 1, Mid{});
@@ -383,11 +454,12 @@ void product_kernel(ProdArgs g) {
     }
     // LDS reads of step 0, the refill, then each step's reads before the
     // previous step's MFMAs
-    __builtin_amdgcn_sched_group_barrier(0x100, C::FN + C::FM, 0);
+    constexpr int READS = C::FN * (BX ? 2 : 1) + C::FM * (AX ? 2 : 1);
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
     if constexpr (NEXT != 0) __builtin_amdgcn_sched_group_barrier(0x10, C::A_LOADS + C::B_LOADS, 0);
 #pragma unroll
     for (int kk = 0; kk < C::KK; ++kk) {
-      if (kk + 1 < C::KK) __builtin_amdgcn_sched_group_barrier(0x100, C::FN + C::FM, 0);
+      if (kk + 1 < C::KK) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
       __builtin_amdgcn_sched_group_barrier(0x8, C::FN * C::FM, 0);
     }
   };
@@ -542,21 +614,19 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
   }
 }
 
-// --- gradients: dz and transposed copies ---------------------------------------
+// --- gradients: dz --------------------------------------------------------------
 
 struct DzArgs {
   const void* d_out;      // [M, N]
   const uint16_t* pre;    // [M, N or 2N]
   uint16_t* dz;           // [M, ldz] or null
-  uint16_t* dzt;          // [N or 2N, mp] or null
-  float* sums;            // [mp / 64][N or 2N] column sums of 64 rows each, or null
-  int64_t M, ldd, ldp, ldz, mp;
+  float* sums;            // [ceil(M / 64)][N or 2N] column sums of 64 rows each, or null
+  int64_t M, ldd, ldp, ldz;
   int N, act, d_f32, vec;
 };
 
 // 64 rows x 64 columns a workgroup: thread t forms row t / 4, columns 16 (t % 4)
-// .. + 15.  Rows past M and columns past N (up to ldz, a multiple of 8) are
-// zeros in both copies.
+// .. + 15.  Columns past N, up to ldz (a multiple of 8), are zeros.
 template <bool F16>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
   __shared__ float tile[64][65];
@@ -610,7 +680,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
       for (int i = 0; i < 64; ++i) s += tile[i][tid];
       a.sums[blockIdx.y * (int64_t)halves * a.N + first + n0 + tid] = s;
     }
-    // 8 values of one row (dz) or column (its transpose) a store, 64 x 8 stores
+    // 8 values of a row a store, 64 x 8 stores
     for (int i = tid; i < 512; i += 256) {
       const int row = i / 8, part8 = (i % 8) * 8;
       if (a.dz && m0 + row < a.M) {
@@ -627,13 +697,6 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
             if (c < end) d[c] = b[c];
         }
       }
-      if (a.dzt && n0 + row < a.N) {
-        uint16_t b[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) b[c] = Elem<F16>::bits(tile[part8 + c][row]);
-        *(uint4*)(a.dzt + (first + n0 + row) * a.mp + m0 + part8) =
-            make_uint4(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16, b[4] | (uint32_t)b[5] << 16, b[6] | (uint32_t)b[7] << 16);
-      }
     }
   }
 }
@@ -648,33 +711,6 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float* sums, int r
   out[n] = Elem<F16>::bits(s);
 }
 
-// out[c][r] = in[r][c], 16-bit values, cols a multiple of 8; rows from R up to
-// the output's pitch (a multiple of 64) are zeros
-__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* in, int64_t ld, int64_t R, int cols,
-                                                        uint16_t* out, int64_t pitch) {
-  __shared__ uint16_t tile[64][66];
-  const int tid = threadIdx.x;
-  const int64_t r0 = (int64_t)blockIdx.y * 64;
-  const int c0 = blockIdx.x * 64;
-  for (int i = tid; i < 512; i += 256) {
-    const int row = i / 8, c = (i % 8) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r0 + row < R && c0 + c < cols) v = *(const uint4*)(in + (r0 + row) * ld + c0 + c);
-    uint32_t* d = (uint32_t*)&tile[row][c];
-    d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
-  }
-  __syncthreads();
-  for (int i = tid; i < 512; i += 256) {
-    const int col = i / 8, r = (i % 8) * 8;
-    if (c0 + col >= cols) continue;
-    uint16_t b[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) b[c] = tile[r + c][col];
-    *(uint4*)(out + (int64_t)(c0 + col) * pitch + r0 + r) =
-        make_uint4(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16, b[4] | (uint32_t)b[5] << 16, b[6] | (uint32_t)b[7] << 16);
-  }
-}
-
 // --- host -------------------------------------------------------------------
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -687,9 +723,9 @@ struct Cut {
   int64_t kper;
 };
 
-Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated) {
+Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
   const int64_t NZ = gated ? 2 * N : N;
-  if (M <= 64) return {0, 1, round_up(K, kBK)};
+  if (M <= 64 && !across) return {0, 1, round_up(K, kBK)};
   // time of each choice from the rates one CU reaches with each tile and the
   // cost of the partial sums' round trip; the smallest wins
   static const int bm[4] = {0, 64, 128, 256}, bn[4] = {0, 128, 128, 256}, per_cu[4] = {0, 3, 2, 1};
@@ -698,7 +734,8 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated) {
   Cut best = {1, 1, round_up(K, kBK)};
   double best_us = 1e30;
   for (int t = 1; t <= 3; ++t) {
-    const int64_t tiles = ((M + bm[t] - 1) / bm[t]) * ((NZ + bn[t] - 1) / bn[t]);
+    int64_t tiles = ((M + bm[t] - 1) / bm[t]) * ((NZ + bn[t] - 1) / bn[t]);
+    if (tiles < 1) tiles = 1;   // no rows: nothing to cut
     for (int s = 1; s <= 32; s *= 2) {
       if (s > 1 && steps < 4 * s) break;
       const int64_t per = (steps + s - 1) / s;
@@ -721,22 +758,22 @@ size_t part_bytes(const Cut& c, int64_t M, int64_t N, bool gated) {
   return c.splits > 1 ? (size_t)c.splits * M * round_up(N, 4) * (gated ? 2 : 1) * 4 : 0;
 }
 
-template <class C, bool F16, bool GATED>
+template <class C, bool F16, bool GATED, bool AX, bool BX>
 void launch_tiles(ProdArgs& g, hipStream_t s) {
   constexpr int HB = GATED ? C::BN / 2 : C::BN;
   g.n_mt = (int)((g.e.M + C::BM - 1) / C::BM);
   g.n_nt = (g.e.N + HB - 1) / HB;
   const unsigned grid = (unsigned)((int64_t)g.n_mt * g.n_nt * g.splits);
   if (g.splits == 1) {
-    hipLaunchKernelGGL((product_kernel<C, F16, GATED, false>), dim3(grid), dim3(C::NT), 0, s, g);
+    hipLaunchKernelGGL((product_kernel<C, F16, GATED, false, AX, BX>), dim3(grid), dim3(C::NT), 0, s, g);
     return;
   }
-  hipLaunchKernelGGL((product_kernel<C, F16, GATED, true>), dim3(grid), dim3(C::NT), 0, s, g);
+  hipLaunchKernelGGL((product_kernel<C, F16, GATED, true, AX, BX>), dim3(grid), dim3(C::NT), 0, s, g);
   const int64_t blocks = (g.e.M * ((g.e.N + 3) / 4) + 255) / 256;
   hipLaunchKernelGGL((join_kernel<F16, GATED>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, g);
 }
 
-template <bool F16, bool GATED>
+template <bool F16, bool GATED, bool AX, bool BX>
 hipError_t launch_product(ProdArgs& g, const Cut& c, void* ws, hipStream_t s) {
   if (g.e.M == 0) return hipSuccess;
   g.kper = c.kper;
@@ -745,41 +782,37 @@ hipError_t launch_product(ProdArgs& g, const Cut& c, void* ws, hipStream_t s) {
   g.up_col = (int)round_up(g.e.N, 4);
   g.pitch = (int64_t)g.up_col * (GATED ? 2 : 1);
   if (c.tile == 0) {
-    const dim3 grid((unsigned)((g.e.N + 15) / 16)), block(kFewWaves * 64);
-    if (g.e.M <= 16) hipLaunchKernelGGL((few_rows_kernel<1, F16, GATED>), grid, block, 0, s, g);
-    else if (g.e.M <= 32) hipLaunchKernelGGL((few_rows_kernel<2, F16, GATED>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((few_rows_kernel<4, F16, GATED>), grid, block, 0, s, g);
+    if constexpr (!AX && !BX) {
+      const dim3 grid((unsigned)((g.e.N + 15) / 16)), block(kFewWaves * 64);
+      if (g.e.M <= 16) hipLaunchKernelGGL((few_rows_kernel<1, F16, GATED>), grid, block, 0, s, g);
+      else if (g.e.M <= 32) hipLaunchKernelGGL((few_rows_kernel<2, F16, GATED>), grid, block, 0, s, g);
+      else hipLaunchKernelGGL((few_rows_kernel<4, F16, GATED>), grid, block, 0, s, g);
+    }
   } else if (c.tile == 1) {
-    launch_tiles<Tile64, F16, GATED>(g, s);
+    launch_tiles<Tile64, F16, GATED, AX, BX>(g, s);
   } else if (c.tile == 2) {
-    launch_tiles<Tile128, F16, GATED>(g, s);
+    launch_tiles<Tile128, F16, GATED, AX, BX>(g, s);
   } else {
-    launch_tiles<std::conditional_t<GATED, Tile256G, Tile256>, F16, GATED>(g, s);
+    launch_tiles<std::conditional_t<GATED, Tile256G, Tile256>, F16, GATED, AX, BX>(g, s);
   }
   return hipGetLastError();
 }
 
 bool gated(const moe_linear_desc& d) { return d.act == MOE_ACT_SWIGLU; }
 
-hipError_t run_product(ProdArgs& g, bool f16, bool gate, const Cut& c, void* ws, hipStream_t s) {
-  if (f16) return gate ? launch_product<true, true>(g, c, ws, s) : launch_product<true, false>(g, c, ws, s);
-  return gate ? launch_product<false, true>(g, c, ws, s) : launch_product<false, false>(g, c, ws, s);
-}
-
 // Workspace of the backward pass, in bytes (pieces 256-byte aligned).
 struct BackLayout {
-  int64_t NZ, ldz, mp, np;
+  int64_t NZ, ldz, sums_rows;
   Cut dx, dw;
-  size_t dz, dzt, xt, wt, sums, part, total;
+  size_t dz, sums, part, total;
 };
 BackLayout back_layout(const moe_linear_desc& d) {
   BackLayout L;
   L.NZ = (int64_t)d.cols * (gated(d) ? 2 : 1);
   L.ldz = round_up(L.NZ, 8);
-  L.np = round_up(L.NZ, 64);
-  L.mp = round_up(d.rows, 64);
-  L.dx = choose_cut(d.rows, d.depth, L.ldz, false);
-  L.dw = choose_cut(L.NZ, d.depth, L.mp, false);
+  L.sums_rows = (d.rows + 63) / 64;
+  L.dx = choose_cut(d.rows, d.depth, L.ldz, false, true);
+  L.dw = choose_cut(L.NZ, d.depth, d.rows, false, true);
   size_t off = 0;
   auto take = [&](size_t n) {
     const size_t at = off;
@@ -787,20 +820,17 @@ BackLayout back_layout(const moe_linear_desc& d) {
     return at;
   };
   L.dz = take((size_t)d.rows * L.ldz * 2);
-  L.dzt = take((size_t)L.NZ * L.mp * 2);
-  L.xt = take((size_t)d.depth * L.mp * 2);
-  L.wt = take((size_t)d.depth * L.np * 2);
-  L.sums = take((size_t)(L.mp / 64) * L.NZ * 4);
+  L.sums = take((size_t)L.sums_rows * L.NZ * 4);
   const size_t p1 = part_bytes(L.dx, d.rows, d.depth, false), p2 = part_bytes(L.dw, L.NZ, d.depth, false);
   L.part = take(p1 > p2 ? p1 : p2);
-  L.total = off;
+  L.total = off > 256 ? off : 256;
   return L;
 }
 
 }  // namespace
 
 size_t linear_ws_bytes(const moe_linear_desc& d) {
-  return part_bytes(choose_cut(d.rows, d.cols, d.depth, gated(d)), d.rows, d.cols, gated(d));
+  return part_bytes(choose_cut(d.rows, d.cols, d.depth, gated(d), false), d.rows, d.cols, gated(d));
 }
 
 size_t linear_back_ws_bytes(const moe_linear_desc& d) { return back_layout(d).total; }
@@ -825,7 +855,10 @@ hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void*
   e.vec = d.cols % 4 == 0 && e.ldo % 4 == 0 && aligned_to(b.out, o) && aligned_to(b.bias, 8) &&
           (!b.residual || (e.ldr % 4 == 0 && aligned_to(b.residual, o))) &&
           (!b.pre || (e.ldp % 4 == 0 && aligned_to(b.pre, 8)));
-  return run_product(g, d.dtype == MOE_F16, gated(d), choose_cut(d.rows, d.cols, d.depth, gated(d)), ws, s);
+  const Cut c = choose_cut(d.rows, d.cols, d.depth, gated(d), false);
+  if (d.dtype == MOE_F16)
+    return gated(d) ? launch_product<true, true, false, false>(g, c, ws, s) : launch_product<true, false, false, false>(g, c, ws, s);
+  return gated(d) ? launch_product<false, true, false, false>(g, c, ws, s) : launch_product<false, false, false, false>(g, c, ws, s);
 }
 
 hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b, void* ws, hipStream_t s) {
@@ -833,33 +866,31 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
   char* base = (char*)ws;
   const bool f16 = d.dtype == MOE_F16, f32 = d.out_dtype == MOE_F32;
   uint16_t* dz = (uint16_t*)(base + L.dz);
-  uint16_t* dzt = (uint16_t*)(base + L.dzt);
   // without an activation the incoming gradient can be the operand itself
   const bool direct = d.act == MOE_ACT_NONE && !f32 && d.cols % 8 == 0 && d.ld_out % 8 == 0 && aligned_to(b.d_out, 16);
-  const bool want_dz = b.dx && !direct;
-  if (d.rows > 0 && (want_dz || b.dw || b.dbias)) {
+  const bool want_dz = (b.dx || b.dw) && !direct;
+  if (d.rows > 0 && (want_dz || b.dbias)) {
     DzArgs a;
     a.d_out = b.d_out;
     a.pre = (const uint16_t*)b.pre;
     a.dz = want_dz ? dz : nullptr;
-    a.dzt = b.dw ? dzt : nullptr;
     a.sums = b.dbias ? (float*)(base + L.sums) : nullptr;
     a.M = d.rows; a.N = d.cols;
-    a.ldd = d.ld_out; a.ldp = d.ld_pre; a.ldz = L.ldz; a.mp = L.mp;
+    a.ldd = d.ld_out; a.ldp = d.ld_pre; a.ldz = L.ldz;
     a.act = d.act;
     a.d_f32 = f32;
     a.vec = d.cols % 4 == 0 && a.ldd % 4 == 0 && aligned_to(b.d_out, f32 ? 16 : 8) &&
             (d.act == MOE_ACT_NONE || (a.ldp % 4 == 0 && aligned_to(b.pre, 8)));
     // the up half's columns may start anywhere, and so end up to 7 past N
-    const dim3 grid((unsigned)((d.cols + (gated(d) ? 7 : 0) + 63) / 64), (unsigned)(L.mp / 64));
+    const dim3 grid((unsigned)((d.cols + (gated(d) ? 7 : 0) + 63) / 64), (unsigned)L.sums_rows);
     if (f16) hipLaunchKernelGGL((dz_kernel<true>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((dz_kernel<false>), grid, dim3(256), 0, s, a);
   }
   if (b.dbias) {
     const dim3 grid((unsigned)((L.NZ + 255) / 256));
-    const int rows = (int)(L.mp / 64);
-    if (f16) hipLaunchKernelGGL((bias_grad_kernel<true>), grid, dim3(256), 0, s, (const float*)(base + L.sums), rows, L.NZ, (uint16_t*)b.dbias);
-    else hipLaunchKernelGGL((bias_grad_kernel<false>), grid, dim3(256), 0, s, (const float*)(base + L.sums), rows, L.NZ, (uint16_t*)b.dbias);
+    const float* sums = (const float*)(base + L.sums);
+    if (f16) hipLaunchKernelGGL((bias_grad_kernel<true>), grid, dim3(256), 0, s, sums, (int)L.sums_rows, L.NZ, (uint16_t*)b.dbias);
+    else hipLaunchKernelGGL((bias_grad_kernel<false>), grid, dim3(256), 0, s, sums, (int)L.sums_rows, L.NZ, (uint16_t*)b.dbias);
   }
   hipError_t rc = hipGetLastError();
   if (rc != hipSuccess) return rc;
@@ -870,38 +901,33 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
   e.act = MOE_ACT_NONE;
   e.out_f32 = 0;
   e.N = d.depth;
+  g.a = direct ? (const uint16_t*)b.d_out : dz;
+  g.lda = direct ? d.ld_out : L.ldz;
   if (b.dx && d.rows > 0) {
-    uint16_t* wt = (uint16_t*)(base + L.wt);
-    const dim3 grid((unsigned)((d.depth + 63) / 64), (unsigned)(L.np / 64));
-    hipLaunchKernelGGL(transpose_kernel, grid, dim3(256), 0, s, (const uint16_t*)b.w, d.ld_w, L.NZ, d.depth, wt, L.np);
-    g.a = direct ? (const uint16_t*)b.d_out : dz;
-    g.lda = direct ? d.ld_out : L.ldz;
-    g.b = wt;
-    g.ldb = L.np;
-    g.K = L.ldz;
+    // dx [rows, depth]: dz along its columns, w [n, depth] across them.  dz's
+    // zero columns up to a multiple of 8 meet rows past w's end, also zeros.
+    g.b = (const uint16_t*)b.w;
+    g.ldb = d.ld_w;
+    g.K = L.NZ;
     e.M = d.rows;
     e.out = b.dx;
     e.ldo = d.ld_dx;
     e.vec = e.ldo % 4 == 0 && aligned_to(b.dx, 8);
-    rc = run_product(g, f16, false, L.dx, base + L.part, s);
+    rc = f16 ? launch_product<true, false, false, true>(g, L.dx, base + L.part, s)
+             : launch_product<false, false, false, true>(g, L.dx, base + L.part, s);
     if (rc != hipSuccess) return rc;
   }
   if (b.dw) {
-    uint16_t* xt = (uint16_t*)(base + L.xt);
-    if (d.rows > 0) {
-      const dim3 grid((unsigned)((d.depth + 63) / 64), (unsigned)(L.mp / 64));
-      hipLaunchKernelGGL(transpose_kernel, grid, dim3(256), 0, s, (const uint16_t*)b.x, d.ld_x, d.rows, d.depth, xt, L.mp);
-    }
-    g.a = dzt;
-    g.lda = L.mp;
-    g.b = xt;
-    g.ldb = L.mp;
-    g.K = L.mp;
+    // dw [n, depth]: both operands across the rows that are summed over
+    g.b = (const uint16_t*)b.x;
+    g.ldb = d.ld_x;
+    g.K = d.rows;
     e.M = L.NZ;
     e.out = b.dw;
     e.ldo = d.ld_dw;
     e.vec = e.ldo % 4 == 0 && aligned_to(b.dw, 8);
-    rc = run_product(g, f16, false, L.dw, base + L.part, s);
+    rc = f16 ? launch_product<true, false, true, true>(g, L.dw, base + L.part, s)
+             : launch_product<false, false, true, true>(g, L.dw, base + L.part, s);
   }
   return rc;
 }

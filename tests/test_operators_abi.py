@@ -150,4 +150,6 @@ def test_linear_workspace_sizes():
     assert m.moe_linear_sizes(_desc(m, rows=8192, cols=4096, depth=4096))["forward_bytes"] == 0
     z = m.moe_linear_sizes(_desc(m, rows=128, cols=64, depth=8192))
     assert z["forward_bytes"] % (128 * 64 * 4) == 0 and z["backward_bytes"] > 0
-    assert m.moe_linear_sizes(_desc(m, rows=0))["forward_bytes"] == 0
+    for kw in (dict(rows=0), dict(rows=0, cols=1, depth=8, act=5), dict(rows=1), dict(rows=1 << 21)):
+        z = m.moe_linear_sizes(_desc(m, **kw))
+        assert z["backward_bytes"] > 0 and z["forward_bytes"] == 0, kw
