@@ -82,34 +82,43 @@ constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143
 // gelu_tanh(z) = z (1 + tanh u) / 2 = z logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
 constexpr float kTwoSqrt2OverPi = 1.5957691216057308f, kCubic = 0.044715f;
 
-__device__ __forceinline__ float activate(int act, float z) {
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == MOE_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
+  else if constexpr (ACT == MOE_ACT_SILU) return z * logistic(z);
+  else if constexpr (ACT == MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+  else if constexpr (ACT == MOE_ACT_GELU_TANH) return z * logistic(kTwoSqrt2OverPi * (z + kCubic * z * z * z));
+  else return z;
+}
+template <int W>
+__device__ __forceinline__ void activate_all(int act, const float (&z)[W], float (&y)[W]) {
+  auto all = [&](auto tag) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < W; ++c) y[c] = activate<decltype(tag)::value>(z[c]);
+  };
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);
-    case MOE_ACT_SILU: return z * logistic(z);
-    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-    case MOE_ACT_GELU_TANH: return z * logistic(kTwoSqrt2OverPi * (z + kCubic * z * z * z));
-    default: return z;
+    case MOE_ACT_RELU: all(std::integral_constant<int, MOE_ACT_RELU>{}); break;
+    case MOE_ACT_SILU: all(std::integral_constant<int, MOE_ACT_SILU>{}); break;
+    case MOE_ACT_GELU: all(std::integral_constant<int, MOE_ACT_GELU>{}); break;
+    case MOE_ACT_GELU_TANH: all(std::integral_constant<int, MOE_ACT_GELU_TANH>{}); break;
+    default: all(std::integral_constant<int, MOE_ACT_NONE>{}); break;
   }
 }
 
-__device__ __forceinline__ float slope(int act, float z) {
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+  if constexpr (ACT == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   // far out the smooth activations' slopes are 0 and 1 to the last bit, and
   // their terms would be infinity times zero
-  if (act != MOE_ACT_RELU && act != MOE_ACT_NONE && fabsf(z) > 100.f) return z > 0.f ? 1.f : 0.f;
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case MOE_ACT_SILU: {
-      const float p = logistic(z);
-      return p * (1.0f + z * logistic(-z));
-    }
-    case MOE_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z) * kInvSqrt2Pi;
-    case MOE_ACT_GELU_TANH: {
-      const float u = kTwoSqrt2OverPi * (z + kCubic * z * z * z);
-      const float p = logistic(u);
-      return p + z * p * logistic(-u) * kTwoSqrt2OverPi * (1.0f + 3.0f * kCubic * z * z);
-    }
-    default: return 1.f;
+  if (fabsf(z) > 100.f) return z > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == MOE_ACT_SILU) {
+    return logistic(z) * (1.0f + z * logistic(-z));
+  } else if constexpr (ACT == MOE_ACT_GELU) {
+    return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z) * kInvSqrt2Pi;
+  } else {
+    const float u = kTwoSqrt2OverPi * (z + kCubic * z * z * z);
+    const float p = logistic(u);
+    return p + z * p * logistic(-u) * kTwoSqrt2OverPi * (1.0f + 3.0f * kCubic * z * z);
   }
 }
 
@@ -124,91 +133,111 @@ struct Epilogue {
   int N;         // output columns; a gated product has N gate and N up columns before the activation
   int act;
   int out_f32;
-  int vec;       // 4 columns an access: N and the pitches multiples of 4, bases aligned
+  int vec;       // columns an access may take: 8, 4 (N and the pitches multiples of it, the bases aligned) or 1
 };
 
-template <bool F16>
-__device__ __forceinline__ void load4(const uint16_t* p, int n, bool vec, float (&v)[4]) {
-  if (vec) {
-    const uint2 x = *(const uint2*)p;
-    v[0] = Elem<F16>::to_float((uint16_t)x.x); v[1] = Elem<F16>::to_float((uint16_t)(x.x >> 16));
-    v[2] = Elem<F16>::to_float((uint16_t)x.y); v[3] = Elem<F16>::to_float((uint16_t)(x.y >> 16));
+// W = 4 or 8 values of 16 bits, `left` of them in the row, `vec` as above
+template <bool F16, int W>
+__device__ __forceinline__ void load16(const uint16_t* p, int left, int vec, float (&v)[W]) {
+  if (W == 8 && vec == 8) {
+    const uint4 x = *(const uint4*)p;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int c = 0; c < W; ++c) v[c] = Elem<F16>::to_float((uint16_t)(w[c / 2] >> (c % 2 * 16)));
+  } else if (vec >= 4) {
+#pragma unroll
+    for (int h = 0; h < W; h += 4) {
+      const uint2 x = h < left ? *(const uint2*)(p + h) : make_uint2(0, 0);
+      v[h] = Elem<F16>::to_float((uint16_t)x.x); v[h + 1] = Elem<F16>::to_float((uint16_t)(x.x >> 16));
+      v[h + 2] = Elem<F16>::to_float((uint16_t)x.y); v[h + 3] = Elem<F16>::to_float((uint16_t)(x.y >> 16));
+    }
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = c < n ? Elem<F16>::to_float(p[c]) : 0.f;
+    for (int c = 0; c < W; ++c) v[c] = c < left ? Elem<F16>::to_float(p[c]) : 0.f;
   }
 }
-template <bool F16>
-__device__ __forceinline__ void store4(uint16_t* p, int n, bool vec, const float (&v)[4]) {
-  uint16_t b[4];
+template <bool F16, int W>
+__device__ __forceinline__ void store16(uint16_t* p, int left, int vec, const float (&v)[W]) {
+  uint32_t w[W / 2];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) b[c] = Elem<F16>::bits(v[c]);
-  if (vec) {
-    *(uint2*)p = make_uint2((uint32_t)b[0] | ((uint32_t)b[1] << 16), (uint32_t)b[2] | ((uint32_t)b[3] << 16));
+  for (int c = 0; c < W / 2; ++c)
+    w[c] = (uint32_t)Elem<F16>::bits(v[2 * c]) | ((uint32_t)Elem<F16>::bits(v[2 * c + 1]) << 16);
+  if (W == 8 && vec == 8) {
+    *(uint4*)p = make_uint4(w[0], w[1], w[W / 2 - 2], w[W / 2 - 1]);
+  } else if (vec >= 4) {
+#pragma unroll
+    for (int h = 0; h < W; h += 4)
+      if (h < left) *(uint2*)(p + h) = make_uint2(w[h / 2], w[h / 2 + 1]);
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c < n) p[c] = b[c];
+    for (int c = 0; c < W; ++c)
+      if (c < left) p[c] = (uint16_t)(w[c / 2] >> (c % 2 * 16));
+  }
+}
+// the same for fp32
+template <int W>
+__device__ __forceinline__ void load32(const float* p, int left, int vec, float (&v)[W]) {
+  if (vec >= 4) {
+#pragma unroll
+    for (int h = 0; h < W; h += 4) {
+      const float4 x = h < left ? *(const float4*)(p + h) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[h] = x.x; v[h + 1] = x.y; v[h + 2] = x.z; v[h + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < W; ++c) v[c] = c < left ? p[c] : 0.f;
+  }
+}
+template <int W>
+__device__ __forceinline__ void store32(float* p, int left, int vec, const float (&v)[W]) {
+  if (vec >= 4) {
+#pragma unroll
+    for (int h = 0; h < W; h += 4)
+      if (h < left) *(float4*)(p + h) = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < W; ++c)
+      if (c < left) p[c] = v[c];
   }
 }
 
-// Columns n .. n+3 of row m, of which those below N exist (n < N, m < M): z
-// the sums, u the up columns' sums of a gated product.
-template <bool F16, bool GATED>
-__device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int n, float (&z)[4], float (&u)[4]) {
-  const int left = e.N - n;
-  const bool vec = e.vec;
+// Columns n .. n + W - 1 of row m, of which those below N exist (n < N, m < M):
+// z the sums, u the up columns' sums of a gated product.
+template <bool F16, bool GATED, int W>
+__device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int n, float (&z)[W], float (&u)[W]) {
+  const int left = e.N - n, vec = e.vec;
   if (e.bias) {
-    float b[4];
-    load4<F16>(e.bias + n, left, vec, b);
+    float b[W];
+    load16<F16>(e.bias + n, left, vec, b);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) z[c] += b[c];
+    for (int c = 0; c < W; ++c) z[c] += b[c];
     if constexpr (GATED) {
-      load4<F16>(e.bias + e.N + n, left, vec, b);
+      load16<F16>(e.bias + e.N + n, left, vec, b);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) u[c] += b[c];
+      for (int c = 0; c < W; ++c) u[c] += b[c];
     }
   }
   if (e.pre) {
-    store4<F16>(e.pre + m * e.ldp + n, left, vec, z);
-    if constexpr (GATED) store4<F16>(e.pre + m * e.ldp + e.N + n, left, vec, u);
+    store16<F16>(e.pre + m * e.ldp + n, left, vec, z);
+    if constexpr (GATED) store16<F16>(e.pre + m * e.ldp + e.N + n, left, vec, u);
   }
-  float y[4];
+  float y[W];
+  if constexpr (GATED) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if constexpr (GATED) y[c] = z[c] * logistic(z[c]) * u[c];
-    else y[c] = activate(e.act, z[c]);
+    for (int c = 0; c < W; ++c) y[c] = z[c] * logistic(z[c]) * u[c];
+  } else {
+    activate_all(e.act, z, y);
   }
   const int64_t at = m * e.ldo + n;
-  if (e.out_f32) {
-    if (e.res) {
-      const float* r = (const float*)e.res + m * e.ldr + n;
-      if (vec) {
-        const float4 x = *(const float4*)r;
-        y[0] += x.x; y[1] += x.y; y[2] += x.z; y[3] += x.w;
-      } else {
+  if (e.res) {
+    float r[W];
+    if (e.out_f32) load32((const float*)e.res + m * e.ldr + n, left, vec, r);
+    else load16<F16>((const uint16_t*)e.res + m * e.ldr + n, left, vec, r);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < left) y[c] += r[c];
-      }
-    }
-    float* o = (float*)e.out + at;
-    if (vec) {
-      *(float4*)o = make_float4(y[0], y[1], y[2], y[3]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < left) o[c] = y[c];
-    }
-  } else {
-    if (e.res) {
-      float r[4];
-      load4<F16>((const uint16_t*)e.res + m * e.ldr + n, left, vec, r);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] += r[c];
-    }
-    store4<F16>((uint16_t*)e.out + at, left, vec, y);
+    for (int c = 0; c < W; ++c) y[c] += r[c];
   }
+  if (e.out_f32) store32((float*)e.out + at, left, vec, y);
+  else store16<F16>((uint16_t*)e.out + at, left, vec, y);
 }
 
 // --- tiled product ----------------------------------------------------------
@@ -481,10 +510,13 @@ void product_kernel(ProdArgs g) {
   constexpr int PITCH = C::template staged<GATED>::PITCH;
   float* stage = (float*)lds + wave * 32 * PITCH;
   const int ncol = n0 + (GATED ? wave_n * (C::WN / 2) : wave_n * C::WN);
-  constexpr int LPR = CW / 4, RPP = 64 / LPR;   // lanes a row, rows a pass
-  const int er = lane / LPR, ec = (lane % LPR) * 4;
-#pragma unroll
-  for (int j = 0; j < C::FM; ++j) {
+  constexpr int LPR = CW / 8, RPP = 64 / LPR;   // lanes a row (8 columns each), rows a pass
+  const int er = lane / LPR, ec = (lane % LPR) * 8;
+  const int n = ncol + ec;
+  // neither bias, activation, residual nor pre, 16-bit out: short enough to unroll
+  const bool plain = !PART && !GATED && !g.e.bias && !g.e.res && !g.e.pre && g.e.act == MOE_ACT_NONE && !g.e.out_f32;
+  auto rows32 = [&](auto jt) __attribute__((always_inline)) {
+    constexpr int j = decltype(jt)::value;
 #pragma unroll
     for (int i = 0; i < C::FN; ++i)
 #pragma unroll
@@ -493,28 +525,39 @@ void product_kernel(ProdArgs g) {
             make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
     __builtin_amdgcn_wave_barrier();
     const int64_t mj = m0 + wave_m * C::WM + 32 * j;
-#pragma unroll 1
-    for (int r = er; r < 32; r += RPP) {
+    auto row = [&](int r) __attribute__((always_inline)) {
       const int64_t m = mj + r;
-      const int n = ncol + ec;
+      float z[8], u[8];
+      load32(stage + r * PITCH + ec, 8, 4, z);
+      if constexpr (GATED) load32(stage + r * PITCH + CW + ec, 8, 4, u);
       if (m < g.e.M && n < g.e.N) {
-        const float4 x = *(const float4*)(stage + r * PITCH + ec);
-        float z[4] = {x.x, x.y, x.z, x.w}, u[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (GATED) {
-          const float4 y = *(const float4*)(stage + r * PITCH + CW + ec);
-          u[0] = y.x; u[1] = y.y; u[2] = y.z; u[3] = y.w;
-        }
         if constexpr (PART) {
           float* p = g.part + (split * g.e.M + m) * g.pitch + n;
-          *(float4*)p = make_float4(z[0], z[1], z[2], z[3]);
-          if constexpr (GATED) *(float4*)(p + g.up_col) = make_float4(u[0], u[1], u[2], u[3]);
+          store32(p, g.up_col - n, 4, z);
+          if constexpr (GATED) store32(p + g.up_col, g.up_col - n, 4, u);
+        } else if (plain) {
+          store16<F16>((uint16_t*)g.e.out + m * g.e.ldo + n, g.e.N - n, g.e.vec, z);
         } else {
-          finish4<F16, GATED>(g.e, m, n, z, u);
+          finish<F16, GATED>(g.e, m, n, z, u);
         }
       }
+    };
+    if (PART || plain) {
+#pragma unroll
+      for (int r = 0; r < 32; r += RPP) row(r + er);
+    } else {
+#pragma unroll 1
+      for (int r = er; r < 32; r += RPP) row(r);
     }
     __builtin_amdgcn_wave_barrier();
+  };
+  rows32(std::integral_constant<int, 0>{});
+  if constexpr (C::FM > 1) rows32(std::integral_constant<int, 1>{});
+  if constexpr (C::FM > 2) {
+    rows32(std::integral_constant<int, 2>{});
+    rows32(std::integral_constant<int, 3>{});
   }
+  static_assert(C::FM == 1 || C::FM == 2 || C::FM == 4, "row blocks");
 }
 
 // sums of a split product's partial sums, in split order, and the epilogue
@@ -535,7 +578,7 @@ __global__ __launch_bounds__(256) void join_kernel(ProdArgs g) {
         u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
       }
     }
-    finish4<F16, GATED>(g.e, m, n, z, u);
+    finish<F16, GATED>(g.e, m, n, z, u);
   }
 }
 
@@ -571,7 +614,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < TT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int U = TT >= 4 ? 2 : 4;   // K steps with their loads in flight together
+  constexpr int U = 4;   // K steps with their loads in flight together
   for (int k0 = wave * 32; k0 < K; k0 += kFewWaves * 32 * U) {
     v4u32 wv[U][NB], xv[U][TT];
 #pragma unroll
@@ -610,7 +653,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
       }
     }
     const int m = 16 * i + r, n = n0 + (lane >> 4) * 4;
-    if (m < M && n < g.e.N) finish4<F16, GATED>(g.e, m, n, z, u);
+    if (m < M && n < g.e.N) finish<F16, GATED>(g.e, m, n, z, u);
   }
 }
 
@@ -622,93 +665,94 @@ struct DzArgs {
   uint16_t* dz;           // [M, ldz] or null
   float* sums;            // [ceil(M / 64)][N or 2N] column sums of 64 rows each, or null
   int64_t M, ldd, ldp, ldz;
-  int N, act, d_f32, vec;
+  int N, act, d_f32, vec;   // vec as in Epilogue
 };
 
-// 64 rows x 64 columns a workgroup: thread t forms row t / 4, columns 16 (t % 4)
-// .. + 15.  Columns past N, up to ldz (a multiple of 8), are zeros.
-template <bool F16>
+// A thread forms 8 columns of two rows, 8 threads a row of 64 columns, so that
+// each access covers whole lines; with SUMS the 64 x 64 columns of a workgroup
+// are then added down in row order.  Columns past the last, up to ldz (a
+// multiple of 8), become zeros.  Memory bound: 8192 x 2 x 2048 (gated) FIGDZ us.
+template <bool F16, int ACT, bool SUMS>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
-  __shared__ float tile[64][65];
+  constexpr bool GATED = ACT == MOE_ACT_SWIGLU;
+  constexpr int HALVES = GATED ? 2 : 1;
+  __shared__ float tile[SUMS ? HALVES : 1][SUMS ? 32 : 1][SUMS ? 64 : 1];
   const int tid = threadIdx.x;
-  const int64_t m0 = (int64_t)blockIdx.y * 64;
-  const int n0 = blockIdx.x * 64;
-  const int r = tid / 4, c0 = (tid % 4) * 16;
-  const int64_t m = m0 + r;
-  const bool gated = a.act == MOE_ACT_SWIGLU;
-  const int halves = gated ? 2 : 1;
-  float g[16], p[16], u[16];
+  const int n = (int)blockIdx.x * 64 + (tid % 8) * 8;
+  const int left = a.N - n;
+  float part[HALVES][8];
 #pragma unroll
-  for (int c = 0; c < 16; c += 4) {
-    const int n = n0 + c0 + c;
-    float v[4] = {0.f, 0.f, 0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (m < a.M && n < a.N) {
-      const int left = a.N - n;
-      if (a.d_f32) {
-        const float* s = (const float*)a.d_out + m * a.ldd + n;
-        if (a.vec) {
-          const float4 q = *(const float4*)s;
-          v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-        } else {
+  for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < left) v[i] = s[i];
-        }
+    for (int c = 0; c < 8; ++c) part[h][c] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t m = (int64_t)blockIdx.y * 64 + 32 * i + tid / 8;
+    if (m >= a.M) continue;
+    float g[8] = {}, p[8] = {}, u[8] = {}, d[HALVES][8];
+    if (left > 0) {
+      if (a.d_f32) load32((const float*)a.d_out + m * a.ldd + n, left, a.vec, g);
+      else load16<F16>((const uint16_t*)a.d_out + m * a.ldd + n, left, a.vec, g);
+      if constexpr (ACT != MOE_ACT_NONE) load16<F16>(a.pre + m * a.ldp + n, left, a.vec, p);
+      if constexpr (GATED) load16<F16>(a.pre + m * a.ldp + a.N + n, left, a.vec, u);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if constexpr (GATED) {
+        d[0][c] = g[c] * u[c] * slope<MOE_ACT_SILU>(p[c]);
+        d[HALVES - 1][c] = g[c] * activate<MOE_ACT_SILU>(p[c]);
       } else {
-        load4<F16>((const uint16_t*)a.d_out + m * a.ldd + n, left, a.vec, v);
+        d[0][c] = ACT == MOE_ACT_NONE ? g[c] : g[c] * slope<ACT>(p[c]);
       }
-      if (a.act != MOE_ACT_NONE) load4<F16>(a.pre + m * a.ldp + n, left, a.vec, x);
-      if (gated) load4<F16>(a.pre + m * a.ldp + a.N + n, left, a.vec, y);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { g[c + i] = v[i]; p[c + i] = x[i]; u[c + i] = y[i]; }
+    for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) part[h][c] += d[h][c];
+    if (a.dz) {
+      // the last half also writes the zeros behind it
+      uint16_t* z = a.dz + m * a.ldz + n;
+      if constexpr (GATED) {
+        if (left > 0) store16<F16>(z, left, a.vec, d[0]);
+        const int room = (int)(a.ldz - a.N) - n;
+        if (room > 0) store16<F16>(z + a.N, room, a.vec, d[HALVES - 1]);
+      } else {
+        if (n < a.ldz) store16<F16>(z, 8, 8, d[0]);
+      }
+    }
   }
-  for (int h = 0; h < halves; ++h) {
-    if (h) __syncthreads();
+  if constexpr (SUMS) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float d;
-      if (gated) d = h == 0 ? g[c] * u[c] * slope(MOE_ACT_SILU, p[c]) : g[c] * (p[c] * logistic(p[c]));
-      else d = a.act == MOE_ACT_NONE ? g[c] : g[c] * slope(a.act, p[c]);
-      // outside the matrix there is no gradient, whatever the slope at 0
-      tile[r][c0 + c] = m < a.M && n0 + c0 + c < a.N ? d : 0.f;
-    }
+    for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) tile[h][tid / 8][(tid % 8) * 8 + c] = part[h][c];
     __syncthreads();
-    const int64_t first = (int64_t)h * a.N;   // column of the half's start
-    if (a.sums && tid < 64 && n0 + tid < a.N) {
+    const int col = tid % 64, h = tid / 64;
+    if (h < HALVES && (int)blockIdx.x * 64 + col < a.N) {
       float s = 0.f;
-      for (int i = 0; i < 64; ++i) s += tile[i][tid];
-      a.sums[blockIdx.y * (int64_t)halves * a.N + first + n0 + tid] = s;
-    }
-    // 8 values of a row a store, 64 x 8 stores
-    for (int i = tid; i < 512; i += 256) {
-      const int row = i / 8, part8 = (i % 8) * 8;
-      if (a.dz && m0 + row < a.M) {
-        uint16_t* d = a.dz + (m0 + row) * a.ldz + first + n0 + part8;
-        uint16_t b[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) b[c] = Elem<F16>::bits(tile[row][part8 + c]);
-        const int64_t end = h + 1 < halves ? (int64_t)a.N - n0 - part8 : a.ldz - first - n0 - part8;   // columns that are this half's
-        if (end >= 8 && (first & 7) == 0) {
-          *(uint4*)d = make_uint4(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16, b[4] | (uint32_t)b[5] << 16, b[6] | (uint32_t)b[7] << 16);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (c < end) d[c] = b[c];
-        }
-      }
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) s += tile[h][i][col];
+      a.sums[blockIdx.y * (int64_t)HALVES * a.N + (int64_t)h * a.N + blockIdx.x * 64 + col] = s;
     }
   }
 }
 
-// bias gradient: the column sums' rows added in order
+// bias gradient: the partial sums' rows added in a fixed order, four runs of
+// them by four threads a column
 template <bool F16>
 __global__ __launch_bounds__(256) void bias_grad_kernel(const float* sums, int rows, int64_t cols, uint16_t* out) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= cols) return;
+  __shared__ float run[4][64];
+  const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
+  const int q = threadIdx.x / 64, per = (rows + 3) / 4;
   float s = 0.f;
-  for (int i = 0; i < rows; ++i) s += sums[i * cols + n];
-  out[n] = Elem<F16>::bits(s);
+  if (n < cols) {
+#pragma unroll 8
+    for (int i = q * per; i < min(rows, (q + 1) * per); ++i) s += sums[i * cols + n];
+  }
+  run[q][threadIdx.x % 64] = s;
+  __syncthreads();
+  if (q == 0 && n < cols)
+    out[n] = Elem<F16>::bits(run[0][threadIdx.x] + run[1][threadIdx.x] + run[2][threadIdx.x] + run[3][threadIdx.x]);
 }
 
 // --- host -------------------------------------------------------------------
@@ -725,11 +769,21 @@ struct Cut {
 
 Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
   const int64_t NZ = gated ? 2 * N : N;
-  if (M <= 64 && !across) return {0, 1, round_up(K, kBK)};
-  // time of each choice from the rates one CU reaches with each tile and the
-  // cost of the partial sums' round trip; the smallest wins
+  // few rows: 64 x 4096 x 4096 takes 22 us that way and 15 us in tiles, 32 rows 13 us either way
+  if (M <= 32 && !across) return {0, 1, round_up(K, kBK)};
+  // Time of each choice, the smallest wins.  A K step of a CU's workgroups takes
+  // what their multiplications take at the rate the tile reaches, at least a
+  // load's latency; a round of workgroups adds its fill and epilogue; a split
+  // adds its partial sums' round trip and the second launch.  The constants are
+  // fitted to times of every choice over 60 products (both directions, 32 to
+  // 8192 rows): the choice costs 1.5% over the best one on average.  Both sides
+  // of a typical decision: 8192 x 256 x 7168 takes 43 us as 128 x 128 tiles in 4
+  // splits and 50 us as 256 x 256 in 8; 8192 x 2048 x 7168 takes 218 us and, as
+  // 256 x 256 in one piece, 190 us.
   static const int bm[4] = {0, 64, 128, 256}, bn[4] = {0, 128, 128, 256}, per_cu[4] = {0, 3, 2, 1};
-  static const double rate[4] = {0, 2.2e6, 3.4e6, 4.7e6};   // flop per us and CU
+  static const double rate[4] = {0, 3.5e6, 5.1e6, 6.2e6};       // flop per us and CU
+  static const double latency[4] = {0, 0.45, 0.75, 1.43};       // us a step
+  static const double round_us[4] = {0, 2.9, 4.0, 7.0};
   const int64_t steps = (K + kBK - 1) / kBK;
   Cut best = {1, 1, round_up(K, kBK)};
   double best_us = 1e30;
@@ -741,9 +795,10 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
       const int64_t per = (steps + s - 1) / s;
       const int64_t blocks = tiles * s, slots = (int64_t)kCus * per_cu[t];
       const int64_t conc = blocks >= slots ? per_cu[t] : (blocks + kCus - 1) / kCus;
-      const double step_us = conc * 2.0 * bm[t] * bn[t] * kBK / rate[t];
-      double us = (double)((blocks + kCus * conc - 1) / (kCus * conc)) * (per * (step_us > 0.5 ? step_us : 0.5) + 2.0);
-      if (s > 1) us += 4.0 + (double)s * M * NZ * 8 / 3.5e6;
+      const double work_us = conc * 2.0 * bm[t] * bn[t] * kBK / rate[t];
+      const double step_us = work_us > latency[t] ? work_us : latency[t];
+      double us = (double)((blocks + kCus * conc - 1) / (kCus * conc)) * (per * step_us + round_us[t]);
+      if (s > 1) us += 3.5 + (double)s * M * NZ * 8 / 6.8e6;
       if (us < best_us) {
         best_us = us;
         best = {t, s, per * kBK};
@@ -756,6 +811,26 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
 
 size_t part_bytes(const Cut& c, int64_t M, int64_t N, bool gated) {
   return c.splits > 1 ? (size_t)c.splits * M * round_up(N, 4) * (gated ? 2 : 1) * 4 : 0;
+}
+
+template <bool F16, int ACT>
+void launch_dz_act(const DzArgs& a, const dim3& grid, hipStream_t s) {
+  if (a.sums) hipLaunchKernelGGL((dz_kernel<F16, ACT, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((dz_kernel<F16, ACT, false>), grid, dim3(256), 0, s, a);
+}
+template <bool F16>
+void launch_dz(const DzArgs& a, hipStream_t s) {
+  // the up half's columns may start anywhere, and so end up to 7 past N
+  const int cols = a.N + (a.act == MOE_ACT_SWIGLU ? 7 : 0);
+  const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)((a.M + 63) / 64));
+  switch (a.act) {
+    case MOE_ACT_RELU: launch_dz_act<F16, MOE_ACT_RELU>(a, grid, s); break;
+    case MOE_ACT_SILU: launch_dz_act<F16, MOE_ACT_SILU>(a, grid, s); break;
+    case MOE_ACT_GELU: launch_dz_act<F16, MOE_ACT_GELU>(a, grid, s); break;
+    case MOE_ACT_GELU_TANH: launch_dz_act<F16, MOE_ACT_GELU_TANH>(a, grid, s); break;
+    case MOE_ACT_SWIGLU: launch_dz_act<F16, MOE_ACT_SWIGLU>(a, grid, s); break;
+    default: launch_dz_act<F16, MOE_ACT_NONE>(a, grid, s); break;
+  }
 }
 
 template <class C, bool F16, bool GATED, bool AX, bool BX>
@@ -785,8 +860,7 @@ hipError_t launch_product(ProdArgs& g, const Cut& c, void* ws, hipStream_t s) {
     if constexpr (!AX && !BX) {
       const dim3 grid((unsigned)((g.e.N + 15) / 16)), block(kFewWaves * 64);
       if (g.e.M <= 16) hipLaunchKernelGGL((few_rows_kernel<1, F16, GATED>), grid, block, 0, s, g);
-      else if (g.e.M <= 32) hipLaunchKernelGGL((few_rows_kernel<2, F16, GATED>), grid, block, 0, s, g);
-      else hipLaunchKernelGGL((few_rows_kernel<4, F16, GATED>), grid, block, 0, s, g);
+      else hipLaunchKernelGGL((few_rows_kernel<2, F16, GATED>), grid, block, 0, s, g);
     }
   } else if (c.tile == 1) {
     launch_tiles<Tile64, F16, GATED, AX, BX>(g, s);
@@ -851,10 +925,13 @@ hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void*
   e.ldr = d.ld_residual; e.ldp = d.ld_pre; e.ldo = d.ld_out;
   e.act = d.act;
   e.out_f32 = d.out_dtype == MOE_F32;
-  const size_t o = e.out_f32 ? 16 : 8;
-  e.vec = d.cols % 4 == 0 && e.ldo % 4 == 0 && aligned_to(b.out, o) && aligned_to(b.bias, 8) &&
-          (!b.residual || (e.ldr % 4 == 0 && aligned_to(b.residual, o))) &&
-          (!b.pre || (e.ldp % 4 == 0 && aligned_to(b.pre, 8)));
+  auto fits = [&](int w) {
+    const size_t o = e.out_f32 ? 16 : 2 * w;
+    return d.cols % w == 0 && e.ldo % w == 0 && aligned_to(b.out, o) && aligned_to(b.bias, 2 * w) &&
+           (!b.residual || (e.ldr % w == 0 && aligned_to(b.residual, o))) &&
+           (!b.pre || (e.ldp % w == 0 && aligned_to(b.pre, 2 * w)));
+  };
+  e.vec = fits(8) ? 8 : fits(4) ? 4 : 1;
   const Cut c = choose_cut(d.rows, d.cols, d.depth, gated(d), false);
   if (d.dtype == MOE_F16)
     return gated(d) ? launch_product<true, true, false, false>(g, c, ws, s) : launch_product<true, false, false, false>(g, c, ws, s);
@@ -879,15 +956,16 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
     a.ldd = d.ld_out; a.ldp = d.ld_pre; a.ldz = L.ldz;
     a.act = d.act;
     a.d_f32 = f32;
-    a.vec = d.cols % 4 == 0 && a.ldd % 4 == 0 && aligned_to(b.d_out, f32 ? 16 : 8) &&
-            (d.act == MOE_ACT_NONE || (a.ldp % 4 == 0 && aligned_to(b.pre, 8)));
-    // the up half's columns may start anywhere, and so end up to 7 past N
-    const dim3 grid((unsigned)((d.cols + (gated(d) ? 7 : 0) + 63) / 64), (unsigned)L.sums_rows);
-    if (f16) hipLaunchKernelGGL((dz_kernel<true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((dz_kernel<false>), grid, dim3(256), 0, s, a);
+    auto fits = [&](int w) {
+      return d.cols % w == 0 && a.ldd % w == 0 && aligned_to(b.d_out, f32 ? 16 : 2 * w) &&
+             (d.act == MOE_ACT_NONE || (a.ldp % w == 0 && aligned_to(b.pre, 2 * w)));
+    };
+    a.vec = fits(8) ? 8 : fits(4) ? 4 : 1;
+    if (f16) launch_dz<true>(a, s);
+    else launch_dz<false>(a, s);
   }
   if (b.dbias) {
-    const dim3 grid((unsigned)((L.NZ + 255) / 256));
+    const dim3 grid((unsigned)((L.NZ + 63) / 64));
     const float* sums = (const float*)(base + L.sums);
     if (f16) hipLaunchKernelGGL((bias_grad_kernel<true>), grid, dim3(256), 0, s, sums, (int)L.sums_rows, L.NZ, (uint16_t*)b.dbias);
     else hipLaunchKernelGGL((bias_grad_kernel<false>), grid, dim3(256), 0, s, sums, (int)L.sums_rows, L.NZ, (uint16_t*)b.dbias);
@@ -912,7 +990,7 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
     e.M = d.rows;
     e.out = b.dx;
     e.ldo = d.ld_dx;
-    e.vec = e.ldo % 4 == 0 && aligned_to(b.dx, 8);
+    e.vec = e.ldo % 8 == 0 && aligned_to(b.dx, 16) ? 8 : e.ldo % 4 == 0 && aligned_to(b.dx, 8) ? 4 : 1;
     rc = f16 ? launch_product<true, false, false, true>(g, L.dx, base + L.part, s)
              : launch_product<false, false, false, true>(g, L.dx, base + L.part, s);
     if (rc != hipSuccess) return rc;
@@ -925,7 +1003,7 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
     e.M = L.NZ;
     e.out = b.dw;
     e.ldo = d.ld_dw;
-    e.vec = e.ldo % 4 == 0 && aligned_to(b.dw, 8);
+    e.vec = e.ldo % 8 == 0 && aligned_to(b.dw, 16) ? 8 : e.ldo % 4 == 0 && aligned_to(b.dw, 8) ? 4 : 1;
     rc = f16 ? launch_product<true, false, true, true>(g, L.dw, base + L.part, s)
              : launch_product<false, false, true, true>(g, L.dw, base + L.part, s);
   }
