@@ -614,7 +614,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < TT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int U = 4;   // K steps with their loads in flight together
+  constexpr int U = 8 / TT;   // K steps with their loads in flight together
   for (int k0 = wave * 32; k0 < K; k0 += kFewWaves * 32 * U) {
     v4u32 wv[U][NB], xv[U][TT];
 #pragma unroll
@@ -783,7 +783,7 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
   static const int bm[4] = {0, 64, 128, 256}, bn[4] = {0, 128, 128, 256}, per_cu[4] = {0, 3, 2, 1};
   static const double rate[4] = {0, 3.5e6, 5.1e6, 6.2e6};       // flop per us and CU
   static const double latency[4] = {0, 0.45, 0.75, 1.43};       // us a step
-  static const double round_us[4] = {0, 2.9, 4.0, 7.0};
+  static const double round_us[4] = {0, 2.9, 4.0, 9.0};
   const int64_t steps = (K + kBK - 1) / kBK;
   Cut best = {1, 1, round_up(K, kBK)};
   double best_us = 1e30;

@@ -597,7 +597,8 @@ struct RouteBackArgs {
   float scale;
   int rows;   // rows a wavefront builds at once, at most 64 / SL
   int pitch;  // floats between them in LDS
-  int vec;    // four values a store (E, ld, ldd multiples of 4, bases aligned)
+  int vec;    // four values a store: E and ldd multiples of 4, the base aligned
+  int zvec;   // ... and a load: E and ld, likewise
 };
 
 __device__ __forceinline__ void store_as(void* p, int dtype, int64_t i, float v) {
@@ -617,90 +618,133 @@ __device__ __forceinline__ void store4_as(void* p, int dtype, int64_t i, const f
   }
 }
 
+// Rows t0 .. t0 + n - 1 of the full softmax's gradient, tile - s dot, by SL
+// lanes a row: its maximum and sum in one pass over the logits, 16 values a lane
+// at a time, and the result in a second one (from registers where 16 SL values
+// hold the row).
+template <int DT, int SL>
+__device__ __forceinline__ void full_softmax(const RouteBackArgs& a, int64_t t0, int n, float dot, const float* tile) {
+  constexpr int V = 16;
+  constexpr float kInf = __builtin_inff();
+  const int lane = threadIdx.x & 63, row = lane / SL, j = lane % SL;
+  const int item = DT == MOE_F32 ? 4 : 2;
+  const __amdgpu_buffer_rsrc_t zr = __builtin_amdgcn_make_buffer_rsrc(
+      (char*)const_cast<void*>(a.logits) + t0 * a.ld * item, (short)0, (int)(((n - 1) * a.ld + a.E) * item), kBufWord3);
+  const int chunks = (a.E + V * SL - 1) / (V * SL);
+  float z[V];
+  // values e0 + (i / 4) * 4 SL + i % 4 of the row
+  auto load = [&](int chunk) {
+    const int e0 = chunk * V * SL + 4 * j, rem = a.E - e0;
+    const int cnt = row < n && rem > 0 ? min(rem / (4 * SL) * 4 + min(rem % (4 * SL), 4), V) : 0;
+    load_places<DT, V>(zr, (uint32_t)(row * (uint32_t)a.ld + e0) * item, 4 * SL, cnt, a.zvec, z);
+    return cnt;
+  };
+  float m = -kInf, s = 0.f;
+  int cnt = 0;
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    cnt = load(c);
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, z[i]);
+    if (top > -kInf) {
+      s = m > -kInf ? s * exp_fast(m - top) : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += exp_fast(z[i] - top);
+    }
+    m = top;
+  }
+  const float all = max_lanes<SL>(m);
+  const float base = all == -kInf ? 0.f : all;
+  s = sum_lanes<SL>(m > -kInf ? s * exp_fast(m - base) : 0.f);
+  const float f = s == 0.f ? 0.f * dot : dot / s;   // every expert masked: no gradient (of a NaN row NaN)
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    if (chunks > 1) cnt = load(c);
+    const int e0 = c * V * SL + 4 * j;
+    const int64_t out = (t0 + row) * a.ldd;
+    const float* g = tile + row * a.pitch;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const int e = e0 + i * SL;
+      if (i >= cnt) continue;
+      const float4 h = *(const float4*)(g + e);   // (the pitch is a multiple of 4)
+      const float4 v = make_float4(h.x - f * exp_fast(z[i] - base), h.y - f * exp_fast(z[i + 1] - base),
+                                   h.z - f * exp_fast(z[i + 2] - base), h.w - f * exp_fast(z[i + 3] - base));
+      if (a.vec) {
+        store4_as(a.dz, a.dtype, out + e, v);
+      } else {
+        store_as(a.dz, a.dtype, out + e, v.x);
+        if (i + 1 < cnt) store_as(a.dz, a.dtype, out + e + 1, v.y);
+        if (i + 2 < cnt) store_as(a.dz, a.dtype, out + e + 2, v.z);
+        if (i + 3 < cnt) store_as(a.dz, a.dtype, out + e + 3, v.w);
+      }
+    }
+  }
+}
+
 // SL lanes hold the slots of a row (k <= SL)
 template <int SL>
 __global__ __launch_bounds__(kRouteThreads) void route_back_kernel(RouteBackArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   float* tile = (float*)smem + (size_t)wave * a.rows * a.pitch;
-  const int64_t waves = (int64_t)gridDim.x * (kRouteThreads / 64);
   const int row = lane / SL, j = lane % SL;
-  constexpr float kInf = __builtin_inff();
-  for (int64_t t0 = ((int64_t)blockIdx.x * (kRouteThreads / 64) + wave) * a.rows; t0 < a.T; t0 += waves * a.rows) {
-    const int64_t t = t0 + row;
-    const int n = (int)min((int64_t)a.rows, a.T - t0);
-    const bool on = row < n && j < a.k;
-    int id = -1;
-    float w = 0.f, g = 0.f, z = 0.f;
-    if (on) {
-      id = a.ids[t * a.k + j];
-      w = a.w[t * a.k + j];
-      if (id < 0 || id >= a.E || w == 0.f) id = -1;   // constants, or no expert at all
-      if (id >= 0) {
-        g = a.dw[t * a.k + j];
-        if (a.score == MOE_SCORE_SIGMOID) z = load_as_float(a.logits, a.dtype, t * a.ld + id);
-      } else {
-        w = 0.f;
-      }
-    }
-    for (int i = lane * 4; i < n * a.pitch; i += 256) *(float4*)(tile + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
-    float dot = id >= 0 ? g * w : 0.f;
-    dot = sum_lanes<SL>(dot);
-    float v = 0.f;
+  const int64_t t0 = ((int64_t)blockIdx.x * (kRouteThreads / 64) + wave) * a.rows;
+  if (t0 >= a.T) return;
+  const int64_t t = t0 + row;
+  const int n = (int)min((int64_t)a.rows, a.T - t0);
+  const bool on = row < n && j < a.k;
+  int id = -1;
+  float w = 0.f, g = 0.f, z = 0.f;
+  if (on) {
+    id = a.ids[t * a.k + j];
+    w = a.w[t * a.k + j];
+    if (id < 0 || id >= a.E || w == 0.f) id = -1;   // constants, or no expert at all
     if (id >= 0) {
-      v = a.renorm ? w * (g - dot / a.scale) : w * g;
-      if (a.score == MOE_SCORE_SIGMOID) v *= 1.0f / (1.0f + expf(z));
-    }
-    // an expert listed in several slots: the first of them adds all up
-    float total = 0.f;
-    bool first = true;
-    for (int i = 0; i < a.k; ++i) {
-      const int oid = __shfl(id, row * SL + i);
-      const float ov = __shfl(v, row * SL + i);
-      if (oid == id) {
-        total += ov;
-        if (i < j) first = false;
-      }
-    }
-    if (id >= 0 && first) tile[row * a.pitch + id] = total;
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
-    if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) {
-      // the other part of the full softmax, - s_e D, a row at a time
-      for (int r = 0; r < n; ++r) {
-        const int64_t base = (t0 + r) * a.ld;
-        float m = -kInf;
-        for (int e = lane; e < a.E; e += 64) m = fmaxf(m, load_as_float(a.logits, a.dtype, base + e));
-        m = max_lanes<64>(m);
-        if (m == -kInf) m = 0.f;
-        float s = 0.f;
-        for (int e = lane; e < a.E; e += 64) s += exp_fast(load_as_float(a.logits, a.dtype, base + e) - m);
-        s = sum_lanes<64>(s);
-        const float f = __shfl(dot, r * SL) / (s > 0.f ? s : 1.f);
-        for (int e = lane; e < a.E; e += 64) {
-          const float q = exp_fast(load_as_float(a.logits, a.dtype, base + e) - m);
-          tile[r * a.pitch + e] -= q * f;
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
-      __threadfence_block();
-    }
-    if (a.vec) {
-      const int per = a.E / 4;
-      for (int i = lane; i < n * per; i += 64) {
-        const int r = i / per, e = (i - r * per) * 4;
-        store4_as(a.dz, a.dtype, (t0 + r) * a.ldd + e, *(const float4*)(tile + r * a.pitch + e));
-      }
+      g = a.dw[t * a.k + j];
+      if (a.score == MOE_SCORE_SIGMOID) z = load_as_float(a.logits, a.dtype, t * a.ld + id);
     } else {
-      for (int i = lane; i < n * a.E; i += 64) {
-        const int r = i / a.E, e = i - r * a.E;
-        store_as(a.dz, a.dtype, (t0 + r) * a.ldd + e, tile[r * a.pitch + e]);
-      }
+      w = 0.f;
     }
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
+  }
+  for (int i = lane * 4; i < n * a.pitch; i += 256) *(float4*)(tile + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+  lds_wait();
+  float dot = id >= 0 ? g * w : 0.f;
+  dot = sum_lanes<SL>(dot);
+  float v = 0.f;
+  if (id >= 0) {
+    v = a.renorm ? w * (g - dot / a.scale) : w * g;
+    if (a.score == MOE_SCORE_SIGMOID) v *= 1.0f / (1.0f + expf(z));
+  }
+  // an expert listed in several slots: the first of them adds all up
+  float total = 0.f;
+  bool first = true;
+  for (int i = 0; i < a.k; ++i) {
+    const int oid = __shfl(id, row * SL + i);
+    const float ov = __shfl(v, row * SL + i);
+    if (oid == id) {
+      total += ov;
+      if (i < j) first = false;
+    }
+  }
+  if (id >= 0 && first) tile[row * a.pitch + id] = total;
+  lds_wait();
+  if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) {
+    // the other part of the full softmax, - s_e D: SL lanes a row
+    if (a.dtype == MOE_F32) full_softmax<MOE_F32, SL>(a, t0, n, dot, tile);
+    else if (a.dtype == MOE_BF16) full_softmax<MOE_BF16, SL>(a, t0, n, dot, tile);
+    else full_softmax<MOE_F16, SL>(a, t0, n, dot, tile);
+    return;
+  }
+  if (row >= n) return;
+  const float* from = tile + row * a.pitch;
+  const int64_t to = t * a.ldd;
+  if (a.vec) {
+    for (int e = 4 * j; e < a.E; e += 4 * SL) store4_as(a.dz, a.dtype, to + e, *(const float4*)(from + e));
+  } else {
+    for (int e = j; e < a.E; e += SL) store_as(a.dz, a.dtype, to + e, from[e]);
   }
 }
 
@@ -765,6 +809,7 @@ hipError_t launch_route_backward(int64_t T, int E, int k, const void* logits, in
   a.score = o.score; a.renorm = o.renorm; a.scale = o.scale;
   const size_t item = dtype == MOE_F32 ? 4 : 2;
   a.vec = E % 4 == 0 && ldd % 4 == 0 && aligned_to(dz, 4 * item);
+  a.zvec = E % 4 == 0 && ld % 4 == 0 && aligned_to(logits, 4 * item);
   a.pitch = (E + 3) / 4 * 4;
   const int sl = k <= 8 ? 8 : 32;
   // up to 8 KB of rows a wavefront
@@ -773,8 +818,7 @@ hipError_t launch_route_backward(int64_t T, int E, int k, const void* logits, in
   a.rows = rows < 64 / sl ? rows : 64 / sl;
   constexpr int WPB = kRouteThreads / 64;
   const size_t lds = (size_t)WPB * a.rows * a.pitch * 4;
-  const int64_t blocks = (T + (int64_t)a.rows * WPB - 1) / ((int64_t)a.rows * WPB);
-  const unsigned grid = (unsigned)(blocks < 8192 ? blocks : 8192);
+  const unsigned grid = (unsigned)((T + (int64_t)a.rows * WPB - 1) / ((int64_t)a.rows * WPB));
   if (sl == 8) hipLaunchKernelGGL((route_back_kernel<8>), dim3(grid), dim3(kRouteThreads), lds, s, a);
   else hipLaunchKernelGGL((route_back_kernel<32>), dim3(grid), dim3(kRouteThreads), lds, s, a);
   return hipGetLastError();
