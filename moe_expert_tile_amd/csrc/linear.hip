@@ -133,71 +133,73 @@ struct Epilogue {
   int N;         // output columns; a gated product has N gate and N up columns before the activation
   int act;
   int out_f32;
-  int vec;       // columns an access may take: 8, 4 (N and the pitches multiples of it, the bases aligned) or 1
 };
 
-// W = 4 or 8 values of 16 bits, `left` of them in the row, `vec` as above
+// Whole accesses at any alignment of the element type (rows of odd lengths
+// start anywhere): the global memory instructions allow it.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <class V, int ALIGN>
+struct __attribute__((packed, aligned(ALIGN))) Loose {
+  V v;
+};
+
+// W = 4 or 8 values of 16 bits, of which `left` are in the row
 template <bool F16, int W>
-__device__ __forceinline__ void load16(const uint16_t* p, int left, int vec, float (&v)[W]) {
-  if (W == 8 && vec == 8) {
-    const uint4 x = *(const uint4*)p;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ void load16(const uint16_t* p, int left, float (&v)[W]) {
+  typedef std::conditional_t<W == 8, u32x4, u32x2> V;
+  if (left >= W) {
+    const V x = ((const Loose<V, 2>*)p)->v;
 #pragma unroll
-    for (int c = 0; c < W; ++c) v[c] = Elem<F16>::to_float((uint16_t)(w[c / 2] >> (c % 2 * 16)));
-  } else if (vec >= 4) {
-#pragma unroll
-    for (int h = 0; h < W; h += 4) {
-      const uint2 x = h < left ? *(const uint2*)(p + h) : make_uint2(0, 0);
-      v[h] = Elem<F16>::to_float((uint16_t)x.x); v[h + 1] = Elem<F16>::to_float((uint16_t)(x.x >> 16));
-      v[h + 2] = Elem<F16>::to_float((uint16_t)x.y); v[h + 3] = Elem<F16>::to_float((uint16_t)(x.y >> 16));
-    }
+    for (int c = 0; c < W; ++c) v[c] = Elem<F16>::to_float((uint16_t)(x[c / 2] >> (c % 2 * 16)));
   } else {
 #pragma unroll
     for (int c = 0; c < W; ++c) v[c] = c < left ? Elem<F16>::to_float(p[c]) : 0.f;
   }
 }
 template <bool F16, int W>
-__device__ __forceinline__ void store16(uint16_t* p, int left, int vec, const float (&v)[W]) {
-  uint32_t w[W / 2];
+__device__ __forceinline__ void store16(uint16_t* p, int left, const float (&v)[W]) {
+  typedef std::conditional_t<W == 8, u32x4, u32x2> V;
+  V x;
 #pragma unroll
   for (int c = 0; c < W / 2; ++c)
-    w[c] = (uint32_t)Elem<F16>::bits(v[2 * c]) | ((uint32_t)Elem<F16>::bits(v[2 * c + 1]) << 16);
-  if (W == 8 && vec == 8) {
-    *(uint4*)p = make_uint4(w[0], w[1], w[W / 2 - 2], w[W / 2 - 1]);
-  } else if (vec >= 4) {
-#pragma unroll
-    for (int h = 0; h < W; h += 4)
-      if (h < left) *(uint2*)(p + h) = make_uint2(w[h / 2], w[h / 2 + 1]);
+    x[c] = (uint32_t)Elem<F16>::bits(v[2 * c]) | ((uint32_t)Elem<F16>::bits(v[2 * c + 1]) << 16);
+  if (left >= W) {
+    ((Loose<V, 2>*)p)->v = x;
   } else {
 #pragma unroll
     for (int c = 0; c < W; ++c)
-      if (c < left) p[c] = (uint16_t)(w[c / 2] >> (c % 2 * 16));
+      if (c < left) p[c] = (uint16_t)(x[c / 2] >> (c % 2 * 16));
   }
 }
 // the same for fp32
 template <int W>
-__device__ __forceinline__ void load32(const float* p, int left, int vec, float (&v)[W]) {
-  if (vec >= 4) {
+__device__ __forceinline__ void load32(const float* p, int left, float (&v)[W]) {
+  typedef float V __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int h = 0; h < W; h += 4) {
-      const float4 x = h < left ? *(const float4*)(p + h) : make_float4(0.f, 0.f, 0.f, 0.f);
-      v[h] = x.x; v[h + 1] = x.y; v[h + 2] = x.z; v[h + 3] = x.w;
+  for (int h = 0; h < W; h += 4) {
+    if (left >= h + 4) {
+      const V x = ((const Loose<V, 4>*)(p + h))->v;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[h + c] = x[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[h + c] = h + c < left ? p[h + c] : 0.f;
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < W; ++c) v[c] = c < left ? p[c] : 0.f;
   }
 }
 template <int W>
-__device__ __forceinline__ void store32(float* p, int left, int vec, const float (&v)[W]) {
-  if (vec >= 4) {
+__device__ __forceinline__ void store32(float* p, int left, const float (&v)[W]) {
+  typedef float V __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int h = 0; h < W; h += 4)
-      if (h < left) *(float4*)(p + h) = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
-  } else {
+  for (int h = 0; h < W; h += 4) {
+    if (left >= h + 4) {
+      ((Loose<V, 4>*)(p + h))->v = V{v[h], v[h + 1], v[h + 2], v[h + 3]};
+    } else {
 #pragma unroll
-    for (int c = 0; c < W; ++c)
-      if (c < left) p[c] = v[c];
+      for (int c = 0; c < 4; ++c)
+        if (h + c < left) p[h + c] = v[h + c];
+    }
   }
 }
 
@@ -205,21 +207,21 @@ __device__ __forceinline__ void store32(float* p, int left, int vec, const float
 // z the sums, u the up columns' sums of a gated product.
 template <bool F16, bool GATED, int W>
 __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int n, float (&z)[W], float (&u)[W]) {
-  const int left = e.N - n, vec = e.vec;
+  const int left = e.N - n;
   if (e.bias) {
     float b[W];
-    load16<F16>(e.bias + n, left, vec, b);
+    load16<F16>(e.bias + n, left, b);
 #pragma unroll
     for (int c = 0; c < W; ++c) z[c] += b[c];
     if constexpr (GATED) {
-      load16<F16>(e.bias + e.N + n, left, vec, b);
+      load16<F16>(e.bias + e.N + n, left, b);
 #pragma unroll
       for (int c = 0; c < W; ++c) u[c] += b[c];
     }
   }
   if (e.pre) {
-    store16<F16>(e.pre + m * e.ldp + n, left, vec, z);
-    if constexpr (GATED) store16<F16>(e.pre + m * e.ldp + e.N + n, left, vec, u);
+    store16<F16>(e.pre + m * e.ldp + n, left, z);
+    if constexpr (GATED) store16<F16>(e.pre + m * e.ldp + e.N + n, left, u);
   }
   float y[W];
   if constexpr (GATED) {
@@ -231,13 +233,13 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int n, floa
   const int64_t at = m * e.ldo + n;
   if (e.res) {
     float r[W];
-    if (e.out_f32) load32((const float*)e.res + m * e.ldr + n, left, vec, r);
-    else load16<F16>((const uint16_t*)e.res + m * e.ldr + n, left, vec, r);
+    if (e.out_f32) load32((const float*)e.res + m * e.ldr + n, left, r);
+    else load16<F16>((const uint16_t*)e.res + m * e.ldr + n, left, r);
 #pragma unroll
     for (int c = 0; c < W; ++c) y[c] += r[c];
   }
-  if (e.out_f32) store32((float*)e.out + at, left, vec, y);
-  else store16<F16>((uint16_t*)e.out + at, left, vec, y);
+  if (e.out_f32) store32((float*)e.out + at, left, y);
+  else store16<F16>((uint16_t*)e.out + at, left, y);
 }
 
 // --- tiled product ----------------------------------------------------------
@@ -528,15 +530,19 @@ void product_kernel(ProdArgs g) {
     auto row = [&](int r) __attribute__((always_inline)) {
       const int64_t m = mj + r;
       float z[8], u[8];
-      load32(stage + r * PITCH + ec, 8, 4, z);
-      if constexpr (GATED) load32(stage + r * PITCH + CW + ec, 8, 4, u);
+      const float4 x0 = *(const float4*)(stage + r * PITCH + ec), x1 = *(const float4*)(stage + r * PITCH + ec + 4);
+      z[0] = x0.x; z[1] = x0.y; z[2] = x0.z; z[3] = x0.w; z[4] = x1.x; z[5] = x1.y; z[6] = x1.z; z[7] = x1.w;
+      if constexpr (GATED) {
+        const float4 y0 = *(const float4*)(stage + r * PITCH + CW + ec), y1 = *(const float4*)(stage + r * PITCH + CW + ec + 4);
+        u[0] = y0.x; u[1] = y0.y; u[2] = y0.z; u[3] = y0.w; u[4] = y1.x; u[5] = y1.y; u[6] = y1.z; u[7] = y1.w;
+      }
       if (m < g.e.M && n < g.e.N) {
         if constexpr (PART) {
           float* p = g.part + (split * g.e.M + m) * g.pitch + n;
-          store32(p, g.up_col - n, 4, z);
-          if constexpr (GATED) store32(p + g.up_col, g.up_col - n, 4, u);
+          store32(p, g.up_col - n, z);
+          if constexpr (GATED) store32(p + g.up_col, g.up_col - n, u);
         } else if (plain) {
-          store16<F16>((uint16_t*)g.e.out + m * g.e.ldo + n, g.e.N - n, g.e.vec, z);
+          store16<F16>((uint16_t*)g.e.out + m * g.e.ldo + n, g.e.N - n, z);
         } else {
           finish<F16, GATED>(g.e, m, n, z, u);
         }
@@ -665,7 +671,7 @@ struct DzArgs {
   uint16_t* dz;           // [M, ldz] or null
   float* sums;            // [ceil(M / 64)][N or 2N] column sums of 64 rows each, or null
   int64_t M, ldd, ldp, ldz;
-  int N, act, d_f32, vec;   // vec as in Epilogue
+  int N, act, d_f32;
 };
 
 // A thread forms 8 columns of two rows, 8 threads a row of 64 columns, so that
@@ -691,10 +697,10 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     if (m >= a.M) continue;
     float g[8] = {}, p[8] = {}, u[8] = {}, d[HALVES][8];
     if (left > 0) {
-      if (a.d_f32) load32((const float*)a.d_out + m * a.ldd + n, left, a.vec, g);
-      else load16<F16>((const uint16_t*)a.d_out + m * a.ldd + n, left, a.vec, g);
-      if constexpr (ACT != MOE_ACT_NONE) load16<F16>(a.pre + m * a.ldp + n, left, a.vec, p);
-      if constexpr (GATED) load16<F16>(a.pre + m * a.ldp + a.N + n, left, a.vec, u);
+      if (a.d_f32) load32((const float*)a.d_out + m * a.ldd + n, left, g);
+      else load16<F16>((const uint16_t*)a.d_out + m * a.ldd + n, left, g);
+      if constexpr (ACT != MOE_ACT_NONE) load16<F16>(a.pre + m * a.ldp + n, left, p);
+      if constexpr (GATED) load16<F16>(a.pre + m * a.ldp + a.N + n, left, u);
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -713,11 +719,11 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
       // the last half also writes the zeros behind it
       uint16_t* z = a.dz + m * a.ldz + n;
       if constexpr (GATED) {
-        if (left > 0) store16<F16>(z, left, a.vec, d[0]);
+        if (left > 0) store16<F16>(z, left, d[0]);
         const int room = (int)(a.ldz - a.N) - n;
-        if (room > 0) store16<F16>(z + a.N, room, a.vec, d[HALVES - 1]);
+        if (room > 0) store16<F16>(z + a.N, room, d[HALVES - 1]);
       } else {
-        if (n < a.ldz) store16<F16>(z, 8, 8, d[0]);
+        if (n < a.ldz) store16<F16>(z, 8, d[0]);
       }
     }
   }
@@ -925,13 +931,6 @@ hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void*
   e.ldr = d.ld_residual; e.ldp = d.ld_pre; e.ldo = d.ld_out;
   e.act = d.act;
   e.out_f32 = d.out_dtype == MOE_F32;
-  auto fits = [&](int w) {
-    const size_t o = e.out_f32 ? 16 : 2 * w;
-    return d.cols % w == 0 && e.ldo % w == 0 && aligned_to(b.out, o) && aligned_to(b.bias, 2 * w) &&
-           (!b.residual || (e.ldr % w == 0 && aligned_to(b.residual, o))) &&
-           (!b.pre || (e.ldp % w == 0 && aligned_to(b.pre, 2 * w)));
-  };
-  e.vec = fits(8) ? 8 : fits(4) ? 4 : 1;
   const Cut c = choose_cut(d.rows, d.cols, d.depth, gated(d), false);
   if (d.dtype == MOE_F16)
     return gated(d) ? launch_product<true, true, false, false>(g, c, ws, s) : launch_product<true, false, false, false>(g, c, ws, s);
@@ -956,11 +955,6 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
     a.ldd = d.ld_out; a.ldp = d.ld_pre; a.ldz = L.ldz;
     a.act = d.act;
     a.d_f32 = f32;
-    auto fits = [&](int w) {
-      return d.cols % w == 0 && a.ldd % w == 0 && aligned_to(b.d_out, f32 ? 16 : 2 * w) &&
-             (d.act == MOE_ACT_NONE || (a.ldp % w == 0 && aligned_to(b.pre, 2 * w)));
-    };
-    a.vec = fits(8) ? 8 : fits(4) ? 4 : 1;
     if (f16) launch_dz<true>(a, s);
     else launch_dz<false>(a, s);
   }
@@ -990,7 +984,6 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
     e.M = d.rows;
     e.out = b.dx;
     e.ldo = d.ld_dx;
-    e.vec = e.ldo % 8 == 0 && aligned_to(b.dx, 16) ? 8 : e.ldo % 4 == 0 && aligned_to(b.dx, 8) ? 4 : 1;
     rc = f16 ? launch_product<true, false, false, true>(g, L.dx, base + L.part, s)
              : launch_product<false, false, false, true>(g, L.dx, base + L.part, s);
     if (rc != hipSuccess) return rc;
@@ -1003,7 +996,6 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
     e.M = L.NZ;
     e.out = b.dw;
     e.ldo = d.ld_dw;
-    e.vec = e.ldo % 8 == 0 && aligned_to(b.dw, 16) ? 8 : e.ldo % 4 == 0 && aligned_to(b.dw, 8) ? 4 : 1;
     rc = f16 ? launch_product<true, false, true, true>(g, L.dw, base + L.part, s)
              : launch_product<false, false, true, true>(g, L.dw, base + L.part, s);
   }
