@@ -157,14 +157,14 @@ __device__ __forceinline__ void load16(const uint16_t* p, int left, float (&v)[W
     for (int c = 0; c < W; ++c) v[c] = c < left ? Elem<F16>::to_float(p[c]) : 0.f;
   }
 }
-template <bool F16, int W>
+template <bool F16, int W, bool WHOLE = false>
 __device__ __forceinline__ void store16(uint16_t* p, int left, const float (&v)[W]) {
   typedef std::conditional_t<W == 8, u32x4, u32x2> V;
   V x;
 #pragma unroll
   for (int c = 0; c < W / 2; ++c)
     x[c] = (uint32_t)Elem<F16>::bits(v[2 * c]) | ((uint32_t)Elem<F16>::bits(v[2 * c + 1]) << 16);
-  if (left >= W) {
+  if (WHOLE || left >= W) {
     ((Loose<V, 2>*)p)->v = x;
   } else {
 #pragma unroll
@@ -203,21 +203,43 @@ __device__ __forceinline__ void store32(float* p, int left, const float (&v)[W])
   }
 }
 
-// Columns n .. n + W - 1 of row m, of which those below N exist (n < N, m < M):
-// z the sums, u the up columns' sums of a gated product.
+// The bias of columns n .. n + W - 1 (and of the up columns), and the residual
+// there of row m; zeros without one.  Columns from N on read zeros.
 template <bool F16, bool GATED, int W>
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int n, float (&z)[W], float (&u)[W]) {
+__device__ __forceinline__ void load_bias(const Epilogue& e, int n, float (&bz)[W], float (&bu)[W]) {
+#pragma unroll
+  for (int c = 0; c < W; ++c) bz[c] = bu[c] = 0.f;
+  if (e.bias && n < e.N) {
+    load16<F16>(e.bias + n, e.N - n, bz);
+    if constexpr (GATED) load16<F16>(e.bias + e.N + n, e.N - n, bu);
+  }
+}
+template <bool F16, int W>
+__device__ __forceinline__ void load_residual(const Epilogue& e, int64_t m, int n, float (&r)[W]) {
+#pragma unroll
+  for (int c = 0; c < W; ++c) r[c] = 0.f;
+  if (e.res && m < e.M && n < e.N) {
+    if (e.out_f32) load32((const float*)e.res + m * e.ldr + n, e.N - n, r);
+    else load16<F16>((const uint16_t*)e.res + m * e.ldr + n, e.N - n, r);
+  }
+}
+
+template <bool F16, int W>
+__device__ __forceinline__ void store_out(const Epilogue& e, int64_t m, int n, const float (&y)[W]) {
+  if (e.out_f32) store32((float*)e.out + m * e.ldo + n, e.N - n, y);
+  else store16<F16>((uint16_t*)e.out + m * e.ldo + n, e.N - n, y);
+}
+
+// Columns n .. n + W - 1 of row m, of which those below N exist (n < N, m < M):
+// z the sums, u the up columns' sums of a gated product, bz, bu and r as above.
+template <bool F16, bool GATED, int W>
+__device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int n, float (&z)[W], float (&u)[W],
+                                       const float (&bz)[W], const float (&bu)[W], const float (&r)[W]) {
   const int left = e.N - n;
-  if (e.bias) {
-    float b[W];
-    load16<F16>(e.bias + n, left, b);
 #pragma unroll
-    for (int c = 0; c < W; ++c) z[c] += b[c];
-    if constexpr (GATED) {
-      load16<F16>(e.bias + e.N + n, left, b);
-#pragma unroll
-      for (int c = 0; c < W; ++c) u[c] += b[c];
-    }
+  for (int c = 0; c < W; ++c) {
+    z[c] += bz[c];
+    if constexpr (GATED) u[c] += bu[c];
   }
   if (e.pre) {
     store16<F16>(e.pre + m * e.ldp + n, left, z);
@@ -230,16 +252,9 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int n, floa
   } else {
     activate_all(e.act, z, y);
   }
-  const int64_t at = m * e.ldo + n;
-  if (e.res) {
-    float r[W];
-    if (e.out_f32) load32((const float*)e.res + m * e.ldr + n, left, r);
-    else load16<F16>((const uint16_t*)e.res + m * e.ldr + n, left, r);
 #pragma unroll
-    for (int c = 0; c < W; ++c) y[c] += r[c];
-  }
-  if (e.out_f32) store32((float*)e.out + at, left, y);
-  else store16<F16>((uint16_t*)e.out + at, left, y);
+  for (int c = 0; c < W; ++c) y[c] += r[c];
+  store_out<F16>(e, m, n, y);
 }
 
 // --- tiled product ----------------------------------------------------------
@@ -515,8 +530,12 @@ void product_kernel(ProdArgs g) {
   constexpr int LPR = CW / 8, RPP = 64 / LPR;   // lanes a row (8 columns each), rows a pass
   const int er = lane / LPR, ec = (lane % LPR) * 8;
   const int n = ncol + ec;
-  // neither bias, activation, residual nor pre, 16-bit out: short enough to unroll
-  const bool plain = !PART && !GATED && !g.e.bias && !g.e.res && !g.e.pre && g.e.act == MOE_ACT_NONE && !g.e.out_f32;
+  // neither activation nor pre: short enough to unroll over the passes
+  const bool light = !GATED && !g.e.pre && g.e.act == MOE_ACT_NONE;
+  // gradients and most products: 16-bit sums alone, whole 8 columns
+  const bool plain = light && !g.e.bias && !g.e.res && !g.e.out_f32 && g.e.N % 8 == 0;
+  float bz[8], bu[8];
+  if constexpr (!PART) load_bias<F16, GATED>(g.e, n, bz, bu);
   auto rows32 = [&](auto jt) __attribute__((always_inline)) {
     constexpr int j = decltype(jt)::value;
 #pragma unroll
@@ -527,33 +546,64 @@ void product_kernel(ProdArgs g) {
             make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
     __builtin_amdgcn_wave_barrier();
     const int64_t mj = m0 + wave_m * C::WM + 32 * j;
-    auto row = [&](int r) __attribute__((always_inline)) {
-      const int64_t m = mj + r;
-      float z[8], u[8];
-      const float4 x0 = *(const float4*)(stage + r * PITCH + ec), x1 = *(const float4*)(stage + r * PITCH + ec + 4);
-      z[0] = x0.x; z[1] = x0.y; z[2] = x0.z; z[3] = x0.w; z[4] = x1.x; z[5] = x1.y; z[6] = x1.z; z[7] = x1.w;
-      if constexpr (GATED) {
-        const float4 y0 = *(const float4*)(stage + r * PITCH + CW + ec), y1 = *(const float4*)(stage + r * PITCH + CW + ec + 4);
-        u[0] = y0.x; u[1] = y0.y; u[2] = y0.z; u[3] = y0.w; u[4] = y1.x; u[5] = y1.y; u[6] = y1.z; u[7] = y1.w;
-      }
-      if (m < g.e.M && n < g.e.N) {
-        if constexpr (PART) {
-          float* p = g.part + (split * g.e.M + m) * g.pitch + n;
-          store32(p, g.up_col - n, z);
-          if constexpr (GATED) store32(p + g.up_col, g.up_col - n, u);
-        } else if (plain) {
-          store16<F16>((uint16_t*)g.e.out + m * g.e.ldo + n, g.e.N - n, z);
-        } else {
-          finish<F16, GATED>(g.e, m, n, z, u);
+    auto staged8 = [&](int r, int col, float (&v)[8]) __attribute__((always_inline)) {
+      const float4 a = *(const float4*)(stage + r * PITCH + col), b = *(const float4*)(stage + r * PITCH + col + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    };
+    // The residual is read ahead of the stores: the compiler may not move it
+    // there, as it may be the output itself (a lane stores what it has read).
+    constexpr int PASSES = 32 / RPP;
+    if constexpr (PART) {
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int r = p * RPP + er;
+        const int64_t m = mj + r;
+        float z[8], u[8];
+        staged8(r, ec, z);
+        if constexpr (GATED) staged8(r, CW + ec, u);
+        if (m < g.e.M && n < g.e.N) {
+          float* to = g.part + (split * g.e.M + m) * g.pitch + n;
+          store32(to, g.up_col - n, z);
+          if constexpr (GATED) store32(to + g.up_col, g.up_col - n, u);
         }
       }
-    };
-    if (PART || plain) {
+    } else if (plain) {
 #pragma unroll
-      for (int r = 0; r < 32; r += RPP) row(r + er);
+      for (int p = 0; p < PASSES; ++p) {
+        const int r = p * RPP + er;
+        const int64_t m = mj + r;
+        float z[8];
+        staged8(r, ec, z);
+        if (m < g.e.M && n < g.e.N) store16<F16, 8, true>((uint16_t*)g.e.out + m * g.e.ldo + n, 8, z);
+      }
+    } else if (light) {
+      float res[PASSES][8];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) load_residual<F16>(g.e, mj + p * RPP + er, n, res[p]);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int r = p * RPP + er;
+        const int64_t m = mj + r;
+        float z[8];
+        staged8(r, ec, z);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) z[c] += bz[c] + res[p][c];
+        if (m < g.e.M && n < g.e.N) store_out<F16>(g.e, m, n, z);
+      }
     } else {
+      float res[8];
+      load_residual<F16>(g.e, mj + er, n, res);
 #pragma unroll 1
-      for (int r = er; r < 32; r += RPP) row(r);
+      for (int r = er; r < 32; r += RPP) {
+        const int64_t m = mj + r;
+        float z[8], u[8], next[8];
+        load_residual<F16>(g.e, r + RPP < 32 ? m + RPP : g.e.M, n, next);
+        staged8(r, ec, z);
+        if constexpr (GATED) staged8(r, CW + ec, u);
+        if (m < g.e.M && n < g.e.N) finish<F16, GATED>(g.e, m, n, z, u, bz, bu, res);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) res[c] = next[c];
+      }
     }
     __builtin_amdgcn_wave_barrier();
   };
@@ -584,7 +634,10 @@ __global__ __launch_bounds__(256) void join_kernel(ProdArgs g) {
         u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
       }
     }
-    finish<F16, GATED>(g.e, m, n, z, u);
+    float bz[4], bu[4], r[4];
+    load_bias<F16, GATED>(g.e, n, bz, bu);
+    load_residual<F16>(g.e, m, n, r);
+    finish<F16, GATED>(g.e, m, n, z, u, bz, bu, r);
   }
 }
 
@@ -659,7 +712,12 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
       }
     }
     const int m = 16 * i + r, n = n0 + (lane >> 4) * 4;
-    if (m < M && n < g.e.N) finish<F16, GATED>(g.e, m, n, z, u);
+    if (m < M && n < g.e.N) {
+      float bz[4], bu[4], res[4];
+      load_bias<F16, GATED>(g.e, n, bz, bu);
+      load_residual<F16>(g.e, m, n, res);
+      finish<F16, GATED>(g.e, m, n, z, u, bz, bu, res);
+    }
   }
 }
 
@@ -781,15 +839,15 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
   // what their multiplications take at the rate the tile reaches, at least a
   // load's latency; a round of workgroups adds its fill and epilogue; a split
   // adds its partial sums' round trip and the second launch.  The constants are
-  // fitted to times of every choice over 60 products (both directions, 32 to
+  // fitted to times of every choice over 80 products (both directions, 32 to
   // 8192 rows): the choice costs 1.5% over the best one on average.  Both sides
   // of a typical decision: 8192 x 256 x 7168 takes 43 us as 128 x 128 tiles in 4
   // splits and 50 us as 256 x 256 in 8; 8192 x 2048 x 7168 takes 218 us and, as
   // 256 x 256 in one piece, 190 us.
   static const int bm[4] = {0, 64, 128, 256}, bn[4] = {0, 128, 128, 256}, per_cu[4] = {0, 3, 2, 1};
-  static const double rate[4] = {0, 3.5e6, 5.1e6, 6.2e6};       // flop per us and CU
-  static const double latency[4] = {0, 0.45, 0.75, 1.43};       // us a step
-  static const double round_us[4] = {0, 2.9, 4.0, 9.0};
+  static const double rate[4] = {0, 3.3e6, 4.85e6, 6.8e6};       // flop per us and CU
+  static const double latency[4] = {0, 0.45, 0.75, 1.47};       // us a step
+  static const double round_us[4] = {0, 2.55, 4.0, 7.7};
   const int64_t steps = (K + kBK - 1) / kBK;
   Cut best = {1, 1, round_up(K, kBK)};
   double best_us = 1e30;
@@ -804,7 +862,7 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
       const double work_us = conc * 2.0 * bm[t] * bn[t] * kBK / rate[t];
       const double step_us = work_us > latency[t] ? work_us : latency[t];
       double us = (double)((blocks + kCus * conc - 1) / (kCus * conc)) * (per * step_us + round_us[t]);
-      if (s > 1) us += 3.5 + (double)s * M * NZ * 8 / 6.8e6;
+      if (s > 1) us += 2.9 + (double)s * M * NZ * 8 / 5.05e6;
       if (us < best_us) {
         best_us = us;
         best = {t, s, per * kBK};
