@@ -340,7 +340,7 @@ typedef struct moe_route_opts {
  *   bias      device float [experts], or NULL: none.
  *   opts      NULL: softmax, no renorm, no groups, scale 1.
  *   topk_ids  device int32 [tokens, top_k];  topk_w  device float [tokens, top_k].
- * experts <= 1024, top_k <= 32 and at most the experts of topk_group groups.
+ * tokens <= 2^26, experts <= 1024, top_k <= 32 and at most the experts of topk_group groups.
  */
 int moe_route(int64_t tokens, int32_t experts, int32_t top_k, const void* logits, int32_t dtype, int64_t ld,
               const float* bias, const moe_route_opts* opts, int32_t* topk_ids, float* topk_w, void* stream);
@@ -353,7 +353,8 @@ int moe_route(int64_t tokens, int32_t experts, int32_t top_k, const void* logits
  *   logits, ld, topk_ids, topk_w, opts   as given to and returned by moe_route
  *             (only score, renorm and scale of opts are read).
  *   d_topk_w  device float [tokens, top_k], e.g. from moe_scale_backward.
- *   d_logits  device [tokens, experts] of dtype, rows ld_d elements apart (0 = experts); all written.
+ *   d_logits  device [tokens, experts] of dtype, rows ld_d elements apart (0 = experts); all written.  No overlap
+ *             with the inputs.
  */
 int moe_route_backward(int64_t tokens, int32_t experts, int32_t top_k, const void* logits, int32_t dtype,
                        int64_t ld, const int32_t* topk_ids, const float* topk_w, const float* d_topk_w,
@@ -394,7 +395,7 @@ int moe_linear_sizes(const moe_linear_desc* desc, size_t* forward_bytes, size_t*
  *   residual  device [rows, cols] of out_dtype or NULL; may be `out` itself with the same pitch.
  *   pre       device [rows, n] or NULL: receives x w^T + bias, which moe_linear_backward needs under an
  *             activation.
- *   out       device [rows, cols] of out_dtype.
+ *   out       device [rows, cols] of out_dtype; neither it nor pre overlaps the inputs otherwise.
  *   ws        device workspace, 256-byte aligned, forward_bytes of moe_linear_sizes (NULL if that is 0).  Its
  *             contents do not matter before or after; calls that overlap on the device need one each.
  */

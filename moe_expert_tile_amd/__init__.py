@@ -362,12 +362,13 @@ def _workspace(where, ws, need, x, stream):
         return ws
     if need == 0:
         return None
-    if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=x.device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=x.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device=x.device)
+    if stream is not None:
+        raw = _stream(stream)
+        if raw != _raw_stream(x.device.index):
+            own = torch.cuda.ExternalStream(raw, device=x.device) if raw else torch.cuda.default_stream(x.device)
+            with torch.cuda.stream(own):
+                return torch.empty(need, dtype=torch.uint8, device=x.device)
+    return torch.empty(need, dtype=torch.uint8, device=x.device)
 
 
 def moe_linear(x, w, out, bias=None, residual=None, pre=None, act: int = ACT_NONE, ws=None, stream=None) -> None:

@@ -297,3 +297,37 @@ def test_backward_without_x_or_w(act):
     assert m._lib.moe_linear_backward(ctypes.byref(d), p(a["x"]), None, p(a["pre"]), p(a["d_out"]), None, p(dw), None, p(ws), s) == 0
     torch.cuda.synchronize()
     assert torch.equal(dx, whole["dx"]) and torch.equal(dw, whole["dw"])
+
+
+def test_offsets_beyond_32_bits():
+    """2^21 rows of 1032 columns are 2.16e9 elements: the first and the last
+    rows' results are those of small calls on copies of them."""
+    m = _m()
+    M, K, N = 1 << 21, 1032, 8
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").fill_(0.25)
+    w = torch.randn(N, K, device="cuda").to(torch.bfloat16)
+    ends = (slice(0, 200), slice(M - 200, M))
+    for e in ends:
+        x[e] = torch.randn(200, K, device="cuda").to(torch.bfloat16)
+    out, g = torch.empty(M, N, device="cuda"), torch.zeros(M, N, device="cuda")
+    for e in ends:
+        g[e] = torch.randn(200, N, device="cuda")
+    say("[linear] 2^21 rows")
+    m.moe_linear(x, w, out)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    say("[linear back] 2^21 rows")
+    m.moe_linear_backward(x, w, g, dx=dx, dw=dw)
+    torch.cuda.synchronize()
+    S = 0
+    for e in ends:
+        xe = _np(x[e])
+        z = xe @ _np(w).T
+        assert np.all(np.abs(_np(out[e]) - z) <= (K + 2) * U * (np.abs(xe) @ np.abs(_np(w)).T))
+        small = torch.empty(200, K, dtype=torch.bfloat16, device="cuda")
+        m.moe_linear_backward(x[e].contiguous(), w, g[e].contiguous(), dx=small)
+        assert torch.equal(small, dx[e])
+        S = S + _np(g[e]).T @ xe
+    assert not dx[1000:1100].any()
+    mag = sum(np.abs(_np(g[e])).T @ np.abs(_np(x[e])) for e in ends)
+    half = _half(torch.bfloat16)
+    assert np.all(np.abs(_np(dw) - S) <= half * 1.01 * (mag + np.abs(S)) + 2.0 ** -20)

@@ -263,3 +263,22 @@ def test_gradient_of_a_nan_row_stays_in_it():
     d = torch.empty_like(z)
     m.moe_route_backward(z, ids, w, g, d)
     assert torch.isnan(d).any(1).tolist() == [i == 2 for i in range(8)]
+
+
+def test_offsets_beyond_32_bits():
+    """2^23 + 5 tokens over 264 experts are 2.2e9 logits: the last tokens as in a small call."""
+    m = _m()
+    T, E, k = (1 << 23) + 5, 264, 4
+    z = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    z[-300:] = torch.randn(300, E, device="cuda").to(torch.bfloat16)
+    say("[route] 2^23 tokens")
+    ids, w = _call(z, k, kind="softmax")
+    few, fw = _call(z[-300:].contiguous(), k, kind="softmax")
+    assert torch.equal(ids[-300:], few) and torch.equal(w[-300:], fw)
+    assert ids[12345].tolist() == [0, 1, 2, 3]
+    g = torch.randn(T, k, device="cuda")
+    d, ds = torch.empty_like(z), torch.empty(300, E, dtype=torch.bfloat16, device="cuda")
+    m.moe_route_backward(z, ids, w, g, d)
+    m.moe_route_backward(z[-300:].contiguous(), few, fw, g[-300:].contiguous(), ds)
+    torch.cuda.synchronize()
+    assert torch.equal(d[-300:], ds)

@@ -23,7 +23,7 @@ def _route(m, tokens=4, experts=16, top_k=2, logits=GOOD, dtype=0, ld=0, bias=No
 
 
 @pytest.mark.parametrize("bad", [
-    dict(tokens=-1), dict(tokens=(1 << 30) + 1), dict(experts=0), dict(experts=1025), dict(top_k=0), dict(top_k=17),
+    dict(tokens=-1), dict(tokens=(1 << 26) + 1), dict(experts=0), dict(experts=1025), dict(top_k=0), dict(top_k=17),
     dict(experts=64, top_k=33), dict(dtype=3), dict(dtype=-1), dict(ld=15), dict(ld=-16), dict(ld=(1 << 21) + 1),
     dict(logits=0), dict(logits=GOOD + 1), dict(dtype=2, logits=GOOD + 2), dict(ids=0), dict(ids=GOOD + 2), dict(w=0),
     dict(w=GOOD + 1), dict(bias=GOOD + 2),
