@@ -331,3 +331,55 @@ def test_offsets_beyond_32_bits():
     mag = sum(np.abs(_np(g[e])).T @ np.abs(_np(x[e])) for e in ends)
     half = _half(torch.bfloat16)
     assert np.all(np.abs(_np(dw) - S) <= half * 1.01 * (mag + np.abs(S)) + 2.0 ** -20)
+
+
+# Ragged sizes whose work asks for each tile (64, 128 and 256 rows), whole and
+# split along the sum, in each direction; the reference is float64 on the GPU.
+EACH_TILE = [
+    ("fwd", 101, 11, 1752), ("fwd", 648, 8838, 144), ("fwd", 3417, 9, 5112), ("fwd", 1665, 7185, 144),
+    ("fwd", 8880, 132, 7376), ("gated", 86, 6, 496), ("gated", 101, 6, 1752), ("gated", 648, 4420, 144),
+    ("gated", 3417, 5, 5112), ("gated", 1665, 3593, 144), ("gated", 8880, 67, 7376),
+    ("dx", 535, 182, 8), ("dx", 104, 1502, 8), ("dx", 4551, 149, 1304), ("dx", 3111, 5106, 8), ("dx", 1707, 142, 7216),
+    ("dx", 8623, 7572, 136), ("dw", 467, 44, 16), ("dw", 1618, 12, 8), ("dw", 143, 6333, 912), ("dw", 2350, 6271, 8),
+    ("dw", 141, 2961, 4280), ("dw", 7852, 8460, 136),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("what,M,N,K", EACH_TILE)
+def test_every_tile_whole_and_split(what, M, N, K, dtype):
+    m = _m()
+    say(f"[linear tiles] {what} {M}x{N}x{K} {dtype}")
+    a = _inputs(M, N, K, "swiglu" if what == "gated" else "none", dtype, M + K)
+    x, w, half, tiny = a["x"].double(), a["w"].double(), _half(DT[dtype]), _tiny(DT[dtype])
+    if what in ("fwd", "gated"):
+        b, r = a["bias"].double(), a["residual"].double()
+        m.moe_linear(a["x"], a["w"], a["out"], bias=a["bias"], residual=a["residual"], pre=a["pre"],
+                     act=_act("swiglu" if what == "gated" else "none"))
+        z = torch.mm(x, w.t().contiguous()) + b
+        ez = (K + 2) * U * (torch.mm(x.abs(), w.abs().t().contiguous()) + b.abs())
+        if what == "gated":
+            g, u = z[:, :N], z[:, N:]
+            p = torch.sigmoid(g)
+            sg = (g * p).abs()
+            y = g * p * u
+            ey = (1.13 * ez[:, :N] * u.abs() + sg * ez[:, N:] + 1.13 * ez[:, :N] * ez[:, N:] +
+                  (16 * U + 64 * U * g.abs()) * sg * u.abs())
+        else:
+            y, ey = z, ez
+        y = y + r
+        bound = (ey + U * (y.abs() + r.abs())) * (1 + half) + half * y.abs() + tiny
+        assert bool(((a["out"].double() - y).abs() <= bound).all())
+        assert bool(((a["pre"].double() - z).abs() <= ez * (1 + half) + half * z.abs() + tiny).all())
+        return
+    g = a["d_out"].double()
+    if what == "dx":
+        got = torch.empty_like(a["x"])
+        m.moe_linear_backward(a["x"], a["w"], a["d_out"], dx=got)
+        ref, mag, terms = torch.mm(g, w), torch.mm(g.abs(), w.abs()), N
+    else:
+        got = torch.empty_like(a["w"])
+        m.moe_linear_backward(a["x"], a["w"], a["d_out"], dw=got)
+        ref, mag, terms = torch.mm(g.t().contiguous(), x), torch.mm(g.t().contiguous().abs(), x.abs()), M
+    bound = (terms + 64) * U * mag * (1 + half) + half * ref.abs() + tiny
+    assert bool(((got.double() - ref).abs() <= bound).all())
