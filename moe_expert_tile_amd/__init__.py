@@ -12,6 +12,7 @@ been built; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, List, Optional, Sequence
 
@@ -247,64 +248,77 @@ def _invalid(where: str, what: str):
     return err
 
 
-def _matrix(where, name, t, shape, dtype, device) -> int:
+def _mismatch(where, name, t, shape, dtype, index, kind):
+    on = "the CPU" if index < 0 else f"GPU {index}"
+    return _invalid(where, f"{name} is a {t.dtype} tensor {tuple(t.shape)} with strides {t.stride()} on {t.device}, "
+                           f"not a {kind} {dtype} one {tuple(shape)} on {on}")
+
+
+def _matrix(where, name, t, shape, dtype, index) -> int:
     """Checks a matrix of that shape with unit column stride (None passes);
     returns its row pitch, 0 (packed) where no second row shows it."""
     if t is None:
         return 0
-    if t.shape != shape:
-        raise _invalid(where, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
-    if t.dtype is not dtype:
-        raise _invalid(where, f"{name} is {t.dtype}, not {dtype}")
-    if t.device != device:
-        raise _invalid(where, f"{name} is on {t.device}, not {device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise _mismatch(where, name, t, shape, dtype, index, "row-major")
     rows, cols = shape
     pitch, step = t.stride()
-    if step != 1 and cols > 1 and rows > 0:
-        raise _invalid(where, f"{name}'s columns are not contiguous (strides {t.stride()})")
-    if rows < 2:
-        return 0
-    if pitch < cols:
-        raise _invalid(where, f"{name}'s rows overlap (strides {t.stride()})")
-    return pitch
+    if step != 1 and cols > 1 and rows > 0 or pitch < cols and rows > 1:
+        raise _mismatch(where, name, t, shape, dtype, index, "row-major")
+    return pitch if rows > 1 else 0
 
 
-def _packed(where, name, t, shape, dtype, device) -> Optional[int]:
+def _packed(where, name, t, shape, dtype, index) -> Optional[int]:
     """Checks a contiguous tensor (None passes); returns its address."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise _invalid(where, f"{name} is not a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise _mismatch(where, name, t, shape, dtype, index, "contiguous")
     return t.data_ptr()
 
 
-def _launch(where, device, stream, fn, *args) -> None:
-    """fn(*args, raw stream) with `device` current; raises its errors."""
-    index = device.index
-    if device.type != "cuda":
-        raise _invalid(where, f"the tensors are on {device}, not on a GPU")
-    if torch.cuda.current_device() == index:
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launch(where, index, stream, fn, *args) -> None:
+    """fn(*args, raw stream) with GPU `index` current; raises its errors."""
+    if index < 0:
+        raise _invalid(where, "the tensors are not on a GPU")
+    if _current_device() == index:
         rc = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, _stream(stream))
     if rc != MOE_OK:
         raise MoEError(rc, where)
 
 
+# the library only reads options, so calls with the same ones share them
+@functools.lru_cache(maxsize=256)
+def _route_opts(score, renorm, n_group, topk_group, group_score, scale):
+    return moe_route_opts(score, 1 if renorm else 0, n_group, topk_group, group_score, scale)
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_bytes(M, N, K, dtype, out_dtype, act):
+    return tuple(moe_linear_sizes(moe_linear_desc(M, N, K, dtype, out_dtype, act)).values())
+
+
 def _route_tensors(where, logits, topk_ids, topk_w):
     """(sizes, type, row pitch) of the logits, and the addresses of the others."""
-    if logits.dim() != 2 or logits.dtype not in _DTYPES:
-        raise _invalid(where, "logits is a [tokens, experts] tensor of bfloat16, float16 or float32")
-    if topk_ids.dim() != 2:
-        raise _invalid(where, "topk_ids is a [tokens, top_k] tensor")
-    dtype, device = logits.dtype, logits.device
+    code = _DTYPES.get(logits.dtype)
+    if code is None or logits.dim() != 2 or topk_ids.dim() != 2:
+        raise _invalid(where, "logits is a [tokens, experts] tensor of bfloat16, float16 or float32, topk_ids a "
+                              "[tokens, top_k] one")
+    index = logits.get_device()
     T, E = shape = logits.shape
-    k = topk_ids.shape[1]
-    ld = _matrix(where, "logits", logits, shape, dtype, device)
-    return (T, E, k, logits.data_ptr(), _DTYPES[dtype], ld), (
-        _packed(where, "topk_ids", topk_ids, (T, k), torch.int32, device),
-        _packed(where, "topk_w", topk_w, (T, k), torch.float32, device))
+    picks = topk_ids.shape
+    if picks[0] != T:
+        raise _invalid(where, f"topk_ids has {picks[0]} rows, logits {T}")
+    ld = _matrix(where, "logits", logits, shape, logits.dtype, index)
+    return (T, E, picks[1], logits.data_ptr(), code, ld), (
+        _packed(where, "topk_ids", topk_ids, picks, torch.int32, index),
+        _packed(where, "topk_w", topk_w, picks, torch.float32, index)), index
 
 
 def moe_route(logits, topk_ids, topk_w, bias=None, score: int = SCORE_SOFTMAX, renorm: bool = False,
@@ -312,11 +326,11 @@ def moe_route(logits, topk_ids, topk_w, bias=None, score: int = SCORE_SOFTMAX, r
               stream=None) -> None:
     """Router logits [T, E] -> topk_ids int32 [T, k] (what moe_plan reads) and
     topk_w float32 [T, k] (what moe_scale reads); see include/moe.h."""
-    sizes, outs = _route_tensors("moe_route", logits, topk_ids, topk_w)
-    device = logits.device
-    b = _packed("moe_route", "bias", bias, (sizes[1],), torch.float32, device)
-    opts = moe_route_opts(score, 1 if renorm else 0, n_group, topk_group, group_score, scale)
-    _launch("moe_route", device, stream, _lib.moe_route, *sizes, b, opts, *outs)
+    sizes, outs, index = _route_tensors("moe_route", logits, topk_ids, topk_w)
+    if bias is not None:
+        bias = _packed("moe_route", "bias", bias, (sizes[1],), torch.float32, index)
+    _launch("moe_route", index, stream, _lib.moe_route, *sizes, bias,
+            _route_opts(score, renorm, n_group, topk_group, group_score, scale), *outs)
 
 
 def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, score: int = SCORE_SOFTMAX,
@@ -324,26 +338,28 @@ def moe_route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, score: int 
     """d_logits [T, E] (the logits' type) from d_topk_w float32 [T, k]; logits,
     topk_ids, topk_w, score, renorm and scale as in the moe_route call."""
     where = "moe_route_backward"
-    sizes, ins = _route_tensors(where, logits, topk_ids, topk_w)
-    device = logits.device
-    g = _packed(where, "d_topk_w", d_topk_w, (sizes[0], sizes[2]), torch.float32, device)
-    ld_d = _matrix(where, "d_logits", d_logits, logits.shape, logits.dtype, device)
-    opts = moe_route_opts(score, 1 if renorm else 0, 1, 1, GROUP_MAX, scale)
-    _launch(where, device, stream, _lib.moe_route_backward, *sizes, *ins, g, opts, d_logits.data_ptr(), ld_d)
+    sizes, ins, index = _route_tensors(where, logits, topk_ids, topk_w)
+    g = _packed(where, "d_topk_w", d_topk_w, topk_ids.shape, torch.float32, index)
+    ld_d = _matrix(where, "d_logits", d_logits, logits.shape, logits.dtype, index)
+    _launch(where, index, stream, _lib.moe_route_backward, *sizes, *ins, g,
+            _route_opts(score, renorm, 1, 1, GROUP_MAX, scale), d_logits.data_ptr(), ld_d)
 
 
 def _linear_desc(where, x, w, out, act, out_name):
+    """The product's sizes with the pitches of x, w and out, its rows n, and
+    the GPU."""
+    dtype, out_dtype, index = x.dtype, out.dtype, x.get_device()
     if x.dim() != 2 or w.dim() != 2 or out.dim() != 2:
         raise _invalid(where, f"x, w and {out_name} are matrices")
-    dtype, out_dtype, device = x.dtype, out.dtype, x.device
-    if dtype not in _DTYPES or dtype is torch.float32 or (out_dtype is not dtype and out_dtype is not torch.float32):
+    if dtype is not torch.bfloat16 and dtype is not torch.float16 or (
+            out_dtype is not dtype and out_dtype is not torch.float32):
         raise _invalid(where, f"x is {dtype} and {out_name} {out_dtype}: bfloat16 or float16, and the same or float32")
     M, K = xs = x.shape
     N = out.shape[1]
     n = 2 * N if act == ACT_SWIGLU else N
-    return moe_linear_desc(M, N, K, _DTYPES[dtype], _DTYPES[out_dtype], act, 0, _matrix(where, "x", x, xs, dtype, device),
-                           _matrix(where, "w", w, (n, K), dtype, device), 0, 0,
-                           _matrix(where, out_name, out, (M, N), out_dtype, device), 0, 0), n
+    return moe_linear_desc(M, N, K, _DTYPES[dtype], _DTYPES[out_dtype], act, 0, _matrix(where, "x", x, xs, dtype, index),
+                           _matrix(where, "w", w, (n, K), dtype, index), 0, 0,
+                           _matrix(where, out_name, out, (M, N), out_dtype, index), 0, 0), n, index
 
 
 def moe_linear_sizes(desc: moe_linear_desc) -> Dict[str, int]:
@@ -377,21 +393,20 @@ def moe_linear(x, w, out, bias=None, residual=None, pre=None, act: int = ACT_NON
     receives x w^T + bias.  ws: at least moe_linear_sizes' forward_bytes, or
     None to take it from torch's allocator; see include/moe.h."""
     where = "moe_linear"
-    d, n = _linear_desc(where, x, w, out, act, "out")
-    device = x.device
+    d, n, index = _linear_desc(where, x, w, out, act, "out")
     if residual is not None:
-        d.ld_residual = _matrix(where, "residual", residual, out.shape, out.dtype, device)
+        d.ld_residual = _matrix(where, "residual", residual, out.shape, out.dtype, index)
+        residual = residual.data_ptr()
     if pre is not None:
-        d.ld_pre = _matrix(where, "pre", pre, (x.shape[0], n), x.dtype, device)
-    b = _packed(where, "bias", bias, (n,), x.dtype, device)
-    need = ctypes.c_size_t()
-    rc = _lib.moe_linear_sizes(d, need, None)
-    if rc != MOE_OK:
-        raise MoEError(rc, where)
-    if ws is not None or need.value:
-        ws = _workspace(where, ws, need.value, x, stream)
-    _launch(where, device, stream, _lib.moe_linear, d, x.data_ptr(), w.data_ptr(), b, _ptr(residual), _ptr(pre),
-            out.data_ptr(), _ptr(ws))
+        d.ld_pre = _matrix(where, "pre", pre, (x.shape[0], n), x.dtype, index)
+        pre = pre.data_ptr()
+    if bias is not None:
+        bias = _packed(where, "bias", bias, (n,), x.dtype, index)
+    need = _linear_bytes(d.rows, d.cols, d.depth, d.dtype, d.out_dtype, d.act)[0]
+    if ws is not None or need:
+        ws = _workspace(where, ws, need, x, stream)
+    _launch(where, index, stream, _lib.moe_linear, d, x.data_ptr(), w.data_ptr(), bias, residual, pre, out.data_ptr(),
+            None if ws is None else ws.data_ptr())
 
 
 def moe_linear_backward(x, w, d_out, dx=None, dw=None, dbias=None, pre=None, act: int = ACT_NONE, ws=None,
@@ -400,18 +415,15 @@ def moe_linear_backward(x, w, d_out, dx=None, dw=None, dbias=None, pre=None, act
     w, dbias [n], all of x's type) from d_out [M, N] and, under an activation,
     the forward call's pre; see include/moe.h."""
     where = "moe_linear_backward"
-    d, n = _linear_desc(where, x, w, d_out, act, "d_out")
-    dtype, device = x.dtype, x.device
-    d.ld_pre = _matrix(where, "pre", pre, (x.shape[0], n), dtype, device)
-    d.ld_dx = _matrix(where, "dx", dx, x.shape, dtype, device)
-    d.ld_dw = _matrix(where, "dw", dw, w.shape, dtype, device)
-    db = _packed(where, "dbias", dbias, (n,), dtype, device)
-    need = ctypes.c_size_t()
-    rc = _lib.moe_linear_sizes(d, None, need)
-    if rc != MOE_OK:
-        raise MoEError(rc, where)
-    ws = _workspace(where, ws, need.value, x, stream)
-    _launch(where, device, stream, _lib.moe_linear_backward, d, x.data_ptr(), w.data_ptr(), _ptr(pre),
+    d, n, index = _linear_desc(where, x, w, d_out, act, "d_out")
+    dtype = x.dtype
+    d.ld_pre = _matrix(where, "pre", pre, (x.shape[0], n), dtype, index)
+    d.ld_dx = _matrix(where, "dx", dx, x.shape, dtype, index)
+    d.ld_dw = _matrix(where, "dw", dw, w.shape, dtype, index)
+    db = _packed(where, "dbias", dbias, (n,), dtype, index)
+    need = _linear_bytes(d.rows, d.cols, d.depth, d.dtype, d.out_dtype, d.act)[1]
+    ws = _workspace(where, ws, need, x, stream)
+    _launch(where, index, stream, _lib.moe_linear_backward, d, x.data_ptr(), w.data_ptr(), _ptr(pre),
             d_out.data_ptr(), _ptr(dx), _ptr(dw), db, _ptr(ws))
 
 
