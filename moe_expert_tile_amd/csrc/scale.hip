@@ -120,17 +120,17 @@ __global__ __launch_bounds__(256) void scale_kernel(PlanLayout L, const int32_t*
 // are neighbouring wavefronts, so its gradient comes from the caches after the
 // first of them.
 template <bool DRECV, bool DW>
-__global__ __launch_bounds__(256) void scale_back_kernel(PlanLayout L, const int32_t* __restrict__ ws,
+__global__ __launch_bounds__(256) void scale_back_kernel(const int32_t* __restrict__ hdr,
+                                                         const int32_t* __restrict__ pos, int T_r, int k, int vec,
                                                          const uint4* __restrict__ recv,
                                                          const float* __restrict__ w,
                                                          const uint4* __restrict__ dout, uint4* __restrict__ drecv,
                                                          float* __restrict__ dw) {
-  if (ws[L.o_hdr + H_ERROR] != 0) return;
-  const int32_t* pos = ws + L.o_pos;
-  const int k = L.k, vec = L.d / 8, lane = threadIdx.x & 63;
+  if (hdr[H_ERROR] != 0) return;
+  const int lane = threadIdx.x & 63;
   const int wpb = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int64_t total = (int64_t)L.T_r * k;
+  const int64_t total = (int64_t)T_r * k;
   for (int64_t wv = (int64_t)blockIdx.x * wpb + wave; wv < total; wv += (int64_t)gridDim.x * wpb) {
     const int64_t t = wv / k;
     const float wt = w[wv];
@@ -179,9 +179,13 @@ hipError_t launch_scale_backward(const PlanLayout& L, const int32_t* ws, const u
   const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536)), block(256);
   const uint4 *r = (const uint4*)recv_self, *g = (const uint4*)d_out;
   uint4* dr = (uint4*)d_recv;
-  if (d_recv && d_topk_w) hipLaunchKernelGGL((scale_back_kernel<true, true>), grid, block, 0, s, L, ws, r, topk_w, g, dr, d_topk_w);
-  else if (d_recv) hipLaunchKernelGGL((scale_back_kernel<true, false>), grid, block, 0, s, L, ws, r, topk_w, g, dr, d_topk_w);
-  else hipLaunchKernelGGL((scale_back_kernel<false, true>), grid, block, 0, s, L, ws, r, topk_w, g, dr, d_topk_w);
+  const int32_t *hdr = ws + L.o_hdr, *pos = ws + L.o_pos;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, hdr, pos, L.T_r, L.k, L.d / 8, r, topk_w, g, dr, d_topk_w);
+  };
+  if (d_recv && d_topk_w) go(scale_back_kernel<true, true>);
+  else if (d_recv) go(scale_back_kernel<true, false>);
+  else go(scale_back_kernel<false, true>);
   return hipGetLastError();
 }
 
