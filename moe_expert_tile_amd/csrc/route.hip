@@ -10,9 +10,9 @@
 // expert ascending): the float's bits, remapped so that they order as an
 // integer, above 10 bits of the expert's index, all in the fraction of a
 // double in [1, 2), so that one v_max_f64 compares two keys.  Each lane sorts
-// its keys with
-// a fixed network of v_max_f64 / v_min_f64; then every pick is the largest
-// head over the row's lanes, and the lane that held it moves its list up.
+// its keys with a fixed network of v_max_f64 / v_min_f64; then every pick is
+// the largest head over the row's lanes, and the lane that held it moves its
+// list up.
 //
 // Which values are ranked.  Without a bias the scores are an increasing
 // function of the logits, so the logits themselves are ranked, exactly.  With
@@ -20,6 +20,13 @@
 // 32 bits; where two values that decide something lie closer than the error of
 // that, the row is ranked again in 64 bits (exact_row), one row at a time by
 // the whole wavefront.
+//
+// What bounds it: instructions.  32768 tokens x 256 experts (grouped sigmoid with
+// bias, fp32) take 28 us against 7 us for their bytes: about 1500 vector
+// instructions a wavefront of 4 tokens, a quarter of them the picks, a fifth
+// keys and sorting; the bound loads, keys and one-pass shape took it there from
+// 96 us.  A late row ranked in 64 bits adds about 4 us.  64 tokens take 3.6 us,
+// a launch and the picks' latency.
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -585,7 +592,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 // (a sigmoid's slope is s (1 - s), and 1 - s_j = 1 / (1 + e^z_j)).  So only
 // the full softmax reads whole rows of logits; the others read k of them.
 // A wavefront builds its rows in LDS (zeros, then the k values, summed in slot
-// order where an expert is listed twice) and writes them out whole.
+// order where an expert is listed twice) and writes them out whole.  Bound by
+// those writes: 32768 x 256 fp32, 37 MB with the slots, take 9-11 us, 3.5-4
+// TB/s; 256 x 8 with the full softmax take 3.7 us, a launch.
 struct RouteBackArgs {
   const void* logits;
   const int32_t* ids;
@@ -780,12 +789,16 @@ hipError_t launch_route(int64_t T, int E, int k, const void* logits, int dtype, 
   const bool byc = bias != nullptr || a.top2;
   int gp = 1;
   while (gp < a.groups) gp *= 2;
-  // the fewest lanes that hold a row with at most 16 values each (a row over
-  // more lanes sorts less but shares a pick's exchanges among fewer rows)
+  // Lanes a row.  Fewer hold more values each: more sorting, but a pick's
+  // exchanges serve more rows.  At most 16 values a lane, and at least 8 lanes
+  // past 16 experts.  Over 65 to 128 experts 16 lanes are quicker for a short
+  // batch and 8 for a long one (128 experts, with bias: 64 tokens 4.8 and 6.4
+  // us, 32768 tokens 16.0 and 14.5 us); 32 lanes are slower for both (5.6 and
+  // 35 us), and for 256 experts (5.7 and 36.5 us against 5.6 and 21.7 us with 16).
   auto places = [&](int lpr) { return (a.gsize + 4 * (lpr / gp) - 1) / (4 * (lpr / gp)) * 4; };
   int lpr = gp < 4 ? 4 : gp;
   if (E > 16 && lpr < 8) lpr = 8;
-  if (E > 64 && lpr < 16) lpr = 16;
+  if (E > 64 && lpr < 16 && T < 16384) lpr = 16;
   while (lpr < 64 && places(lpr) > (lpr == 4 ? 4 : 16)) lpr *= 2;
   const int vpl = places(lpr);
   a.lpg = lpr / gp;

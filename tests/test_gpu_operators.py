@@ -74,6 +74,12 @@ def test_scale_backward(tokens, rank, E, k, d):
     sh.scale_backward(w, g, a, None)
     sh.scale_backward(w, g, None, b)
     assert torch.equal(a, d_recv) and torch.equal(b, d_w)
+    # what a gradient does not need may be missing
+    m = _m()
+    b.fill_(9.0)
+    m.moe_scale_backward(sh.shape, sh.plan_ws, sh.recv[rank], None, g, None, b)
+    m.moe_scale_backward(sh.shape, sh.plan_ws, None, w, g, a.fill_(9.0), None)
+    assert torch.equal(a, d_recv) and torch.equal(b, d_w)
 
 
 def test_scale_backward_after_a_routing_error_does_nothing():

@@ -282,3 +282,19 @@ def test_offsets_beyond_32_bits():
     m.moe_route_backward(z[-300:].contiguous(), few, fw, g[-300:].contiguous(), ds)
     torch.cuda.synchronize()
     assert torch.equal(d[-300:], ds)
+
+
+def test_long_batches_of_middle_sizes():
+    """65 to 128 experts and 16384 tokens on take other lanes than short batches:
+    the same result, row by row, as in short calls (compared with the oracle above)."""
+    for E, k, G in ((100, 8, 1), (128, 8, 4), (72, 12, 8), (127, 6, 1)):
+        z = torch.randn(16400, E, device="cuda")
+        bias = torch.randn(E, device="cuda") * 0.1
+        for b in (None, bias):
+            kw = dict(kind="sigmoid", bias=b, renorm=True, n_group=G, topk_group=max(1, G // 2), top2=G > 1)
+            ids, w = _call(z, k, **kw)
+            for t in (0, 5000, 16000):
+                few, fw = _call(z[t:t + 400].contiguous(), k, **kw)
+                assert torch.equal(ids[t:t + 400], few)
+                assert bool(((w[t:t + 400] - fw).abs() <= 2.0 ** -18 * fw).all())
+            _check(z[:40].contiguous(), k, **kw)
