@@ -13,7 +13,9 @@
  *     before any HIP call; nothing is enqueued when validation fails.
  *   - Device pointers are plain device addresses (hipMalloc or a torch
  *     tensor's data_ptr()).  bf16 tensors are passed as uint16_t bit patterns
- *     and must be 16-byte aligned; int32/uint32/float tensors 4-byte aligned.
+ *     and must be 16-byte aligned; int32/uint32/float tensors 4-byte aligned
+ *     (moe_route, moe_linear and their gradients: to their elements, where
+ *     nothing else is said).
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *     Every call is asynchronous on it; nothing synchronises with the host
  *     except moe_device_status.
