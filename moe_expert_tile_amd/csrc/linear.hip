@@ -658,16 +658,18 @@ __global__ __launch_bounds__(256) void join_kernel(ProdArgs g) {
 
 // --- few rows ---------------------------------------------------------------
 //
-// Bound by reading the weights: one row through 7168 x 2048 (29 MB) takes 8.8
+// Bound by reading the weights: one row through 7168 x 2048 (29 MB) takes 7.6
 // us, of which about 2.5 us any launch takes; 8 K steps' loads in flight a
-// wavefront instead of 4 took it from 10.5 to 8.8 us.
-// A workgroup owns 16 output columns; its wavefronts take K in steps of 32 in
-// turn.  Operand lane layout of v_mfma_f32_16x16x32: row (or column) lane % 16,
+// wavefront instead of 4, all issued before the first is waited for, took it
+// there from 9.6 us.
+// A workgroup owns 16 output columns (PART: of one split of K); its wavefronts
+// take K in steps of 32 in turn.  Operand lane layout of v_mfma_f32_16x16x32: row (or column) lane % 16,
 // k = 8 (lane / 16) .. + 7, so a lane's operand is one 16-byte load; result
 // lane: column (token) lane % 16, rows (weight rows) 4 (lane / 16) .. + 3.
 constexpr int kFewWaves = 8;
 
-template <int TT, bool F16, bool GATED>
+// U K steps have their loads in flight together.
+template <int TT, bool F16, bool GATED, bool PART, int U>
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
   typedef typename Elem<F16>::v8 v8;
   constexpr int NB = GATED ? 2 : 1;
@@ -675,13 +677,15 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n0 = blockIdx.x * 16;
   const int r = lane & 15, kc = (lane >> 4) * 8;
-  const int M = (int)g.e.M, K = (int)g.K;
+  const int M = (int)g.e.M;
+  const int64_t kb = PART ? blockIdx.y * g.kper : 0;
+  const int K = (int)(PART ? min(g.K - kb, g.kper) : g.K);   // of this split
   const int brows = min(16, g.e.N - n0);
   const int64_t b_bytes = ((int64_t)(brows - 1) * g.ldb + K) * 2;
   __amdgpu_buffer_rsrc_t b_rsrc[NB];
-  b_rsrc[0] = make_rsrc(g.b + (int64_t)n0 * g.ldb, b_bytes);
-  if constexpr (GATED) b_rsrc[1] = make_rsrc(g.b + ((int64_t)g.e.N + n0) * g.ldb, b_bytes);
-  const __amdgpu_buffer_rsrc_t a_rsrc = make_rsrc(g.a, ((int64_t)(M - 1) * g.lda + K) * 2);
+  b_rsrc[0] = make_rsrc(g.b + (int64_t)n0 * g.ldb + kb, b_bytes);
+  if constexpr (GATED) b_rsrc[1] = make_rsrc(g.b + ((int64_t)g.e.N + n0) * g.ldb + kb, b_bytes);
+  const __amdgpu_buffer_rsrc_t a_rsrc = make_rsrc(g.a + kb, ((int64_t)(M - 1) * g.lda + K) * 2);
   const uint32_t b_off = r < brows ? 2u * ((uint32_t)r * (uint32_t)g.ldb + kc) : kPastEnd;
   uint32_t a_off[TT];
 #pragma unroll
@@ -691,7 +695,6 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < TT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int U = 8 / TT;   // K steps with their loads in flight together
   for (int k0 = wave * 32; k0 < K; k0 += kFewWaves * 32 * U) {
     v4u32 wv[U][NB], xv[U][TT];
 #pragma unroll
@@ -705,6 +708,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
       for (int i = 0; i < TT; ++i)
         xv[s][i] = __builtin_amdgcn_raw_buffer_load_b128(a_rsrc, (int)(on && a_off[i] != kPastEnd ? a_off[i] + 2u * k : kPastEnd), 0, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);   // all of them, before the first is waited for
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
@@ -730,7 +734,12 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
       }
     }
     const int m = 16 * i + r, n = n0 + (lane >> 4) * 4;
-    if (m < M && n < g.e.N) {
+    if (m >= M || n >= g.e.N) continue;
+    if constexpr (PART) {
+      float* to = g.part + ((int64_t)blockIdx.y * M + m) * g.pitch + n;
+      store32(to, 4, z);
+      if constexpr (GATED) store32(to + g.up_col, 4, u);
+    } else {
       float bz[4], bu[4], res[4];
       load_bias<F16, GATED>(g.e, n, bz, bu);
       load_residual<F16>(g.e, m, n, res);
@@ -853,7 +862,19 @@ struct Cut {
 Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
   const int64_t NZ = gated ? 2 * N : N;
   // few rows: 64 x 4096 x 4096 takes 22 us that way and 15 us in tiles, 32 rows 13 us either way
-  if (M <= 32 && !across) return {0, 1, round_up(K, kBK)};
+  if (M <= 32 && !across) {
+    // A CU takes about 30 KB/us from the caches (64 lines in flight), so a few
+    // workgroups with long sums are split along K, where that saves more than
+    // the join's launch: 20 rows through 256 x 7168 17.0 us whole and 8.1 us in 8
+    // splits, one row 10.0 and 7.0 us; one row through 1024 x 4096, below that,
+    // 6.8 us whole.
+    const int64_t blocks = (N + 15) / 16, bytes = (16 * (gated ? 2 : 1) + M) * K * 2;
+    int64_t s = 1;
+    while (s < 8 && 2 * s * blocks <= kCus && K / (2 * s) >= 256) s *= 2;
+    if ((double)bytes / 30e3 * (1.0 - 1.0 / s) < 4.5) s = 1;
+    const int64_t kper = round_up((K + s - 1) / s, kBK);
+    return {0, K > 0 ? (int)((K + kper - 1) / kper) : 1, kper};
+  }
   // Time of each choice, the smallest wins.  A K step of a CU's workgroups takes
   // what their multiplications take at the rate the tile reaches, at least a
   // load's latency; a round of workgroups adds its fill and epilogue; a split
@@ -916,6 +937,12 @@ void launch_dz(const DzArgs& a, hipStream_t s) {
   }
 }
 
+template <bool F16, bool GATED>
+void launch_join(const ProdArgs& g, hipStream_t s) {
+  const int64_t blocks = (g.e.M * ((g.e.N + 3) / 4) + 255) / 256;
+  hipLaunchKernelGGL((join_kernel<F16, GATED>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, g);
+}
+
 template <class C, bool F16, bool GATED, bool AX, bool BX>
 void launch_tiles(ProdArgs& g, hipStream_t s) {
   constexpr int HB = GATED ? C::BN / 2 : C::BN;
@@ -927,8 +954,7 @@ void launch_tiles(ProdArgs& g, hipStream_t s) {
     return;
   }
   hipLaunchKernelGGL((product_kernel<C, F16, GATED, true, AX, BX>), dim3(grid), dim3(C::NT), 0, s, g);
-  const int64_t blocks = (g.e.M * ((g.e.N + 3) / 4) + 255) / 256;
-  hipLaunchKernelGGL((join_kernel<F16, GATED>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, g);
+  launch_join<F16, GATED>(g, s);
 }
 
 template <bool F16, bool GATED, bool AX, bool BX>
@@ -941,9 +967,26 @@ hipError_t launch_product(ProdArgs& g, const Cut& c, void* ws, hipStream_t s) {
   g.pitch = (int64_t)g.up_col * (GATED ? 2 : 1);
   if (c.tile == 0) {
     if constexpr (!AX && !BX) {
-      const dim3 grid((unsigned)((g.e.N + 15) / 16)), block(kFewWaves * 64);
-      if (g.e.M <= 16) hipLaunchKernelGGL((few_rows_kernel<1, F16, GATED>), grid, block, 0, s, g);
-      else hipLaunchKernelGGL((few_rows_kernel<2, F16, GATED>), grid, block, 0, s, g);
+      const dim3 grid((unsigned)((g.e.N + 15) / 16), (unsigned)g.splits), block(kFewWaves * 64);
+      // More loads in flight for longer sums, as the registers allow (16 K steps'
+      // instead of 8: one row, 4096 x 4096 7.6 instead of 8.6 us, 7168 x 2048
+      // unchanged and without their masked loads).
+      auto go = [&](auto tt, auto part) {
+        constexpr int TT = decltype(tt)::value, D = TT + (GATED ? 2 : 1) > 2 ? 2 : 1;
+        constexpr bool P = decltype(part)::value;
+        if (g.kper > 2048) hipLaunchKernelGGL((few_rows_kernel<TT, F16, GATED, P, 16 / D>), grid, block, 0, s, g);
+        else hipLaunchKernelGGL((few_rows_kernel<TT, F16, GATED, P, 8 / D>), grid, block, 0, s, g);
+      };
+      using One = std::integral_constant<int, 1>;
+      using Two = std::integral_constant<int, 2>;
+      if (g.splits == 1) {
+        if (g.e.M <= 16) go(One{}, std::false_type{});
+        else go(Two{}, std::false_type{});
+      } else {
+        if (g.e.M <= 16) go(One{}, std::true_type{});
+        else go(Two{}, std::true_type{});
+        launch_join<F16, GATED>(g, s);
+      }
     }
   } else if (c.tile == 1) {
     launch_tiles<Tile64, F16, GATED, AX, BX>(g, s);

@@ -95,7 +95,7 @@ def _check_forward(a, act, ws=None):
 
 
 # every tile, edges of each, sums from one chunk to several splits
-SIZES = [(1, 1, 8), (1, 7168, 2048), (2, 16, 64), (7, 33, 40), (16, 100, 512), (17, 60, 256), (31, 48, 1000),
+SIZES = [(1, 1, 8), (1, 7168, 2048), (1, 250, 7168), (3, 40, 8200), (20, 256, 7176), (32, 1030, 4096), (2, 16, 64), (7, 33, 40), (16, 100, 512), (17, 60, 256), (31, 48, 1000),
          (33, 130, 72), (64, 64, 64), (65, 60, 512), (65, 1, 8), (100, 256, 4096), (128, 128, 128), (129, 513, 264),
          (200, 60, 2056), (257, 255, 192), (300, 1000, 8), (512, 256, 1024), (1000, 130, 136), (2049, 516, 328),
          (4100, 2052, 72)]
