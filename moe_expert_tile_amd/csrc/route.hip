@@ -490,7 +490,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
   for (int r = 0; r < NS; ++r)
     pick[r] = key_index(slot[r]) | (key_value(slot[r]) == -kInf ? 1 << 16 : 0);
-  if constexpr (BYC) {
+  float zpick[NS];   // the picks' logits
+  if constexpr (!BYC) {
+#pragma unroll
+    for (int r = 0; r < NS; ++r) zpick[r] = key_value(slot[r]);
+  } else {
     // neighbours in the order that are close, unless their logits and
     // biases are the same and the index decides (zero biases over 16-bit
     // logits are full of those)
@@ -501,6 +505,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
       const bool on = live && j < picks;
       const float c = key_value(slot[r]);
       const float zj = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : 0.f;
+      zpick[r] = zj;
       const float bj = on && a.bias ? a.bias[pick[r] & 0xffff] : 0.f;
       const float sj = exp_fast(zj - zmax) * zinv;   // of a softmax
       float qc = __shfl_up(c, 1, LPR), qz = __shfl_up(zj, 1, LPR), qb = __shfl_up(bj, 1, LPR);
@@ -526,7 +531,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
       if (lane / LPR == at / LPR) {
 #pragma unroll
         for (int r = 0; r < NS; ++r)
-          if (r * LPR + l < a.k) pick[r] = pbuf[r * LPR + l];
+          if (r * LPR + l < a.k) {
+            pick[r] = pbuf[r * LPR + l];
+            zpick[r] = load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff));
+          }
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -537,8 +545,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
   for (int r = 0; r < NS; ++r) {
     const bool on = live && r * LPR + l < a.k && !(pick[r] >> 16);
-    if constexpr (BYC) zs[r] = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : -kInf;
-    else zs[r] = on ? key_value(slot[r]) : -kInf;
+    zs[r] = on ? zpick[r] : -kInf;
     top = fmaxf(top, zs[r]);
   }
   if (a.score == MOE_SCORE_SOFTMAX) bad |= top == kInf;

@@ -383,3 +383,17 @@ def test_every_tile_whole_and_split(what, M, N, K, dtype):
         ref, mag, terms = torch.mm(g.t().contiguous(), x), torch.mm(g.t().contiguous().abs(), x.abs()), M
     bound = (terms + 64) * U * mag * (1 + half) + half * ref.abs() + tiny
     assert bool(((got.double() - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_a_vocabulary_of_columns(M):
+    """Far more columns than rows: 200003 of them, an odd number."""
+    a = _inputs(M, 200003, 64, "none", "bf16", 12)
+    _m().moe_linear(a["x"], a["w"], a["out"], bias=a["bias"], residual=a["residual"])
+    z = torch.mm(a["x"].double(), a["w"].double().t().contiguous()) + a["bias"].double()
+    y = z + a["residual"].double()
+    S = torch.mm(a["x"].double().abs(), a["w"].double().abs().t().contiguous()) + a["bias"].double().abs()
+    bound = (66 * U * S + U * (y.abs() + a["residual"].double().abs())) * 1.01 + _half(torch.bfloat16) * y.abs()
+    assert bool(((a["out"].double() - y).abs() <= bound).all())
+    got = _check_backward(dict(a, pre=None, w=a["w"][:4099], d_out=a["d_out"][:, :4099].contiguous()), "none")
+    assert got["dw"].shape == (4099, 64)

@@ -298,3 +298,18 @@ def test_long_batches_of_middle_sizes():
                 assert torch.equal(ids[t:t + 400], few)
                 assert bool(((w[t:t + 400] - fw).abs() <= 2.0 ** -18 * fw).all())
             _check(z[:40].contiguous(), k, **kw)
+
+
+def test_default_options_through_the_c_entry_point():
+    m = _m()
+    z = torch.randn(20, 24, device="cuda")
+    ids, w = torch.zeros(20, 3, dtype=torch.int32, device="cuda"), torch.zeros(20, 3, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    assert m._lib.moe_route(20, 24, 3, z.data_ptr(), 2, 0, None, None, ids.data_ptr(), w.data_ptr(), s) == m.MOE_OK
+    want, ww = _check(z, 3)
+    assert torch.equal(ids, want) and torch.equal(w, ww)
+    d, dn, g = torch.empty_like(z), torch.empty_like(z), torch.randn(20, 3, device="cuda")
+    assert m._lib.moe_route_backward(20, 24, 3, z.data_ptr(), 2, 0, ids.data_ptr(), w.data_ptr(), g.data_ptr(), None,
+                                     d.data_ptr(), 0, s) == m.MOE_OK
+    m.moe_route_backward(z, ids, w, g, dn)
+    assert torch.equal(d, dn)
