@@ -265,13 +265,15 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int n, floa
 // us.)  Counters of the gated one: 1.86 GHz under load, MFMA busy 62% of the
 // time, LDS 24%, no bank conflicts, wavefronts waiting 36%: what is left is the
 // loads' latency per CU.  Other shapes measured: 256 x 256 as four wavefronts of
-// 128 x 128 5-10% slower; 128 x 256 and 256 x 128 with three stages within 2% of
-// the choice made without them; the stage's first operand fetches moved in front
-// of the meeting of the wavefronts within 1%.  The two-stage ring of a
-// 256 x 256 tile takes 128 KB of LDS, so a CU holds one workgroup of it, two of
-// 128 x 128 and three of 64 x 128, whose epilogues overlap other workgroups'
-// multiplications: with little K those win (dx of 8192 x 256 x 7168 57 us in
-// 256 x 256, 52 us in 128 x 128; its dw, K = 8192, 51 and 45 us).
+// 128 x 128 5-10% slower; 256 x 128 with three stages, next to 128 x 256, 0.2% less
+// over 104 products; the stage's first operand fetches moved in front of the
+// meeting of the wavefronts within 1%.  The two-stage ring of a 256 x 256 tile takes
+// 128 KB of LDS, so a CU holds one workgroup of it, two of 128 x 128 and three of
+// 64 x 128, whose epilogues overlap other workgroups' multiplications: they win
+// with little K or many splits (gated 20000 x 512 x 1024 69 us in 256 x 256, 64 us in
+// 128 x 128).  Between them 128 x 256 keeps three stages in 144 KB, two of them in
+// flight, for sums that are long where output tiles are few (8192 x 512 x 4096
+// 59 us without it, 51 us with it; dw of 8192 x 256 x 7168 58 and 52 us).
 
 struct ProdArgs {
   const uint16_t *a, *b;   // A [M, K] or, across k, [K, M]; B [N or 2N, K] or [K, N]
@@ -287,9 +289,9 @@ struct ProdArgs {
 
 constexpr int kBK = 64;    // K step
 
-template <int BM_, int BN_, int WAVES_M, int WAVES_N>
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int STAGES_ = 2>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_;
+  static constexpr int BM = BM_, BN = BN_, STAGES = STAGES_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int FM = WM / 32, FN = WN / 32;
@@ -306,7 +308,7 @@ struct Tile {
     static constexpr int PITCH = FN * 32 + 4;
   };
   static constexpr int EPI_ELEMS = NW * 32 * (FN * 32 + 4) * 2;
-  static constexpr int LDS_ELEMS = 2 * STAGE > EPI_ELEMS ? 2 * STAGE : EPI_ELEMS;
+  static constexpr int LDS_ELEMS = STAGES * STAGE > EPI_ELEMS ? STAGES * STAGE : EPI_ELEMS;
   static constexpr int A_LOADS = BM / 8 / NW;     // 1 KB wave loads a stage (8 rows of 128 bytes)
   static constexpr int B_LOADS = BN / 8 / NW;
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole wave loads");
@@ -317,6 +319,7 @@ typedef Tile<256, 256, 2, 4> Tile256;
 typedef Tile<256, 256, 4, 2> Tile256G;    // gated: each wave's columns hold as many gate as up ones
 typedef Tile<128, 128, 2, 2> Tile128;
 typedef Tile<64, 128, 2, 2> Tile64;
+typedef Tile<128, 256, 2, 4, 3> TileWide;
 
 // a workgroup's place in the tile order: workgroup i runs on XCD i mod 8; each
 // XCD gets a contiguous run, in which 8 row tiles x 4 column tiles share their
@@ -428,9 +431,12 @@ void product_kernel(ProdArgs g) {
   // stage k into half k % 2 of the ring.  Along k, `last` masks the chunks past
   // the end of K (each is whole or absent, or dz's with its zeros);
   // across k, a stage has a descriptor of its own that ends with its last row.
+  auto ring = [&](int k) __attribute__((always_inline)) {
+    return C::STAGES == 2 ? lds + (k & 1) * C::STAGE : lds + (k % C::STAGES) * C::STAGE;
+  };
   auto issue = [&](int k, auto last_tag) __attribute__((always_inline)) {
     constexpr bool LAST = decltype(last_tag)::value;
-    char* base = (char*)(lds + (k & 1) * C::STAGE);
+    char* base = (char*)ring(k);
     const int koff = 2 * kBK * k;
     const int64_t rows = LAST ? klast : kBK;
     const __amdgpu_buffer_rsrc_t ar =
@@ -477,14 +483,17 @@ void product_kernel(ProdArgs g) {
 
   using Mid = std::integral_constant<bool, false>;
   using Last = std::integral_constant<bool, true>;
-  // one stage: wait for its loads and for every wave's reads of the other
-  // half, refill that half (next: 0 nothing, 1 a whole stage, 2 the last one),
-  // multiply with the operand fetches one MFMA step ahead
-  auto step = [&](int k, auto next_tag) __attribute__((always_inline)) {
+  // one stage: wait for its loads (a three-stage ring leaves the next stage's in
+  // flight) and for every wave's reads of the part refilled next, refill that
+  // (next: 0 nothing, 1 a whole stage, 2 the last one), multiply with the
+  // operand fetches one MFMA step ahead
+  auto step = [&](int k, auto next_tag, auto flying_tag) __attribute__((always_inline)) {
     constexpr int NEXT = decltype(next_tag)::value;
-    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+    constexpr int FLYING = decltype(flying_tag)::value ? C::A_LOADS + C::B_LOADS : 0;   // loads that may be outstanding
+    static_assert(FLYING < 16, "vector memory counter's low bits");
+    __builtin_amdgcn_s_waitcnt(0x70 | FLYING);   // vmcnt(FLYING) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
-    const uint16_t* sa = lds + (k & 1) * C::STAGE;
+    const uint16_t* sa = ring(k);
     const uint16_t* sb = sa + C::A_ELEMS;
     v8 pw[2][C::FN], px[2][C::FM];
     auto fetch = [&](int kk) __attribute__((always_inline)) {
@@ -502,8 +511,8 @@ void product_kernel(ProdArgs g) {
       }
     };
     fetch(0);
-    if constexpr (NEXT == 1) issue(k + 1, Mid{});
-    if constexpr (NEXT == 2) issue(k + 1, Last{});
+    if constexpr (NEXT == 1) issue(k + C::STAGES - 1, Mid{});
+    if constexpr (NEXT == 2) issue(k + C::STAGES - 1, Last{});
 #pragma unroll
     for (int kk = 0; kk < C::KK; ++kk) {
       if (kk + 1 < C::KK) fetch(kk + 1);
@@ -524,12 +533,22 @@ void product_kernel(ProdArgs g) {
     }
   };
   if (KT > 0) {
-    if (KT > 1) issue(0, Mid{});
-    else issue(0, Last{});
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    constexpr int AHEAD = C::STAGES - 1;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (k + 1 < KT) issue(k, Mid{});
+      else if (k + 1 == KT) issue(k, Last{});
+    }
+    using Fly = std::integral_constant<bool, (C::STAGES > 2)>;
     int k = 0;
-    for (; k + 2 < KT; ++k) step(k, std::integral_constant<int, 1>{});
-    if (k + 1 < KT) step(k++, std::integral_constant<int, 2>{});
-    step(k, std::integral_constant<int, 0>{});
+    for (; k + AHEAD + 1 < KT; ++k) step(k, I1{}, Fly{});
+    if (k + AHEAD < KT) step(k++, I2{}, Fly{});
+    if constexpr (C::STAGES > 2)
+      if (k + 1 < KT) step(k++, I0{}, Fly{});
+    step(k, I0{}, Mid{});
   }
 
   // Epilogue: 32 rows of a wave's columns at a time go through LDS (each wave
@@ -853,7 +872,8 @@ int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // How a product is cut: tile 0 = few rows, 1 = 64 x 128, 2 = 128 x 128,
-// 3 = 256 x 256 (a gated product's columns count twice), and the splits of K.
+// 3 = 256 x 256, 4 = 128 x 256 (a gated product's columns count twice), and the
+// splits of K.
 struct Cut {
   int tile, splits;
   int64_t kper;
@@ -875,34 +895,38 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
     const int64_t kper = round_up((K + s - 1) / s, kBK);
     return {0, K > 0 ? (int)((K + kper - 1) / kper) : 1, kper};
   }
-  // Time of each choice, the smallest wins.  A K step of a CU's workgroups takes
-  // what their multiplications take at the rate the tile reaches, at least a
-  // load's latency; a round of workgroups adds its fill and epilogue; a split
-  // adds its partial sums' round trip and the second launch.  The constants are
-  // fitted to times of every choice over 80 products (both directions, 32 to
-  // 8192 rows): the choice costs 1.5% over the best one on average.  Both sides
-  // of a typical decision: 8192 x 256 x 7168 takes 43 us as 128 x 128 tiles in 4
-  // splits and 50 us as 256 x 256 in 8; 8192 x 2048 x 7168 takes 218 us and, as
-  // 256 x 256 in one piece, 190 us.
-  static const int bm[4] = {0, 64, 128, 256}, bn[4] = {0, 128, 128, 256}, per_cu[4] = {0, 3, 2, 1};
-  static const double rate[4] = {0, 3.3e6, 4.85e6, 6.8e6};       // flop per us and CU
-  static const double latency[4] = {0, 0.45, 0.75, 1.47};       // us a step
-  static const double round_us[4] = {0, 2.55, 4.0, 7.7};
+  // Time of each choice, the smallest wins.  A K step takes a load's latency, or
+  // what the multiplications of the workgroups that share a CU take; a round of
+  // workgroups adds its fill and epilogue; a split adds its partial sums' round
+  // trip and the second launch, which adds them up one after the other.  The
+  // constants are fitted to times of every choice over 228 products (forward,
+  // gated, dx and dw, 33 to 30000 rows, operands not in a cache): the choice
+  // costs 1.3% over the best one on average.  Both sides of typical decisions:
+  // 8192 x 256 x 7168 takes 49 us as 128 x 256 tiles in 4 splits, 54 us as
+  // 128 x 128 in 4, 58 us as 256 x 256 in 8 and 62 us as 64 x 128 in 2;
+  // 8192 x 2048 x 7168 takes 196 us as 256 x 256 in one piece and 224 us as
+  // 128 x 256; 40 x 512 x 4096 takes 12.2 us as 64 x 128 in 12 splits, 15.5 us in 4.
+  static const int bm[5] = {0, 64, 128, 256, 128}, bn[5] = {0, 128, 128, 256, 256};
+  static const int per_cu[5] = {0, 3, 2, 1, 1};                       // workgroups of it a CU holds
+  static const double latency[5] = {0, 0.591, 0.739, 1.32, 0.816};     // us a step
+  static const double shared[5] = {0, 0.352, 0.496, 0, 0};            // ... and workgroup on the CU
+  static const double round_us[5] = {0, 4.32, 4.77, 8.5, 5.7};
+  static const int pieces[] = {1, 2, 3, 4, 6, 8, 12, 16, 32};
   const int64_t steps = (K + kBK - 1) / kBK;
   Cut best = {1, 1, round_up(K, kBK)};
   double best_us = 1e30;
-  for (int t = 1; t <= 3; ++t) {
+  for (int t = 1; t <= 4; ++t) {
     int64_t tiles = ((M + bm[t] - 1) / bm[t]) * ((NZ + bn[t] - 1) / bn[t]);
     if (tiles < 1) tiles = 1;   // no rows: nothing to cut
-    for (int s = 1; s <= 32; s *= 2) {
+    for (int s : pieces) {
       if (s > 1 && steps < 4 * s) break;
       const int64_t per = (steps + s - 1) / s;
       const int64_t blocks = tiles * s, slots = (int64_t)kCus * per_cu[t];
       const int64_t conc = blocks >= slots ? per_cu[t] : (blocks + kCus - 1) / kCus;
-      const double work_us = conc * 2.0 * bm[t] * bn[t] * kBK / rate[t];
+      const double work_us = conc * shared[t];
       const double step_us = work_us > latency[t] ? work_us : latency[t];
       double us = (double)((blocks + kCus * conc - 1) / (kCus * conc)) * (per * step_us + round_us[t]);
-      if (s > 1) us += 2.9 + (double)s * M * NZ * 8 / 5.05e6;
+      if (s > 1) us += 2.0 + 0.24 * s + (double)s * M * NZ * 8 / 5.7e6;
       if (us < best_us) {
         best_us = us;
         best = {t, s, per * kBK};
@@ -992,6 +1016,8 @@ hipError_t launch_product(ProdArgs& g, const Cut& c, void* ws, hipStream_t s) {
     launch_tiles<Tile64, F16, GATED, AX, BX>(g, s);
   } else if (c.tile == 2) {
     launch_tiles<Tile128, F16, GATED, AX, BX>(g, s);
+  } else if (c.tile == 4) {
+    launch_tiles<TileWide, F16, GATED, AX, BX>(g, s);
   } else {
     launch_tiles<std::conditional_t<GATED, Tile256G, Tile256>, F16, GATED, AX, BX>(g, s);
   }

@@ -342,6 +342,14 @@ EACH_TILE = [
     ("dx", 535, 182, 8), ("dx", 104, 1502, 8), ("dx", 4551, 149, 1304), ("dx", 3111, 5106, 8), ("dx", 1707, 142, 7216),
     ("dx", 8623, 7572, 136), ("dw", 467, 44, 16), ("dw", 1618, 12, 8), ("dw", 143, 6333, 912), ("dw", 2350, 6271, 8),
     ("dw", 141, 2961, 4280), ("dw", 7852, 8460, 136),
+    # the 128 x 256 tile with its three stages: whole, and splits that end with 1, 2 and more stages
+    ("fwd", 459, 8251, 328), ("fwd", 2065, 134, 8472), ("fwd", 2636, 145, 8560), ("fwd", 2834, 130, 3904),
+    ("gated", 3022, 650, 336), ("gated", 2087, 70, 8480), ("gated", 71, 2412, 8576), ("gated", 70, 5517, 1808),
+    ("dx", 8861, 327, 416), ("dx", 2073, 8460, 184), ("dx", 2793, 3937, 136),
+    ("dw", 337, 9480, 416), ("dw", 7812, 2131, 136), ("dw", 2988, 69, 8416),
+    # the others split (and 64 rows whole)
+    ("fwd", 40, 2, 8), ("fwd", 4500, 2, 3592), ("fwd", 8253, 394, 3712), ("gated", 6777, 2, 2032),
+    ("gated", 206, 8224, 3448), ("dx", 8343, 1848, 8), ("dw", 4252, 8292, 392),
 ]
 
 
