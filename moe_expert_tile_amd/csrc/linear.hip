@@ -650,15 +650,19 @@ void product_kernel(ProdArgs g) {
 }
 
 // Sums of a split product's partial sums, in split order, and the epilogue.
-// Memory bound (8192 x 256 in 4 splits, 42 MB, 7 us).
+// Memory bound (8192 x 256 in 4 splits, 42 MB, 7 us) or, with little to write,
+// bound by the partial sums' latency: four of them are read together and a
+// workgroup is one wavefront, so that small outputs spread over the CUs
+// (40 x 512 x 4096 in 16 splits 12.0 us with one after the other, 9.3 us so).
 template <bool F16, bool GATED>
-__global__ __launch_bounds__(256) void join_kernel(ProdArgs g) {
+__global__ __launch_bounds__(64) void join_kernel(ProdArgs g) {
   const int quads = (g.e.N + 3) / 4;
   const int64_t total = g.e.M * quads;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 64) {
     const int64_t m = i / quads;
     const int n = (int)(i - m * quads) * 4;
     float z[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int s = 0; s < g.splits; ++s) {
       const float* p = g.part + (s * g.e.M + m) * g.pitch + n;
       const float4 x = *(const float4*)p;
@@ -885,32 +889,32 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
   if (M <= 32 && !across) {
     // A CU takes about 30 KB/us from the caches (64 lines in flight), so a few
     // workgroups with long sums are split along K, where that saves more than
-    // the join's launch: 20 rows through 256 x 7168 17.0 us whole and 8.1 us in 8
-    // splits, one row 10.0 and 7.0 us; one row through 1024 x 4096, below that,
-    // 6.8 us whole.
+    // the join's launch: 20 rows through 256 x 7168 18.1 us whole and 7.5 us in 8
+    // splits, one row 10.8 and 6.7 us; 16 rows through 256 x 2048, below that,
+    // 5.8 us whole and 6.2 us in 4 splits.
     const int64_t blocks = (N + 15) / 16, bytes = (16 * (gated ? 2 : 1) + M) * K * 2;
     int64_t s = 1;
     while (s < 8 && 2 * s * blocks <= kCus && K / (2 * s) >= 256) s *= 2;
-    if ((double)bytes / 30e3 * (1.0 - 1.0 / s) < 4.5) s = 1;
+    if ((double)bytes / 30e3 * (1.0 - 1.0 / s) < 3.9) s = 1;
     const int64_t kper = round_up((K + s - 1) / s, kBK);
     return {0, K > 0 ? (int)((K + kper - 1) / kper) : 1, kper};
   }
   // Time of each choice, the smallest wins.  A K step takes a load's latency, or
   // what the multiplications of the workgroups that share a CU take; a round of
   // workgroups adds its fill and epilogue; a split adds its partial sums' round
-  // trip and the second launch, which adds them up one after the other.  The
-  // constants are fitted to times of every choice over 228 products (forward,
-  // gated, dx and dw, 33 to 30000 rows, operands not in a cache): the choice
-  // costs 1.3% over the best one on average.  Both sides of typical decisions:
+  // trip and the second launch.  The constants are fitted to times of every
+  // choice over 228 products (forward, gated, dx and dw, 33 to 30000 rows,
+  // operands not in a cache): the choice costs 1% over the best one on average.
+  // Both sides of typical decisions:
   // 8192 x 256 x 7168 takes 49 us as 128 x 256 tiles in 4 splits, 54 us as
   // 128 x 128 in 4, 58 us as 256 x 256 in 8 and 62 us as 64 x 128 in 2;
   // 8192 x 2048 x 7168 takes 196 us as 256 x 256 in one piece and 224 us as
-  // 128 x 256; 40 x 512 x 4096 takes 12.2 us as 64 x 128 in 12 splits, 15.5 us in 4.
+  // 128 x 256; 40 x 512 x 4096 takes 10.2 us as 64 x 128 in 16 splits, 14.5 us in 4.
   static const int bm[5] = {0, 64, 128, 256, 128}, bn[5] = {0, 128, 128, 256, 256};
   static const int per_cu[5] = {0, 3, 2, 1, 1};                       // workgroups of it a CU holds
-  static const double latency[5] = {0, 0.591, 0.739, 1.32, 0.816};     // us a step
-  static const double shared[5] = {0, 0.352, 0.496, 0, 0};            // ... and workgroup on the CU
-  static const double round_us[5] = {0, 4.32, 4.77, 8.5, 5.7};
+  static const double latency[5] = {0, 0.564, 0.751, 1.327, 0.831};    // us a step
+  static const double shared[5] = {0, 0.353, 0.51, 0, 0};             // ... and workgroup on the CU
+  static const double round_us[5] = {0, 4.55, 4.76, 7.9, 5.7};
   static const int pieces[] = {1, 2, 3, 4, 6, 8, 12, 16, 32};
   const int64_t steps = (K + kBK - 1) / kBK;
   Cut best = {1, 1, round_up(K, kBK)};
@@ -926,7 +930,7 @@ Cut choose_cut(int64_t M, int64_t N, int64_t K, bool gated, bool across) {
       const double work_us = conc * shared[t];
       const double step_us = work_us > latency[t] ? work_us : latency[t];
       double us = (double)((blocks + kCus * conc - 1) / (kCus * conc)) * (per * step_us + round_us[t]);
-      if (s > 1) us += 2.0 + 0.24 * s + (double)s * M * NZ * 8 / 5.7e6;
+      if (s > 1) us += 2.2 + 0.047 * s + (double)s * M * NZ * 8 / 5.58e6;
       if (us < best_us) {
         best_us = us;
         best = {t, s, per * kBK};
@@ -963,8 +967,8 @@ void launch_dz(const DzArgs& a, hipStream_t s) {
 
 template <bool F16, bool GATED>
 void launch_join(const ProdArgs& g, hipStream_t s) {
-  const int64_t blocks = (g.e.M * ((g.e.N + 3) / 4) + 255) / 256;
-  hipLaunchKernelGGL((join_kernel<F16, GATED>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, g);
+  const int64_t blocks = (g.e.M * ((g.e.N + 3) / 4) + 63) / 64;
+  hipLaunchKernelGGL((join_kernel<F16, GATED>), dim3((unsigned)(blocks < 32768 ? blocks : 32768)), dim3(64), 0, s, g);
 }
 
 template <class C, bool F16, bool GATED, bool AX, bool BX>

@@ -349,7 +349,8 @@ EACH_TILE = [
     ("dw", 337, 9480, 416), ("dw", 7812, 2131, 136), ("dw", 2988, 69, 8416),
     # the others split (and 64 rows whole)
     ("fwd", 40, 2, 8), ("fwd", 4500, 2, 3592), ("fwd", 8253, 394, 3712), ("gated", 6777, 2, 2032),
-    ("gated", 206, 8224, 3448), ("dx", 8343, 1848, 8), ("dw", 4252, 8292, 392),
+    ("gated", 206, 8224, 3448), ("dx", 8343, 1848, 8), ("dx", 6726, 3380, 536), ("dx", 2085, 5704, 136),
+    ("dw", 4252, 8292, 392), ("dw", 3606, 66, 5648),
 ]
 
 
