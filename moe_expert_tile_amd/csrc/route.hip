@@ -490,14 +490,17 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
   for (int r = 0; r < NS; ++r)
     pick[r] = key_index(slot[r]) | (key_value(slot[r]) == -kInf ? 1 << 16 : 0);
-  float zpick[NS];   // the picks' logits
+  float zpick[NS], bpick[NS];   // the picks' logits, and with BYC biases
   if constexpr (!BYC) {
 #pragma unroll
     for (int r = 0; r < NS; ++r) zpick[r] = key_value(slot[r]);
   } else {
-    // neighbours in the order that are close, unless their logits and
+    // neighbours among the picks that are close, unless their logits and
     // biases are the same and the index decides (zero biases over 16-bit
-    // logits are full of those)
+    // logits are full of those).  The last pick and the first one left out are
+    // held against the largest error of any score (`edge`): what is left out
+    // further down may have a larger score, and error, than they have.
+    bool edge = false;
     float pc = kInf, pz = 0.f, pb = 0.f, ps = 0.f;   // the last lane's pick of the previous round
 #pragma unroll
     for (int r = 0; r < NS; ++r) {
@@ -507,16 +510,53 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
       const float zj = on ? load_as_float(a.logits, a.dtype, t * a.ld + (pick[r] & 0xffff)) : 0.f;
       zpick[r] = zj;
       const float bj = on && a.bias ? a.bias[pick[r] & 0xffff] : 0.f;
+      bpick[r] = bj;
       const float sj = exp_fast(zj - zmax) * zinv;   // of a softmax
       float qc = __shfl_up(c, 1, LPR), qz = __shfl_up(zj, 1, LPR), qb = __shfl_up(bj, 1, LPR);
       float qs = __shfl_up(sj, 1, LPR);
       if (l == 0) { qc = pc; qz = pz; qb = pb; qs = ps; }
-      near |= on && j > 0 && qc - c <= error2(fabsf(qc), fmaxf(qs, sj)) && !(qz == zj && qb == bj);
+      if (j < a.k) near |= on && j > 0 && qc - c <= error2(fabsf(qc), fmaxf(qs, sj)) && !(qz == zj && qb == bj);
+      else edge |= on && qc - c <= error2(fabsf(qc), zinv);
       if constexpr (NS > 1) {
         pc = __shfl(c, LPR - 1, LPR);
         pz = __shfl(zj, LPR - 1, LPR);
         pb = __shfl(bj, LPR - 1, LPR);
         ps = __shfl(sj, LPR - 1, LPR);
+      }
+    }
+    if (__ballot(edge)) {
+      // Everything left out within reach of the last pick, by its own error
+      // then: the first one, and what the lanes' lists still hold (copies
+      // that moving up left at a list's end are not below the last pick, or
+      // are looked at twice).
+      edge = max_lanes<LPR>(near ? 2.f : edge ? 1.f : 0.f) == 1.f;   // (not where the row is ranked again anyway)
+      const int at = (lane - l) + (a.k - 1) % LPR;
+      double last = kKeyAbsent;
+      float zk = 0.f, bk = 0.f;
+#pragma unroll
+      for (int r = 0; r < NS; ++r) {
+        if ((a.k - 1) / LPR == r) {
+          last = __shfl(slot[r], at);
+          zk = __shfl(zpick[r], at);
+          bk = __shfl(bpick[r], at);
+        }
+      }
+      const float ck = key_value(last);
+      const float low = ck - 0.5f * error2(fabsf(ck), exp_fast(zk - zmax) * zinv);
+      auto reaches = [&](float c, float s) { return c + 0.5f * error2(fabsf(c), s) >= low; };
+      auto look = [&](float c, float zc, float bc) {
+        if (reaches(c, exp_fast(zc - zmax) * zinv) && !(zc == zk && bc == bk)) near = true;
+      };
+#pragma unroll
+      for (int r = 0; r < NS; ++r)
+        if (edge && r * LPR + l == a.k) look(key_value(slot[r]), zpick[r], bpick[r]);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float c = key_value(key[i]);
+        if (edge && key[i] < last && reaches(c, zinv)) {
+          const int e = key_index(key[i]);
+          look(c, load_as_float(a.logits, a.dtype, t * a.ld + e), a.bias ? a.bias[e] : 0.f);
+        }
       }
     }
     near = max_lanes<LPR>(near ? 1.f : 0.f) > 0.f;
