@@ -318,7 +318,7 @@ typedef struct moe_route_opts {
   int32_t n_group;      /* experts in groups of E / n_group neighbours (a divisor of E, at most 64); 0 = 1 */
   int32_t topk_group;   /* groups a token may choose from; 0 = n_group */
   int32_t group_score;  /* MOE_GROUP_MAX: a group's best c; MOE_GROUP_TOP2: the sum of its two best (groups of
-                           two experts at least) */
+                           two experts at least), -infinity if fewer than two of them are not masked */
   float scale;          /* factor on the weights, finite and above 0; 0 = 1 */
 } moe_route_opts;
 

@@ -444,7 +444,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     if constexpr (LPR > 8) merge(std::integral_constant<int, 8>{});
     if constexpr (LPR > 16) merge(std::integral_constant<int, 16>{});
     if constexpr (LPR > 32) merge(std::integral_constant<int, 32>{});
-    const float sc = a.top2 ? b1 + b2 : b1;
+    const float sc = a.top2 ? (b2 == -kInf ? -kInf : b1 + b2) : b1;   // (+inf, of a bias, and masked ones: masked)
     int better = 0;
     for (int o = 0; o < a.groups; ++o) {
       const float os = __shfl(sc, (lane - l) + o * a.lpg);
@@ -515,8 +515,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
       float qc = __shfl_up(c, 1, LPR), qz = __shfl_up(zj, 1, LPR), qb = __shfl_up(bj, 1, LPR);
       float qs = __shfl_up(sj, 1, LPR);
       if (l == 0) { qc = pc; qz = pz; qb = pb; qs = ps; }
-      if (j < a.k) near |= on && j > 0 && qc - c <= error2(fabsf(qc), fmaxf(qs, sj)) && !(qz == zj && qb == bj);
-      else edge |= on && qc - c <= error2(fabsf(qc), zinv);
+      // (an infinite c, of a bias, is exact)
+      if (j < a.k) near |= on && j > 0 && qc < kInf && qc - c <= error2(fabsf(qc), fmaxf(qs, sj)) && !(qz == zj && qb == bj);
+      else edge |= on && qc < kInf && qc - c <= error2(fabsf(qc), zinv);
       if constexpr (NS > 1) {
         pc = __shfl(c, LPR - 1, LPR);
         pz = __shfl(zj, LPR - 1, LPR);

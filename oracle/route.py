@@ -34,7 +34,7 @@ def route(z, k, kind="softmax", bias=None, renorm=False, n_group=1, topk_group=0
         c = np.where(np.isneginf(z[t]), -np.inf, c)
         if n_group > 1:
             parts = [sorted(c[g * size:(g + 1) * size], reverse=True) for g in range(n_group)]
-            value = [p[0] + p[1] if top2 else p[0] for p in parts]
+            value = [(-np.inf if np.isneginf(p[1]) else p[0] + p[1]) if top2 else p[0] for p in parts]
             kept = sorted(range(n_group), key=lambda g: (-value[g], g))[:keep]
             for g in range(n_group):
                 if g not in kept:

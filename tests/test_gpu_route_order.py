@@ -118,3 +118,42 @@ def test_ties_around_the_last_pick(E, k):
             ids, _ = _ids(z, k, kind, bias)
             want, _ = OR.route(z, k, kind=kind, bias=bias)
             assert np.array_equal(ids, want)
+
+
+@pytest.mark.parametrize("E,G", [(16, 4), (64, 8), (256, 8), (1024, 64)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_a_group_of_one_expert_with_an_infinite_bias(E, G, kind):
+    """A +inf bias puts its expert first.  Its group's two best are +inf and a
+    masked expert, so under the sum of two the group ranks as masked; under
+    the maximum, or with a second expert, it ranks first."""
+    size = E // G
+    rng = np.random.default_rng(E)
+    z = rng.standard_normal((20, E)).astype(np.float32)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    bias[E - 1] = np.inf
+    alone = z.copy()
+    alone[:, E - size:E - 1] = -np.inf
+    for logits, top2 in ((alone, True), (alone, False), (z, True), (z, False)):
+        for k in (1, 3):
+            kw = dict(n_group=G, topk_group=2, top2=top2)
+            ids, w = _ids(logits, k, kind, bias, **kw)
+            want, ww = OR.route(logits, k, kind=kind, bias=bias, **kw)
+            assert np.array_equal(ids, want), (ids[:3], want[:3])
+            assert np.all(np.abs(w - ww) <= 2.0 ** -18 * ww)
+            assert (ids[:, 0] == E - 1).all() == (not (top2 and logits is alone))
+
+
+def test_several_infinite_biases():
+    """+inf ones rank first among themselves by index, then the others; near
+    ones behind them are still ranked in 64 bits."""
+    rng = np.random.default_rng(3)
+    z = np.repeat(rng.standard_normal((1, 96)), 30, 0).astype(np.float32)
+    for kind in ("softmax", "sigmoid"):
+        bias = _bias_for(np.full(96, 0.5), OR.scores(z[:1], kind)[0])
+        bias[[70, 11, 40]] = np.inf
+        bias[5] = -np.inf
+        for k in (1, 2, 3, 4, 12):
+            for kw in ({}, dict(n_group=8, topk_group=4), dict(n_group=8, topk_group=4, top2=True)):
+                ids, _ = _ids(z, k, kind, bias, **kw)
+                want, _ = OR.route(z, k, kind=kind, bias=bias, **kw)
+                assert np.array_equal(ids, want), (k, kw)
