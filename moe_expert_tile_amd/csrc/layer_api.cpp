@@ -22,7 +22,7 @@ constexpr int64_t kMaxPitch = 1 << 21;
 // checks shared by the routing calls; fills in the defaults of opts and ld
 int check_route(int64_t tokens, int32_t experts, int32_t top_k, const void* logits, int32_t dtype, int64_t* ld,
                 const moe_route_opts* opts, moe_route_opts* o) {
-  if (tokens < 0 || tokens > (1ll << 26)) return MOE_EINVAL;   // threads of a launch in 32 bits
+  if (tokens < 0 || tokens > (1ll << 26)) return MOE_EINVAL;
   if (experts < 1 || experts > 1024 || top_k < 1 || top_k > 32 || top_k > experts) return MOE_EINVAL;
   if (dtype < MOE_BF16 || dtype > MOE_F32) return MOE_EINVAL;
   if (*ld == 0) *ld = experts;

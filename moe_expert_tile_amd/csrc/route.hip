@@ -807,17 +807,30 @@ __global__ __launch_bounds__(kRouteThreads) void route_back_kernel(RouteBackArgs
 
 bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Workgroups of one launch: a launch's threads are counted in 32 bits, and 64
+// lanes a row make 2^32 of them for the 2^26 tokens a call may have, so such a
+// batch takes two launches.
+constexpr int64_t kLaunchBlocks = 1 << 23;
+static_assert(kLaunchBlocks * kRouteThreads < (1ll << 32), "threads of a launch");
+
 template <int LPR, int VPL>
-void launch_route_k(const RouteArgs& a, bool byc, hipStream_t s) {
+void launch_route_k(const RouteArgs& all, bool byc, hipStream_t s) {
   constexpr int RPW = 64 / LPR, WPB = kRouteThreads / 64;
-  const unsigned grid = (unsigned)((a.T + RPW * WPB - 1) / (RPW * WPB));
-  const size_t lds = byc ? (size_t)WPB * (a.E + a.groups + 16 + 1) * 8 : 0;
-  if (a.k <= 8) {
-    if (byc) hipLaunchKernelGGL((route_kernel<LPR, VPL, 8, true>), dim3(grid), dim3(kRouteThreads), lds, s, a);
-    else hipLaunchKernelGGL((route_kernel<LPR, VPL, 8, false>), dim3(grid), dim3(kRouteThreads), 0, s, a);
-  } else {
-    if (byc) hipLaunchKernelGGL((route_kernel<LPR, VPL, 32, true>), dim3(grid), dim3(kRouteThreads), lds, s, a);
-    else hipLaunchKernelGGL((route_kernel<LPR, VPL, 32, false>), dim3(grid), dim3(kRouteThreads), 0, s, a);
+  const size_t lds = byc ? (size_t)WPB * (all.E + all.groups + 16 + 1) * 8 : 0;
+  for (int64_t t0 = 0; t0 < all.T; t0 += kLaunchBlocks * RPW * WPB) {
+    RouteArgs a = all;
+    a.T = all.T - t0 < kLaunchBlocks * RPW * WPB ? all.T - t0 : kLaunchBlocks * RPW * WPB;
+    a.logits = (const char*)all.logits + t0 * all.ld * (all.dtype == MOE_F32 ? 4 : 2);
+    a.ids += t0 * all.k;
+    a.w += t0 * all.k;
+    const unsigned grid = (unsigned)((a.T + RPW * WPB - 1) / (RPW * WPB));
+    if (a.k <= 8) {
+      if (byc) hipLaunchKernelGGL((route_kernel<LPR, VPL, 8, true>), dim3(grid), dim3(kRouteThreads), lds, s, a);
+      else hipLaunchKernelGGL((route_kernel<LPR, VPL, 8, false>), dim3(grid), dim3(kRouteThreads), 0, s, a);
+    } else {
+      if (byc) hipLaunchKernelGGL((route_kernel<LPR, VPL, 32, true>), dim3(grid), dim3(kRouteThreads), lds, s, a);
+      else hipLaunchKernelGGL((route_kernel<LPR, VPL, 32, false>), dim3(grid), dim3(kRouteThreads), 0, s, a);
+    }
   }
 }
 
@@ -879,6 +892,7 @@ hipError_t launch_route_backward(int64_t T, int E, int k, const void* logits, in
   a.rows = rows < 64 / sl ? rows : 64 / sl;
   constexpr int WPB = kRouteThreads / 64;
   const size_t lds = (size_t)WPB * a.rows * a.pitch * 4;
+  // (two rows a wavefront at least: 2^31 threads for 2^26 tokens)
   const unsigned grid = (unsigned)((T + (int64_t)a.rows * WPB - 1) / ((int64_t)a.rows * WPB));
   if (sl == 8) hipLaunchKernelGGL((route_back_kernel<8>), dim3(grid), dim3(kRouteThreads), lds, s, a);
   else hipLaunchKernelGGL((route_back_kernel<32>), dim3(grid), dim3(kRouteThreads), lds, s, a);
