@@ -232,16 +232,10 @@ def moe_scale(shape: Shape, plan_ws, recv_self, topk_w, out, stream=None) -> Non
                           _stream(stream)), "moe_scale")
 
 
-def moe_scale_backward(shape: Shape, plan_ws, recv_self, topk_w, d_out, d_recv=None, d_topk_w=None,
-                       stream=None) -> None:
-    _check(_lib.moe_scale_backward(shape.ptr, _ptr(plan_ws), _ptr(recv_self), _ptr(topk_w), _ptr(d_out),
-                                   _ptr(d_recv), _ptr(d_topk_w), _stream(stream)), "moe_scale_backward")
-
-
-# --- routing and the dense product -------------------------------------------
-# These take their sizes, types and row pitches from the tensors, so the
-# tensors are checked here; they run on the tensors' device (on its current
-# stream unless one is given).
+# --- routing, the dense product and the gradients ------------------------------
+# The tensors of these calls are checked here (most of them take their sizes,
+# types and row pitches from them); they run on the tensors' device (on its
+# current stream unless one is given).
 
 def _invalid(where: str, what: str):
     err = MoEError(MOE_EINVAL, where)
@@ -292,6 +286,51 @@ def _launch(where, index, stream, fn, *args) -> None:
             rc = fn(*args, _stream(stream))
     if rc != MOE_OK:
         raise MoEError(rc, where)
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_F32 = (torch.float32,)
+
+
+def _rows(where, name, t, rows, cols, dtypes, index):
+    """Checks a contiguous tensor of at least that many rows (None and plain
+    addresses pass); returns its address."""
+    if t is None or isinstance(t, int):
+        return t
+    shape = t.shape
+    if (t.dtype not in dtypes or len(shape) != 2 or shape[1] != cols or shape[0] < rows or t.get_device() != index or
+            not t.is_contiguous()):
+        raise _mismatch(where, name, t, (rows, cols), dtypes[0], index, "contiguous")
+    return t.data_ptr()
+
+
+def moe_scale_backward(shape: Shape, plan_ws, recv_self, topk_w, d_out, d_recv=None, d_topk_w=None,
+                       stream=None) -> None:
+    """Gradients of moe_scale from d_out [T_r, d]: d_recv [T_r*k, d] (bf16, as
+    recv_self and d_out) and d_topk_w float32 [T_r, k]; tensors may have more
+    rows, which stay as they are.  See include/moe.h."""
+    where = "moe_scale_backward"
+    c = shape.c
+    d, k, r = c.hidden, c.top_k, c.rank
+    tokens = shape.tokens
+    T = tokens[r] if 0 <= r < len(tokens) else 0   # a bad shape is the library's to refuse
+    index = None
+    for t in (d_out, plan_ws, recv_self, topk_w, d_recv, d_topk_w):
+        if isinstance(t, torch.Tensor):
+            index = t.get_device()
+            break
+    if isinstance(plan_ws, torch.Tensor):
+        if plan_ws.get_device() != index or not plan_ws.is_contiguous():
+            raise _invalid(where, "plan_ws is not a contiguous tensor on the others' device")
+        plan_ws = plan_ws.data_ptr()
+    args = (ctypes.byref(c), plan_ws, _rows(where, "recv_self", recv_self, T * k, d, _BF16, index),
+            _rows(where, "topk_w", topk_w, T, k, _F32, index), _rows(where, "d_out", d_out, T, d, _BF16, index),
+            _rows(where, "d_recv", d_recv, T * k, d, _BF16, index),
+            _rows(where, "d_topk_w", d_topk_w, T, k, _F32, index))
+    if index is None:   # addresses alone: on the current device
+        _check(_lib.moe_scale_backward(*args, _stream(stream)), where)
+    else:
+        _launch(where, index, stream, _lib.moe_scale_backward, *args)
 
 
 # the library only reads options, so calls with the same ones share them

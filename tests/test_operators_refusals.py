@@ -1,0 +1,57 @@
+"""More refusals of the operators' binding, without a GPU: what a tensor's
+shape, type, layout or place shows to be wrong is an error before any call."""
+import os
+
+import pytest
+import torch
+
+LIB = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "moe_expert_tile_amd", "libmoe.so")
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libmoe.so not built")
+
+
+def _m():
+    import moe_expert_tile_amd as m
+    return m
+
+
+def _scale_args(m, T=6, k=2, d=256):
+    s = m.Shape(1, 0, 4, k, d, 128, 32, [T], T * k)
+    plan = torch.zeros(m.moe_query_sizes(s)["plan_bytes"] // 4, dtype=torch.int32)
+    bf = torch.bfloat16
+    return s, dict(plan_ws=plan, recv_self=torch.zeros(T * k, d, dtype=bf), topk_w=torch.zeros(T, k),
+                   d_out=torch.zeros(T, d, dtype=bf), d_recv=torch.zeros(T * k, d, dtype=bf),
+                   d_topk_w=torch.zeros(T, k))
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("d_out", lambda t: t[:1].expand(6, 256)),           # the gradient of a sum
+    ("d_out", lambda t: t.t().contiguous().t()), ("d_out", lambda t: t.float()), ("d_out", lambda t: t.half()),
+    ("d_out", lambda t: t[:5]), ("d_out", lambda t: t[:, :128].contiguous()), ("d_out", lambda t: t.view(-1)),
+    ("recv_self", lambda t: t[:11]), ("recv_self", lambda t: t[:, ::2]), ("recv_self", lambda t: t.float()),
+    ("topk_w", lambda t: t.double()), ("topk_w", lambda t: t.bfloat16()), ("topk_w", lambda t: t.t().contiguous().t()),
+    ("topk_w", lambda t: t[:5]), ("topk_w", lambda t: t[:, :1].contiguous()),
+    ("d_recv", lambda t: t[:11]), ("d_recv", lambda t: t.float()), ("d_recv", lambda t: t.view(6, 512)),
+    ("d_recv", lambda t: t[:1].expand(12, 256)),
+    ("d_topk_w", lambda t: t.bfloat16()), ("d_topk_w", lambda t: t[:5]), ("d_topk_w", lambda t: t[:1].expand(6, 2)),
+    ("plan_ws", lambda t: t[::2]),
+])
+def test_bad_scale_backward_tensors_are_rejected(name, bad):
+    m = _m()
+    s, a = _scale_args(m)
+    a[name] = bad(a[name])
+    with pytest.raises(m.MoEError, match=name) as ei:
+        m.moe_scale_backward(s, **a)
+    assert ei.value.status == m.MOE_EINVAL
+
+
+def test_scale_backward_on_the_cpu_is_rejected():
+    """Sound tensors but for their place; more rows than needed are sound."""
+    m = _m()
+    s, a = _scale_args(m)
+    a["d_out"] = torch.zeros(7, 256, dtype=torch.bfloat16)
+    a["d_recv"] = torch.zeros(20, 256, dtype=torch.int16)
+    with pytest.raises(m.MoEError, match="not on a GPU"):
+        m.moe_scale_backward(s, **a)
+    bad = m.Shape(1, 3, 4, 2, 256, 128, 32, [6], 12)
+    with pytest.raises(m.MoEError):
+        m.moe_scale_backward(bad, **a)
