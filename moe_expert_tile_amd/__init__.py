@@ -275,10 +275,18 @@ def _packed(where, name, t, shape, dtype, index) -> Optional[int]:
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _launch(where, index, stream, fn, *args) -> None:
-    """fn(*args, raw stream) with GPU `index` current; raises its errors."""
+def _place(where, index, stream) -> None:
+    """Refuses tensors that are on no GPU, and a stream of another one."""
     if index < 0:
         raise _invalid(where, "the tensors are not on a GPU")
+    if stream is not None and getattr(stream, "device_index", index) != index:
+        raise _invalid(where, f"the stream is on GPU {stream.device_index}, the tensors are on GPU {index}")
+
+
+def _launch(where, index, stream, fn, *args) -> None:
+    """fn(*args, raw stream) with GPU `index` current; raises its errors."""
+    if index < 0 or stream is not None:
+        _place(where, index, stream)
     if _current_device() == index:
         rc = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
@@ -419,6 +427,7 @@ def _workspace(where, ws, need, x, stream):
     if need == 0:
         return None
     if stream is not None:
+        _place(where, x.get_device(), stream)
         raw = _stream(stream)
         if raw != _raw_stream(x.device.index):
             own = torch.cuda.ExternalStream(raw, device=x.device) if raw else torch.cuda.default_stream(x.device)

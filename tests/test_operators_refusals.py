@@ -55,3 +55,41 @@ def test_scale_backward_on_the_cpu_is_rejected():
     bad = m.Shape(1, 3, 4, 2, 256, 128, 32, [6], 12)
     with pytest.raises(m.MoEError):
         m.moe_scale_backward(bad, **a)
+
+
+@pytest.mark.parametrize("stream", [None, 0, 1 << 20])
+def test_tensors_on_the_cpu_are_rejected_whatever_the_stream(stream):
+    m = _m()
+    bf = torch.bfloat16
+    x, w, out = torch.zeros(128, 8192, dtype=bf), torch.zeros(64, 8192, dtype=bf), torch.zeros(128, 64, dtype=bf)
+    z, ids, wt = torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for call in (lambda: m.moe_linear(x, w, out, stream=stream),        # (a size that needs a workspace)
+                 lambda: m.moe_linear_backward(x, w, out, dx=torch.zeros_like(x), stream=stream),
+                 lambda: m.moe_route(z, ids, wt, stream=stream),
+                 lambda: m.moe_route_backward(z, ids, wt, wt, torch.zeros_like(z), stream=stream)):
+        with pytest.raises(m.MoEError, match="not on a GPU") as ei:
+            call()
+        assert ei.value.status == m.MOE_EINVAL
+
+
+@pytest.mark.gpu
+def test_a_stream_of_another_gpu_is_rejected():
+    import types
+    m = _m()
+    bf = torch.bfloat16
+    other = types.SimpleNamespace(cuda_stream=torch.cuda.current_stream().cuda_stream, device_index=1)
+    s, a = _scale_args(m)
+    a = {k: v.cuda() for k, v in a.items()}
+    x, w, out = (torch.zeros(*n, dtype=bf, device="cuda") for n in ((128, 8192), (64, 8192), (128, 64)))
+    z, wt = torch.zeros(4, 16, device="cuda"), torch.zeros(4, 2, device="cuda")
+    ids = torch.full((4, 2), 3, dtype=torch.int32, device="cuda")
+    for call in (lambda: m.moe_linear(x, w, out, stream=other),
+                 lambda: m.moe_linear_backward(x, w, out, dx=torch.zeros_like(x), stream=other),
+                 lambda: m.moe_route(z, ids, wt, stream=other),
+                 lambda: m.moe_route_backward(z, ids, wt, wt, torch.zeros_like(z), stream=other),
+                 lambda: m.moe_scale_backward(s, **a, stream=other)):
+        with pytest.raises(m.MoEError, match="GPU 1") as ei:
+            call()
+        assert ei.value.status == m.MOE_EINVAL
+    torch.cuda.synchronize()
+    assert bool((ids == 3).all())
