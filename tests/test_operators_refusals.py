@@ -93,3 +93,15 @@ def test_a_stream_of_another_gpu_is_rejected():
         assert ei.value.status == m.MOE_EINVAL
     torch.cuda.synchronize()
     assert bool((ids == 3).all())
+
+
+def test_a_scale_of_zero_is_rejected():
+    """In the C options 0 stands for 1; a number given to the binding is meant."""
+    m = _m()
+    z, ids, w = torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for scale in (0, 0.0, -0.0):
+        with pytest.raises(m.MoEError, match="scale is 0") as ei:
+            m.moe_route(z, ids, w, scale=scale)
+        assert ei.value.status == m.MOE_EINVAL
+        with pytest.raises(m.MoEError, match="scale is 0"):
+            m.moe_route_backward(z, ids, w, w, torch.zeros_like(z), scale=scale)
