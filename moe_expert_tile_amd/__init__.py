@@ -344,7 +344,7 @@ def moe_scale_backward(shape: Shape, plan_ws, recv_self, topk_w, d_out, d_recv=N
 # the library only reads options, so calls with the same ones share them
 @functools.lru_cache(maxsize=256)
 def _route_opts(score, renorm, n_group, topk_group, group_score, scale):
-    if scale == 0:   # the C options' default, 1, is not what a caller who computed 0 means
+    if ctypes.c_float(scale).value == 0:   # the C options' default, 1, is not what a caller who computed 0 means
         raise _invalid("moe_route_opts", "scale is 0, not finite and above 0")
     return moe_route_opts(score, 1 if renorm else 0, n_group, topk_group, group_score, scale)
 

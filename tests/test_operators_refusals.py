@@ -105,3 +105,10 @@ def test_a_scale_of_zero_is_rejected():
         assert ei.value.status == m.MOE_EINVAL
         with pytest.raises(m.MoEError, match="scale is 0"):
             m.moe_route_backward(z, ids, w, w, torch.zeros_like(z), scale=scale)
+
+
+def test_a_scale_below_the_smallest_float_is_rejected():
+    m = _m()
+    z, ids, w = torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    with pytest.raises(m.MoEError, match="scale is 0"):
+        m.moe_route(z, ids, w, scale=1e-50)
