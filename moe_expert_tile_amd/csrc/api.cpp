@@ -7,7 +7,7 @@
 #include <string.h>
 
 #include "moe.h"
-#include "moe_internal.h"
+#include "layer_internal.h"
 
 namespace moe {
 

@@ -7,13 +7,12 @@
 #include <string.h>
 
 #include "moe.h"
-#include "moe_internal.h"
+#include "layer_internal.h"
 
 using namespace moe;
 
 namespace {
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int hip_rc(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 size_t item(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 
@@ -27,7 +26,7 @@ int check_route(int64_t tokens, int32_t experts, int32_t top_k, const void* logi
   if (dtype < MOE_BF16 || dtype > MOE_F32) return MOE_EINVAL;
   if (*ld == 0) *ld = experts;
   if (*ld < experts || *ld > kMaxPitch) return MOE_EINVAL;
-  if (!aligned(logits, item(dtype))) return MOE_EINVAL;
+  if (!aligned_to(logits, item(dtype))) return MOE_EINVAL;
   memset(o, 0, sizeof(*o));
   if (opts) *o = *opts;
   if (o->score != MOE_SCORE_SOFTMAX && o->score != MOE_SCORE_SIGMOID) return MOE_EINVAL;
@@ -80,7 +79,7 @@ int moe_route(int64_t tokens, int32_t experts, int32_t top_k, const void* logits
   int rc = check_route(tokens, experts, top_k, logits, dtype, &ld, opts, &o);
   if (!rc) rc = check_groups(experts, top_k, &o);
   if (rc) return rc;
-  if (!aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4)) return MOE_EINVAL;
+  if (!aligned_to(bias, 4) || !aligned_to(topk_ids, 4) || !aligned_to(topk_w, 4)) return MOE_EINVAL;
   if (tokens > 0 && (!logits || !topk_ids || !topk_w)) return MOE_EINVAL;
   rc = prepare_device();
   if (rc || tokens == 0) return rc;
@@ -95,7 +94,8 @@ int moe_route_backward(int64_t tokens, int32_t experts, int32_t top_k, const voi
   if (rc) return rc;
   if (ld_d == 0) ld_d = experts;
   if (ld_d < experts || ld_d > kMaxPitch) return MOE_EINVAL;
-  if (!aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(d_topk_w, 4) || !aligned(d_logits, item(dtype)))
+  if (!aligned_to(topk_ids, 4) || !aligned_to(topk_w, 4) || !aligned_to(d_topk_w, 4) ||
+      !aligned_to(d_logits, item(dtype)))
     return MOE_EINVAL;
   if (tokens > 0 && (!logits || !topk_ids || !topk_w || !d_topk_w || !d_logits)) return MOE_EINVAL;
   rc = prepare_device();
@@ -119,8 +119,8 @@ int moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const 
   int rc = check_linear(desc, &d);
   if (rc) return rc;
   const size_t o = item(d.out_dtype);
-  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 2) || !aligned(residual, o) || !aligned(pre, 2) ||
-      !aligned(out, o) || !aligned(ws, 256))
+  if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(bias, 2) || !aligned_to(residual, o) ||
+      !aligned_to(pre, 2) || !aligned_to(out, o) || !aligned_to(ws, 256))
     return MOE_EINVAL;
   if (d.rows > 0 && (!x || !w || !out)) return MOE_EINVAL;
   if (residual && residual == out && d.ld_residual != d.ld_out) return MOE_EINVAL;
@@ -137,8 +137,8 @@ int moe_linear_backward(const moe_linear_desc* desc, const void* x, const void* 
   int rc = check_linear(desc, &d);
   if (rc) return rc;
   if (!dx && !dw && !dbias) return MOE_EINVAL;
-  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(pre, 2) || !aligned(d_out, item(d.out_dtype)) ||
-      !aligned(dx, 2) || !aligned(dw, 2) || !aligned(dbias, 2) || !ws || !aligned(ws, 256))
+  if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(pre, 2) || !aligned_to(d_out, item(d.out_dtype)) ||
+      !aligned_to(dx, 2) || !aligned_to(dw, 2) || !aligned_to(dbias, 2) || !ws || !aligned_to(ws, 256))
     return MOE_EINVAL;
   if (d.rows > 0 && (!d_out || (dw && !x) || (dx && !w) || (d.act != MOE_ACT_NONE && !pre))) return MOE_EINVAL;
   rc = prepare_device();

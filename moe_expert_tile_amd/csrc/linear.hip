@@ -26,7 +26,7 @@
 // Without an activation dz is d_out itself where its type and layout allow.
 #include <type_traits>
 
-#include "moe_internal.h"
+#include "layer_internal.h"
 
 namespace moe {
 namespace {
@@ -38,8 +38,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-constexpr int kBufWord3 = 0x00020000;        // raw buffer access: data format 32, other fields zero
-constexpr uint32_t kPastEnd = 0x80000000u;   // beyond every descriptor's extent (all below 2^31 bytes)
 constexpr int kCus = 256;                    // compute units the work is split for
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
@@ -873,7 +871,6 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float* sums, int r
 // --- host -------------------------------------------------------------------
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // How a product is cut: tile 0 = few rows, 1 = 64 x 128, 2 = 128 x 128,
 // 3 = 256 x 256, 4 = 128 x 256 (a gated product's columns count twice), and the

@@ -258,35 +258,6 @@ hipError_t launch_consumer_rows(const PlanLayout& L, int32_t* ws, const uint16_t
                                 uint32_t epoch, const RecvPtrs& recv, int64_t timeout_ticks, hipStream_t s);
 hipError_t launch_scale(const PlanLayout& L, const int32_t* ws, const uint16_t* recv_self,
                         const float* topk_w, uint16_t* out, hipStream_t s);
-hipError_t launch_scale_backward(const PlanLayout& L, const int32_t* ws, const uint16_t* recv_self,
-                                 const float* topk_w, const uint16_t* d_out, uint16_t* d_recv, float* d_topk_w,
-                                 hipStream_t s);
-
-// routing (route.hip); `o` has its defaults filled in
-hipError_t launch_route(int64_t T, int E, int k, const void* logits, int dtype, int64_t ld, const float* bias,
-                        const moe_route_opts& o, int32_t* ids, float* w, hipStream_t s);
-hipError_t launch_route_backward(int64_t T, int E, int k, const void* logits, int dtype, int64_t ld,
-                                 const int32_t* ids, const float* w, const float* dw, const moe_route_opts& o,
-                                 void* dz, int64_t ldd, hipStream_t s);
-
-// dense product (linear.hip); `d` has its row pitches filled in
-struct LinearBuffers {
-  const void *x, *w, *bias, *residual;
-  void *pre, *out;
-};
-struct LinearGrads {
-  const void *x, *w, *pre, *d_out;
-  void *dx, *dw, *dbias;
-};
-// workspace bytes of the forward product, and of the backward pass that
-// computes all of its gradients
-size_t linear_ws_bytes(const moe_linear_desc& d);
-size_t linear_back_ws_bytes(const moe_linear_desc& d);
-hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void* ws, hipStream_t s);
-hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b, void* ws, hipStream_t s);
-
-// the current device, checked to be a gfx950 (api.cpp); a moe_status
-int prepare_device();
 
 // device helpers ------------------------------------------------------------
 #if defined(__HIPCC__)

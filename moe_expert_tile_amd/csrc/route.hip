@@ -29,7 +29,7 @@
 // a launch and the picks' latency.
 #include <type_traits>
 
-#include "moe_internal.h"
+#include "layer_internal.h"
 
 namespace moe {
 namespace {
@@ -44,9 +44,6 @@ __device__ __forceinline__ float load_as_float(const void* p, int dtype, int64_t
   if (dtype == MOE_BF16) return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
   return (float)((const _Float16*)p)[i];
 }
-
-constexpr int kBufWord3 = 0x00020000;        // raw buffer access: data format 32, other fields zero
-constexpr uint32_t kPastEnd = 0x80000000u;   // past every descriptor's extent: loads there return zeros
 
 // VPL values of a row into z: place i at byte offset row_off + item * (chunk
 // i / 4 of this lane, `step` values apart); places from cnt on are -inf.  All
@@ -804,8 +801,6 @@ __global__ __launch_bounds__(kRouteThreads) void route_back_kernel(RouteBackArgs
     for (int e = j; e < a.E; e += SL) store_as(a.dz, a.dtype, to + e, from[e]);
   }
 }
-
-bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // Workgroups of one launch: a launch's threads are counted in 32 bits, and 64
 // lanes a row make 2^32 of them for the 2^26 tokens a call may have, so such a

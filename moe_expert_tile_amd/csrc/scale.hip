@@ -10,13 +10,12 @@
 // once, mostly from HBM, with nontemporal loads: measured 4-9% faster in the
 // step and 3-8% with a cold Infinity Cache, though 10% slower when the rows
 // are still in that cache.
-#include "moe_internal.h"
+#include "layer_internal.h"
 
 namespace moe {
 namespace {
 
 typedef unsigned int v4u32 __attribute__((ext_vector_type(4)));
-constexpr int kBufWord3 = 0x00020000;   // raw buffer access: data format 32, other fields zero
 constexpr int kNontemporal = 2;         // nt cache-policy bit
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
