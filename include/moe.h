@@ -408,7 +408,9 @@ int moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const 
  * moe_linear_backward — with dz = d_out * act'(pre) (SWIGLU: for both halves):
  *   dx = dz w,  dw = dz^T x,  dbias = column sums of dz.
  * dz is rounded to dtype before the two products (their operands are 16-bit),
- * not for dbias; sums are fp32, rounded once.  The residual's gradient is d_out.
+ * not for dbias; sums are fp32, rounded once.  In fp16 it is scaled by a power
+ * of two around that, so that only values below 2^-39 of its largest one
+ * vanish.  The residual's gradient is d_out.
  *   d_out   device [rows, cols] of out_dtype.
  *   pre     device [rows, n]; not read without an activation (may be NULL then).
  *   dx      device [rows, depth], dw device [n, depth], dbias device [n]: any may be NULL, not all.

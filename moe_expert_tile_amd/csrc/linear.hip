@@ -24,6 +24,11 @@
 // which the matrix cores need; its column sums for the bias are taken before
 // the rounding), then dx = dz w and dw = dz^T x are products of the same form.
 // Without an activation dz is d_out itself where its type and layout allow.
+// Fp16's range is narrow for that (gradients of a mean over many tokens lie
+// below its smallest step): a dz rounded to fp16 is multiplied by the power of two
+// that brings its largest value to 2^14 .. 2^15, found in a pass of its own, and the
+// products' sums by its inverse.  A rounding is then off by half a step, 2^-11 of
+// the value, or 2^-39 of the largest one, whichever is more.
 #include <type_traits>
 
 #include "layer_internal.h"
@@ -131,6 +136,7 @@ struct Epilogue {
   int N;         // output columns; a gated product has N gate and N up columns before the activation
   int act;
   int out_f32;
+  const float* scale;   // a factor on the sums of a gradient's product, in device memory, or null
 };
 
 // Whole accesses at any alignment of the element type (rows of odd lengths
@@ -564,6 +570,8 @@ void product_kernel(ProdArgs g) {
   // neither activation nor pre: short enough to unroll over the passes
   const bool light = !GATED && !g.e.pre && g.e.act == MOE_ACT_NONE;
   // gradients and most products: 16-bit sums alone, whole 8 columns
+  constexpr bool SCALES = F16 && BX;   // gradients' products in fp16 alone
+  const float factor = SCALES && g.e.scale ? *g.e.scale : 1.0f;
   const bool plain = light && !g.e.bias && !g.e.res && !g.e.out_f32 && g.e.N % 8 == 0;
   float bz[8], bu[8];
   if constexpr (!PART) load_bias<F16, GATED>(g.e, n, bz, bu);
@@ -605,6 +613,10 @@ void product_kernel(ProdArgs g) {
         const int64_t m = mj + r;
         float z[8];
         staged8(r, ec, z);
+        if constexpr (SCALES) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) z[c] *= factor;
+        }
         if (m < g.e.M && n < g.e.N) store16<F16, 8, true>((uint16_t*)g.e.out + m * g.e.ldo + n, 8, z);
       }
     } else if (light) {
@@ -618,7 +630,7 @@ void product_kernel(ProdArgs g) {
         float z[8];
         staged8(r, ec, z);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) z[c] += bz[c] + res[p][c];
+        for (int c = 0; c < 8; ++c) z[c] = (SCALES ? z[c] * factor : z[c]) + (bz[c] + res[p][c]);
         if (m < g.e.M && n < g.e.N) store_out<F16>(g.e, m, n, z);
       }
     } else {
@@ -668,6 +680,12 @@ __global__ __launch_bounds__(64) void join_kernel(ProdArgs g) {
       if constexpr (GATED) {
         const float4 y = *(const float4*)(p + g.up_col);
         u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+      }
+    }
+    if constexpr (F16 && !GATED) {
+      if (g.e.scale) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) z[c] *= *g.e.scale;
       }
     }
     float bz[4], bu[4], r[4];
@@ -771,14 +789,88 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(ProdArgs g) {
 
 // --- gradients: dz --------------------------------------------------------------
 
+constexpr int kRangeBlocks = 1024;
+
 struct DzArgs {
   const void* d_out;      // [M, N]
   const uint16_t* pre;    // [M, N or 2N]
   uint16_t* dz;           // [M, ldz] or null
   float* sums;            // [ceil(M / 64)][N or 2N] column sums of 64 rows each, or null
+  float* range;           // [kRangeBlocks + 1] or null: largest finite |dz| of range_n workgroups; at kRangeBlocks
+                          // the inverse of dz's factor
   int64_t M, ldd, ldp, ldz;
-  int N, act, d_f32;
+  int N, act, d_f32, range_n;
 };
+
+// dz of row m, columns n .. n + 7 (and the up columns' in the last half), zeros from `left` on
+template <bool F16, int ACT, int HALVES>
+__device__ __forceinline__ void form_dz(const DzArgs& a, int64_t m, int n, int left, float (&d)[HALVES][8]) {
+  constexpr bool GATED = ACT == MOE_ACT_SWIGLU;
+  float g[8] = {}, p[8] = {}, u[8] = {};
+  if (left > 0) {
+    if (a.d_f32) load32((const float*)a.d_out + m * a.ldd + n, left, g);
+    else load16<F16>((const uint16_t*)a.d_out + m * a.ldd + n, left, g);
+    if constexpr (ACT != MOE_ACT_NONE) load16<F16>(a.pre + m * a.ldp + n, left, p);
+    if constexpr (GATED) load16<F16>(a.pre + m * a.ldp + a.N + n, left, u);
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    if constexpr (GATED) {
+      d[0][c] = g[c] * u[c] * slope<MOE_ACT_SILU>(p[c]);
+      d[HALVES - 1][c] = g[c] * activate<MOE_ACT_SILU>(p[c]);
+    } else {
+      d[0][c] = ACT == MOE_ACT_NONE ? g[c] : g[c] * slope<ACT>(p[c]);
+    }
+  }
+}
+
+// the largest of a workgroup's values, to all of its 256 threads
+__device__ __forceinline__ float block_max(float v) {
+  __shared__ float wave_max[4];
+#pragma unroll
+  for (int s = 32; s; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
+  if (threadIdx.x % 64 == 0) wave_max[threadIdx.x / 64] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+}
+
+// The largest finite |dz| of each workgroup's 32 x 64 tiles, before an fp16 dz
+// is formed: one more reading of d_out and pre, at HBM's rate (8192 x 2 x 2048 gated
+// columns, 134 MB, 37 us of a backward pass's 955; 8192 x 256 from fp32 4.6 of 109).
+template <int ACT>
+__global__ __launch_bounds__(256) void dz_range_kernel(DzArgs a) {
+  constexpr int HALVES = ACT == MOE_ACT_SWIGLU ? 2 : 1;
+  const int tid = threadIdx.x, across = (a.N + 63) / 64;
+  const int64_t tiles = (a.M + 31) / 32 * across;
+  float top = 0.f;
+  for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+    const int64_t m = i / across * 32 + tid / 8;
+    const int n = (int)(i % across) * 64 + (tid % 8) * 8;
+    if (m >= a.M) continue;
+    float d[HALVES][8];
+    form_dz<true, ACT>(a, m, n, a.N - n, d);
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float v = fabsf(d[h][c]);
+        if (v < __builtin_inff()) top = fmaxf(top, v);
+      }
+  }
+  top = block_max(top);
+  if (tid == 0) a.range[blockIdx.x] = top;
+}
+
+// dz's factor from the workgroups' largest values: a power of two, at most
+// 2^126 so that its inverse is a normal number
+__device__ __forceinline__ float dz_factor(const DzArgs& a) {
+  float top = 0.f;
+  for (int i = threadIdx.x; i < a.range_n; i += 256) top = fmaxf(top, a.range[i]);
+  top = block_max(top);
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;   // top in [2^e, 2^(e + 1)), or below 2^-126
+  const int f = min(14 - e, 126);
+  return top > 0.f ? __uint_as_float((uint32_t)(f + 127) << 23) : 1.0f;
+}
 
 // A thread forms 8 columns of two rows, 8 threads a row of 64 columns, so that
 // each access covers whole lines; with SUMS the 64 x 64 columns of a workgroup
@@ -793,6 +885,13 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
   const int tid = threadIdx.x;
   const int n = (int)blockIdx.x * 64 + (tid % 8) * 8;
   const int left = a.N - n;
+  float factor = 1.0f;
+  if constexpr (F16) {
+    if (a.range) {
+      factor = dz_factor(a);
+      if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.range[kRangeBlocks] = 1.0f / factor;
+    }
+  }
   float part[HALVES][8];
 #pragma unroll
   for (int h = 0; h < HALVES; ++h)
@@ -802,26 +901,15 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
   for (int i = 0; i < 2; ++i) {
     const int64_t m = (int64_t)blockIdx.y * 64 + 32 * i + tid / 8;
     if (m >= a.M) continue;
-    float g[8] = {}, p[8] = {}, u[8] = {}, d[HALVES][8];
-    if (left > 0) {
-      if (a.d_f32) load32((const float*)a.d_out + m * a.ldd + n, left, g);
-      else load16<F16>((const uint16_t*)a.d_out + m * a.ldd + n, left, g);
-      if constexpr (ACT != MOE_ACT_NONE) load16<F16>(a.pre + m * a.ldp + n, left, p);
-      if constexpr (GATED) load16<F16>(a.pre + m * a.ldp + a.N + n, left, u);
-    }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if constexpr (GATED) {
-        d[0][c] = g[c] * u[c] * slope<MOE_ACT_SILU>(p[c]);
-        d[HALVES - 1][c] = g[c] * activate<MOE_ACT_SILU>(p[c]);
-      } else {
-        d[0][c] = ACT == MOE_ACT_NONE ? g[c] : g[c] * slope<ACT>(p[c]);
-      }
-    }
+    float d[HALVES][8];
+    form_dz<F16, ACT>(a, m, n, left, d);
 #pragma unroll
     for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) part[h][c] += d[h][c];
+      for (int c = 0; c < 8; ++c) {
+        part[h][c] += d[h][c];
+        if constexpr (F16) d[h][c] *= factor;
+      }
     if (a.dz) {
       // the last half also writes the zeros behind it
       uint16_t* z = a.dz + m * a.ldz + n;
@@ -944,6 +1032,8 @@ size_t part_bytes(const Cut& c, int64_t M, int64_t N, bool gated) {
 
 template <bool F16, int ACT>
 void launch_dz_act(const DzArgs& a, const dim3& grid, hipStream_t s) {
+  if constexpr (F16)
+    if (a.range) hipLaunchKernelGGL((dz_range_kernel<ACT>), dim3((unsigned)a.range_n), dim3(256), 0, s, a);
   if (a.sums) hipLaunchKernelGGL((dz_kernel<F16, ACT, true>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((dz_kernel<F16, ACT, false>), grid, dim3(256), 0, s, a);
 }
@@ -1031,7 +1121,8 @@ bool gated(const moe_linear_desc& d) { return d.act == MOE_ACT_SWIGLU; }
 struct BackLayout {
   int64_t NZ, ldz, sums_rows;
   Cut dx, dw;
-  size_t dz, sums, part, total;
+  bool scaled;   // dz is rounded to fp16 (without an activation a 16-bit d_out is copied at most)
+  size_t dz, sums, part, range, total;
 };
 BackLayout back_layout(const moe_linear_desc& d) {
   BackLayout L;
@@ -1050,6 +1141,8 @@ BackLayout back_layout(const moe_linear_desc& d) {
   L.sums = take((size_t)L.sums_rows * L.NZ * 4);
   const size_t p1 = part_bytes(L.dx, d.rows, d.depth, false), p2 = part_bytes(L.dw, L.NZ, d.depth, false);
   L.part = take(p1 > p2 ? p1 : p2);
+  L.scaled = d.dtype == MOE_F16 && (d.act != MOE_ACT_NONE || d.out_dtype == MOE_F32);
+  L.range = take(L.scaled ? (kRangeBlocks + 1) * sizeof(float) : 0);
   L.total = off > 256 ? off : 256;
   return L;
 }
@@ -1078,6 +1171,7 @@ hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void*
   e.ldr = d.ld_residual; e.ldp = d.ld_pre; e.ldo = d.ld_out;
   e.act = d.act;
   e.out_f32 = d.out_dtype == MOE_F32;
+  e.scale = nullptr;
   const Cut c = choose_cut(d.rows, d.cols, d.depth, gated(d), false);
   if (d.dtype == MOE_F16)
     return gated(d) ? launch_product<true, true, false, false>(g, c, ws, s) : launch_product<true, false, false, false>(g, c, ws, s);
@@ -1092,6 +1186,7 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
   // without an activation the incoming gradient can be the operand itself
   const bool direct = d.act == MOE_ACT_NONE && !f32 && d.cols % 8 == 0 && d.ld_out % 8 == 0 && aligned_to(b.d_out, 16);
   const bool want_dz = (b.dx || b.dw) && !direct;
+  float* range = L.scaled && want_dz && d.rows > 0 ? (float*)(base + L.range) : nullptr;
   if (d.rows > 0 && (want_dz || b.dbias)) {
     DzArgs a;
     a.d_out = b.d_out;
@@ -1102,6 +1197,9 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
     a.ldd = d.ld_out; a.ldp = d.ld_pre; a.ldz = L.ldz;
     a.act = d.act;
     a.d_f32 = f32;
+    a.range = range;
+    const int64_t tiles = (d.rows + 31) / 32 * ((d.cols + 63) / 64);
+    a.range_n = (int)(tiles < kRangeBlocks ? tiles : kRangeBlocks);
     if (f16) launch_dz<true>(a, s);
     else launch_dz<false>(a, s);
   }
@@ -1119,6 +1217,7 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b
   e.ldr = e.ldp = 0;
   e.act = MOE_ACT_NONE;
   e.out_f32 = 0;
+  e.scale = range ? range + kRangeBlocks : nullptr;
   e.N = d.depth;
   g.a = direct ? (const uint16_t*)b.d_out : dz;
   g.lda = direct ? d.ld_out : L.ldz;
