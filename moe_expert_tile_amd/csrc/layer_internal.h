@@ -34,6 +34,9 @@ struct LinearGrads {
 // computes all of its gradients
 size_t linear_ws_bytes(const moe_linear_desc& d);
 size_t linear_back_ws_bytes(const moe_linear_desc& d);
+// for tests: tile (0 few rows, 1 64 x 128, 2 128 x 128, 3 256 x 256, 4 128 x 256) and splits of K of the forward
+// product, of dx and of dw
+void linear_cuts(const moe_linear_desc& d, int32_t cuts[6]);
 hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void* ws, hipStream_t s);
 hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b, void* ws, hipStream_t s);
 

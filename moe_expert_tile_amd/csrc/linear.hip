@@ -1155,6 +1155,15 @@ size_t linear_ws_bytes(const moe_linear_desc& d) {
 
 size_t linear_back_ws_bytes(const moe_linear_desc& d) { return back_layout(d).total; }
 
+void linear_cuts(const moe_linear_desc& d, int32_t cuts[6]) {
+  const BackLayout L = back_layout(d);
+  const Cut all[3] = {choose_cut(d.rows, d.cols, d.depth, gated(d), false), L.dx, L.dw};
+  for (int i = 0; i < 3; ++i) {
+    cuts[2 * i] = all[i].tile;
+    cuts[2 * i + 1] = all[i].splits;
+  }
+}
+
 hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void* ws, hipStream_t s) {
   ProdArgs g;
   g.a = (const uint16_t*)b.x;

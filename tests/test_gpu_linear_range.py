@@ -13,6 +13,7 @@ import torch
 
 from gpu_helpers import say
 from oracle import linear as OL
+from test_gpu_linear import EACH_TILE
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +165,29 @@ def test_parts_and_replays():
         torch.cuda.synchronize()
         assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]), e
         _check(a, "swiglu", dict(_run(a, "swiglu"), dx=dx, dw=dw))
+
+
+@pytest.mark.parametrize("what,M,N,K", [c for c in EACH_TILE if c[0] in ("dx", "dw")])
+def test_every_tile_of_the_gradients(what, M, N, K):
+    """Each tile, whole and split: the factor is taken off in the tiles'
+    epilogue and in the join.  The reference is float64 on the GPU."""
+    m = _m()
+    say(f"[linear range] {what} {M}x{N}x{K}")
+    size = 2.0 ** -26
+    terms = M if what == "dw" else N
+    s = min(2.0 ** 12, 2.0 ** 4 / (size * terms))
+    a = _inputs(M, N, K, "none", F32, M + K, size, s, s)
+    g, x, w = a["d_out"].double(), a["x"].double(), a["w"].double()
+    # (all terms are positive: the sum of magnitudes is the sum)
+    if what == "dx":
+        got, ref = torch.empty_like(a["x"]), torch.mm(g, w)
+        m.moe_linear_backward(a["x"], a["w"], a["d_out"], dx=got)
+        tail = 2.0 ** -39 * g.max() * w.sum(0, keepdim=True)
+    else:
+        got, ref = torch.empty_like(a["w"]), torch.mm(g.t().contiguous(), x)
+        m.moe_linear_backward(a["x"], a["w"], a["d_out"], dw=got)
+        tail = 2.0 ** -39 * g.max() * x.sum(0, keepdim=True)
+    err = HALF * ref + tail + (terms + 64) * U * (1 + HALF) * ref
+    bound = err * (1 + HALF) + HALF * ref + 2.0 ** -25
+    assert bool(((got.double() - ref).abs() <= bound).all())
+    assert float(ref.max()) > 2.0 ** -14 and float(ref.max()) < 65504
