@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from operator import index as _int
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
@@ -341,12 +342,18 @@ def moe_scale_backward(shape: Shape, plan_ws, recv_self, topk_w, d_out, d_recv=N
         _launch(where, index, stream, _lib.moe_scale_backward, *args)
 
 
-# the library only reads options, so calls with the same ones share them
+# the library only reads options, so calls with the same ones share them (plain
+# numbers alone are keys: a tensor would be one by its identity)
 @functools.lru_cache(maxsize=256)
-def _route_opts(score, renorm, n_group, topk_group, group_score, scale):
+def _shared_route_opts(score, renorm, n_group, topk_group, group_score, scale):
     if ctypes.c_float(scale).value == 0:   # the C options' default, 1, is not what a caller who computed 0 means
         raise _invalid("moe_route_opts", "scale is 0, not finite and above 0")
-    return moe_route_opts(score, 1 if renorm else 0, n_group, topk_group, group_score, scale)
+    return moe_route_opts(score, renorm, n_group, topk_group, group_score, scale)
+
+
+def _route_opts(score, renorm, n_group, topk_group, group_score, scale):
+    return _shared_route_opts(_int(score), 1 if renorm else 0, _int(n_group), _int(topk_group), _int(group_score),
+                              float(scale))
 
 
 @functools.lru_cache(maxsize=4096)

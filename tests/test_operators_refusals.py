@@ -112,3 +112,22 @@ def test_a_scale_below_the_smallest_float_is_rejected():
     z, ids, w = torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
     with pytest.raises(m.MoEError, match="scale is 0"):
         m.moe_route(z, ids, w, scale=1e-50)
+
+
+@pytest.mark.gpu
+def test_a_scale_held_in_a_tensor_is_read_at_every_call():
+    m = _m()
+    z = torch.randn(64, 16, device="cuda")
+    ids, w = torch.empty(64, 2, dtype=torch.int32, device="cuda"), torch.empty(64, 2, device="cuda")
+    scale = torch.tensor(1.0)
+    m.moe_route(z, ids, w, scale=scale)
+    once = w.clone()
+    scale.fill_(2.0)
+    m.moe_route(z, ids, w, scale=scale)
+    assert torch.equal(w, 2 * once)
+    d, twice = torch.empty_like(z), torch.empty_like(z)
+    m.moe_route_backward(z, ids, w, torch.ones_like(w), d, scale=2.0)
+    m.moe_route_backward(z, ids, w, torch.ones_like(w), twice, scale=scale)
+    assert torch.equal(d, twice)
+    with pytest.raises(TypeError):
+        m.moe_route(z, ids, w, n_group=2.0)
