@@ -263,10 +263,10 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int n, floa
 
 // --- tiled product ----------------------------------------------------------
 //
-// Rates (bf16, 8192 rows): 8192 x 4096 (gated) x 7168 390 us, 1.23 PFLOP/s;
-// 8192 x 2048 x 7168 186 us, 1.29; its dx 225 us, 1.07, its dw 199 us, 1.21;
-// 8192 x 7168 x 2048 208 us, 1.16.  (The library's plain 8192 x 4096 x 7168: 307
-// us.)  Counters of the gated one: 1.86 GHz under load, MFMA busy 62% of the
+// Rates (bf16, 8192 rows, a call among others): 8192 x 4096 (gated) x 7168 387 us,
+// 1.24 PFLOP/s; 8192 x 2048 x 7168 190 us, 1.26; its dx 220 us, 1.09, its dw 202
+// us, 1.19; 8192 x 7168 x 2048 220 us, 1.10, with a residual 276.  (The library's
+// plain 8192 x 4096 x 7168: 359-370 us in the same run, 307 at best.)  Counters of the gated one: 1.86 GHz under load, MFMA busy 62% of the
 // time, LDS 24%, no bank conflicts, wavefronts waiting 36%: what is left is the
 // loads' latency per CU.  Other shapes measured: 256 x 256 as four wavefronts of
 // 128 x 128 5-10% slower; 256 x 128 with three stages, next to 128 x 256, 0.2% less
@@ -660,7 +660,7 @@ void product_kernel(ProdArgs g) {
 }
 
 // Sums of a split product's partial sums, in split order, and the epilogue.
-// Memory bound (8192 x 256 in 4 splits, 42 MB, 7 us) or, with little to write,
+// Memory bound (8192 x 256 in 4 splits, 42 MB, 8.4 us) or, with little to write,
 // bound by the partial sums' latency: four of them are read together and a
 // workgroup is one wavefront, so that small outputs spread over the CUs
 // (40 x 512 x 4096 in 16 splits 12.0 us with one after the other, 9.3 us so).
@@ -698,7 +698,7 @@ __global__ __launch_bounds__(64) void join_kernel(ProdArgs g) {
 // --- few rows ---------------------------------------------------------------
 //
 // Bound by reading the weights: one row through 7168 x 2048 (29 MB) takes 7.6
-// us, of which about 2.5 us any launch takes; 8 K steps' loads in flight a
+// us (9.1 with the weights in no cache), of which about 2.5 us any launch takes; 8 K steps' loads in flight a
 // wavefront instead of 4, all issued before the first is waited for, took it
 // there from 9.6 us.
 // A workgroup owns 16 output columns (PART: of one split of K); its wavefronts
@@ -876,7 +876,7 @@ __device__ __forceinline__ float dz_factor(const DzArgs& a) {
 // each access covers whole lines; with SUMS the 64 x 64 columns of a workgroup
 // are then added down in row order.  Columns past the last, up to ldz (a
 // multiple of 8), become zeros.  Memory bound: 8192 x 2 x 2048
-// gated columns, 168 MB, take 38 us, 4.4 TB/s.
+// gated columns, 168 MB, take 36 us, 4.7 TB/s.
 template <bool F16, int ACT, bool SUMS>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
   constexpr bool GATED = ACT == MOE_ACT_SWIGLU;

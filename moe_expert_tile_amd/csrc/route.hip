@@ -22,11 +22,13 @@
 // the whole wavefront.
 //
 // What bounds it: instructions.  32768 tokens x 256 experts (grouped sigmoid with
-// bias, fp32) take 28 us against 7 us for their bytes: about 1500 vector
+// bias, fp32) take 28 us (29-32 by the profiler) against 7 us for their bytes: about 1500 vector
 // instructions a wavefront of 4 tokens, a quarter of them the picks, a fifth
 // keys and sorting; the bound loads, keys and one-pass shape took it there from
-// 96 us.  A late row ranked in 64 bits adds about 4 us.  64 tokens take 3.6 us,
-// a launch and the picks' latency.
+// 96 us.  A late row ranked in 64 bits adds about 4 us; where every row is (scores
+// closer than the bound throughout: a peaked softmax's small ones, or sigmoids of
+// far negative logits, under equal biases) 32768 x 256 take 83-90 us, 109 in groups.
+// 64 tokens take 3.5 us, a launch and the picks' latency.
 #include <type_traits>
 
 #include "layer_internal.h"
@@ -638,8 +640,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 // the full softmax reads whole rows of logits; the others read k of them.
 // A wavefront builds its rows in LDS (zeros, then the k values, summed in slot
 // order where an expert is listed twice) and writes them out whole.  Bound by
-// those writes: 32768 x 256 fp32, 37 MB with the slots, take 9-11 us, 3.5-4
-// TB/s; 256 x 8 with the full softmax take 3.7 us, a launch.
+// those writes: 32768 x 256 fp32, 37 MB with the slots, take 10-11 us, 3.5
+// TB/s; with the full softmax, which reads as much again, 16.5 us, 4.3 TB/s (bf16
+// 11.5 us); 256 x 8 with the full softmax take 3.7 us, a launch.
 struct RouteBackArgs {
   const void* logits;
   const int32_t* ids;
@@ -848,8 +851,10 @@ hipError_t launch_route(int64_t T, int E, int k, const void* logits, int dtype, 
   // Lanes a row.  Fewer hold more values each: more sorting, but a pick's
   // exchanges serve more rows.  At most 16 values a lane, and at least 8 lanes
   // past 16 experts.  Over 65 to 128 experts 16 lanes are quicker for a short
-  // batch and 8 for a long one (128 experts, with bias: 64 tokens 4.8 and 6.4
-  // us, 32768 tokens 16.0 and 14.5 us); 32 lanes are slower for both (5.6 and
+  // batch and 8 for a long one (128 experts, without bias: 64 tokens 3.7 and 4.4
+  // us, 12288 5.6 and 6.1, 16384 6.4 and 6.3, 24576 8.3 and 7.4, 32768 10.0 and
+  // 8.6; with one 64 tokens 4.9 and 6.4 us, 12288 10.2 and 10.9, 16384 12.8 and
+  // 12.8, 24576 13.6 and 14.3, 32768 15.4 and 14.9); 32 lanes are slower for both (5.6 and
   // 35 us), and for 256 experts (5.7 and 36.5 us against 5.6 and 21.7 us with 16).
   auto places = [&](int lpr) { return (a.gsize + 4 * (lpr / gp) - 1) / (4 * (lpr / gp)) * 4; };
   int lpr = gp < 4 ? 4 : gp;
