@@ -421,6 +421,77 @@ int moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const 
 int moe_linear_backward(const moe_linear_desc* desc, const void* x, const void* w, const void* pre,
                         const void* d_out, void* dx, void* dw, void* dbias, void* ws, void* stream);
 
+/*
+ * Rows sorted by expert, without a plan: the tokens of one rank to its experts
+ * and back (moe_sort, moe_permute, the experts' products, moe_unpermute), for
+ * serving and, with the gradients, for training.
+ */
+
+/* Workspace bytes of moe_sort (may be 0).  Host only; no HIP call. */
+int moe_sort_sizes(int64_t tokens, int32_t top_k, int32_t experts, size_t* ws_bytes);
+
+/*
+ * moe_sort — the (token, slot) pairs of a batch in the order of their experts,
+ * pairs of one expert in the order of the batch (token, then slot).  The
+ * rank hosts experts first .. first + experts - 1; a pair with any other id
+ * has no row.
+ *   topk_ids  device int32 [tokens, top_k], e.g. from moe_route.
+ *   pos       device int32 [tokens, top_k]: the row of each pair, -1 if it has none.
+ *   src       device int32 [tokens * top_k] or NULL: the pair t * top_k + j of each row; from
+ *             offsets[experts] on it is left as it was.
+ *   offsets   device int32 [experts + 1]: rows offsets[e] .. offsets[e + 1] - 1 are expert first + e's.
+ *   ws        device workspace, 256-byte aligned, of moe_sort_sizes' bytes (NULL if that is 0); calls that
+ *             overlap on the device need one each.
+ * tokens <= 2^26, experts <= 1024, top_k <= 32, tokens * top_k < 2^31, first >= 0.
+ */
+int moe_sort(int64_t tokens, int32_t top_k, int32_t experts, int32_t first, const int32_t* topk_ids, int32_t* pos,
+             int32_t* src, int32_t* offsets, void* ws, void* stream);
+
+/* Sizes of the calls below.  Row pitches are in elements, at least cols, at
+ * most 2^21; 0 = packed.  Tensors are aligned to their elements. */
+typedef struct moe_rows_desc {
+  int64_t tokens;        /* of x, out, dx, d_out, pos; 0..2^26 */
+  int64_t rows;          /* of the sorted rows' buffers; 0..2^31 - 1 */
+  int32_t top_k;         /* 1..32 */
+  int32_t cols;          /* 1..2^20 */
+  int32_t dtype;         /* MOE_BF16, MOE_F16 or MOE_F32 */
+  int32_t pad;           /* zero */
+  int64_t ld_x;          /* of x, out, dx, d_out */
+  int64_t ld_rows;       /* of rows; of d_rows in moe_permute_backward */
+  int64_t ld_d_rows;     /* of d_rows in moe_unpermute_backward */
+} moe_rows_desc;
+
+/*
+ * moe_permute — rows[pos[t][j]] = x[t].  A slot whose pos is outside
+ * [0, rows) is left out, here and in the calls below; rows that no slot names
+ * stay as they were.  No two slots may name the same row.
+ */
+int moe_permute(const moe_rows_desc* desc, const void* x, const int32_t* pos, void* rows, void* stream);
+
+/* moe_permute_backward — dx[t] = sum_j d_rows[pos[t][j]], fp32 in slot order,
+ * rounded once; zeros for a token without a row.  All of dx is written. */
+int moe_permute_backward(const moe_rows_desc* desc, const void* d_rows, const int32_t* pos, void* dx, void* stream);
+
+/*
+ * moe_unpermute — out[t] = sum_j topk_w[t][j] rows[pos[t][j]], fp32 in slot
+ * order, rounded once; zeros for a token without a row.
+ *   topk_w   device float [tokens, top_k], or NULL: every weight is 1.
+ */
+int moe_unpermute(const moe_rows_desc* desc, const void* rows, const int32_t* pos, const float* topk_w, void* out,
+                  void* stream);
+
+/*
+ * moe_unpermute_backward — the gradient of moe_unpermute: with g = d_out,
+ *   d_rows[pos[t][j]] = topk_w[t][j] g[t],  d_topk_w[t][j] = sum_c g[t][c] rows[pos[t][j]][c]
+ * (fp32 sums; 0 for a slot without a row).  Rows of d_rows that no slot names
+ * stay as they were.
+ *   rows      as given to moe_unpermute; may be NULL when d_topk_w is.
+ *   topk_w    NULL: every weight is 1.
+ *   d_rows, d_topk_w   no overlap with the inputs; either may be NULL, not both.
+ */
+int moe_unpermute_backward(const moe_rows_desc* desc, const void* rows, const int32_t* pos, const float* topk_w,
+                           const void* d_out, void* d_rows, float* d_topk_w, void* stream);
+
 /* Synchronises `stream`, then returns the device error word of the plan
  * (MOE_OK, MOE_ETIMEOUT or MOE_EROUTING), or MOE_EHIP. */
 int moe_device_status(const void* plan_ws, void* stream);

@@ -83,6 +83,12 @@ class moe_linear_desc(ctypes.Structure):
                 ("ld_dx", ctypes.c_int64), ("ld_dw", ctypes.c_int64)]
 
 
+class moe_rows_desc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32), ("pad", ctypes.c_int32),
+                ("ld_x", ctypes.c_int64), ("ld_rows", ctypes.c_int64), ("ld_d_rows", ctypes.c_int64)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -113,6 +119,12 @@ def _load():
         "moe_linear_sizes": (I, [P(moe_linear_desc), P(ctypes.c_size_t), P(ctypes.c_size_t)]),
         "moe_linear": (I, [P(moe_linear_desc), V, V, V, V, V, V, V, V]),
         "moe_linear_backward": (I, [P(moe_linear_desc), V, V, V, V, V, V, V, V, V]),
+        "moe_sort_sizes": (I, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, P(ctypes.c_size_t)]),
+        "moe_sort": (I, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, V, V, V, V, V, V]),
+        "moe_permute": (I, [P(moe_rows_desc), V, V, V, V]),
+        "moe_permute_backward": (I, [P(moe_rows_desc), V, V, V, V]),
+        "moe_unpermute": (I, [P(moe_rows_desc), V, V, V, V, V]),
+        "moe_unpermute_backward": (I, [P(moe_rows_desc), V, V, V, V, V, V, V]),
         "moe_device_status": (I, [V, V]),
         "moe_device_cus": (I, []),
     }
@@ -127,7 +139,8 @@ _lib = _load()
 EXPORTED = ["moe_status_string", "moe_query_sizes", "moe_plan_offsets", "moe_plan",
             "moe_expert_combine", "moe_expert_combine_noalloc", "moe_scale", "moe_device_status",
             "moe_device_cus", "moe_scale_backward", "moe_route", "moe_route_backward", "moe_linear_sizes",
-            "moe_linear", "moe_linear_backward"]
+            "moe_linear", "moe_linear_backward", "moe_sort_sizes", "moe_sort", "moe_permute",
+            "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward"]
 
 
 def library_path() -> str:
@@ -483,6 +496,95 @@ def moe_linear_backward(x, w, d_out, dx=None, dw=None, dbias=None, pre=None, act
     ws = _workspace(where, ws, need, x, stream)
     _launch(where, index, stream, _lib.moe_linear_backward, d, x.data_ptr(), w.data_ptr(), _ptr(pre),
             d_out.data_ptr(), _ptr(dx), _ptr(dw), db, _ptr(ws))
+
+
+# --- rows sorted by expert ------------------------------------------------------
+
+@functools.lru_cache(maxsize=4096)
+def moe_sort_sizes(tokens: int, top_k: int, experts: int) -> int:
+    """Workspace bytes of moe_sort."""
+    out = ctypes.c_size_t()
+    _check(_lib.moe_sort_sizes(tokens, top_k, experts, ctypes.byref(out)), "moe_sort_sizes")
+    return out.value
+
+
+def _pairs(where, name, t):
+    """(tokens, top_k) and the GPU of a [tokens, top_k] tensor of int32."""
+    if t.dim() != 2 or t.dtype is not torch.int32 or not t.is_contiguous():
+        raise _invalid(where, f"{name} is a {t.dtype} tensor {tuple(t.shape)} with strides {t.stride()}, not a contiguous "
+                              "[tokens, top_k] one of int32")
+    return t.shape, t.get_device()
+
+
+def moe_sort(topk_ids, pos, offsets, src=None, first: int = 0, ws=None, stream=None) -> None:
+    """topk_ids int32 [T, k] -> pos int32 [T, k], the row of each slot among the
+    rows sorted by expert (-1 for an id outside first .. first + E - 1), offsets
+    int32 [E + 1], each expert's first row, and src int32 [T * k], the slot of
+    each row.  ws: at least moe_sort_sizes' bytes, or None to take it from
+    torch's allocator; see include/moe.h."""
+    where = "moe_sort"
+    shape, index = _pairs(where, "topk_ids", topk_ids)
+    T, k = shape
+    E = offsets.numel() - 1
+    args = (topk_ids.data_ptr(), _packed(where, "pos", pos, shape, torch.int32, index),
+            _packed(where, "src", src, (T * k,), torch.int32, index),
+            _packed(where, "offsets", offsets, (E + 1,), torch.int32, index))
+    need = moe_sort_sizes(T, k, E)
+    if ws is not None or need:
+        ws = _workspace(where, ws, need, topk_ids, stream)
+    _launch(where, index, stream, _lib.moe_sort, T, k, E, _int(first), *args, None if ws is None else ws.data_ptr())
+
+
+def _rows_desc(where, x, x_name, rows, rows_name, pos):
+    """The sizes of a call on sorted rows, and the GPU."""
+    (T, k), index = _pairs(where, "pos", pos)
+    dtype = x.dtype
+    code = _DTYPES.get(dtype)
+    if code is None or x.dim() != 2 or rows.dim() != 2:
+        raise _invalid(where, f"{x_name} and {rows_name} are matrices of bfloat16, float16 or float32")
+    d, R = x.shape[1], rows.shape[0]
+    return moe_rows_desc(T, R, k, d, code, 0, _matrix(where, x_name, x, (T, d), dtype, index),
+                         _matrix(where, rows_name, rows, (R, d), dtype, index), 0), index
+
+
+def moe_permute(x, pos, rows, stream=None) -> None:
+    """rows[pos[t][j]] = x[t]: x [T, d], pos int32 [T, k] of moe_sort, rows
+    [R, d] of x's type; rows that no slot names stay as they were."""
+    where = "moe_permute"
+    d, index = _rows_desc(where, x, "x", rows, "rows", pos)
+    _launch(where, index, stream, _lib.moe_permute, d, x.data_ptr(), pos.data_ptr(), rows.data_ptr())
+
+
+def moe_permute_backward(d_rows, pos, dx, stream=None) -> None:
+    """dx[t] = sum of d_rows[pos[t][j]] over the slots that have a row."""
+    where = "moe_permute_backward"
+    d, index = _rows_desc(where, dx, "dx", d_rows, "d_rows", pos)
+    _launch(where, index, stream, _lib.moe_permute_backward, d, d_rows.data_ptr(), pos.data_ptr(), dx.data_ptr())
+
+
+def moe_unpermute(rows, pos, out, topk_w=None, stream=None) -> None:
+    """out[t] = sum of topk_w[t][j] * rows[pos[t][j]]: topk_w float32 [T, k], or
+    None for weights of 1."""
+    where = "moe_unpermute"
+    d, index = _rows_desc(where, out, "out", rows, "rows", pos)
+    _launch(where, index, stream, _lib.moe_unpermute, d, rows.data_ptr(), pos.data_ptr(),
+            _packed(where, "topk_w", topk_w, pos.shape, torch.float32, index), out.data_ptr())
+
+
+def moe_unpermute_backward(pos, d_out, rows=None, topk_w=None, d_rows=None, d_topk_w=None, stream=None) -> None:
+    """The gradients of moe_unpermute that are given a tensor: d_rows [R, d] and
+    d_topk_w float32 [T, k] (this one needs rows) from d_out [T, d]."""
+    where = "moe_unpermute_backward"
+    given, name = (rows, "rows") if d_rows is None else (d_rows, "d_rows")
+    if given is None:
+        raise _invalid(where, "neither d_rows nor rows is given")
+    d, index = _rows_desc(where, d_out, "d_out", given, name, pos)
+    if d_rows is not None:
+        d.ld_d_rows = d.ld_rows
+        d.ld_rows = _matrix(where, "rows", rows, given.shape, d_out.dtype, index)
+    _launch(where, index, stream, _lib.moe_unpermute_backward, d, _ptr(rows), pos.data_ptr(),
+            _packed(where, "topk_w", topk_w, pos.shape, torch.float32, index), d_out.data_ptr(), _ptr(d_rows),
+            _packed(where, "d_topk_w", d_topk_w, pos.shape, torch.float32, index))
 
 
 def moe_device_status(plan_ws, stream=None) -> int:

@@ -1,6 +1,7 @@
 // C ABI of the operators around the experts (declared in include/moe.h):
-// routing and the dense product, with their gradients.  Host-side validation;
-// the launches are in route.hip and linear.hip.
+// routing, the dense product and the rows sorted by expert, with their
+// gradients.  Host-side validation; the launches are in route.hip, linear.hip
+// and rows.hip.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -67,6 +68,26 @@ int check_linear(const moe_linear_desc* desc, moe_linear_desc* d) {
     if (*p.ld < p.least || *p.ld > kMaxPitch || *p.ld % p.unit != 0) return MOE_EINVAL;
   }
   return MOE_OK;
+}
+
+// checks shared by the calls on sorted rows; fills in the row pitches
+int check_rows(const moe_rows_desc* desc, const int32_t* pos, moe_rows_desc* d) {
+  if (!desc) return MOE_EINVAL;
+  *d = *desc;
+  if (d->tokens < 0 || d->tokens > (1ll << 26) || d->rows < 0 || d->rows > INT32_MAX) return MOE_EINVAL;
+  if (d->top_k < 1 || d->top_k > 32 || d->cols < 1 || d->cols > (1 << 20)) return MOE_EINVAL;
+  if (d->dtype < MOE_BF16 || d->dtype > MOE_F32 || d->pad != 0) return MOE_EINVAL;
+  for (int64_t* ld : {&d->ld_x, &d->ld_rows, &d->ld_d_rows}) {
+    if (*ld == 0) *ld = d->cols;
+    if (*ld < d->cols || *ld > kMaxPitch) return MOE_EINVAL;
+  }
+  if (!aligned_to(pos, 4) || (d->tokens > 0 && !pos)) return MOE_EINVAL;
+  return MOE_OK;
+}
+
+// whether a buffer of `count` rows is there and aligned to its elements
+bool row_buffer(const moe_rows_desc& d, const void* p, int64_t count) {
+  return aligned_to(p, item(d.dtype)) && (p || count == 0);
 }
 
 }  // namespace
@@ -145,6 +166,66 @@ int moe_linear_backward(const moe_linear_desc* desc, const void* x, const void* 
   if (rc) return rc;
   LinearGrads b = {x, w, pre, d_out, dx, dw, dbias};
   return hip_rc(launch_linear_backward(d, b, ws, (hipStream_t)stream));
+}
+
+int moe_sort_sizes(int64_t tokens, int32_t top_k, int32_t experts, size_t* ws_bytes) {
+  if (tokens < 0 || tokens > (1ll << 26) || top_k < 1 || top_k > 32 || tokens * top_k > INT32_MAX) return MOE_EINVAL;
+  if (experts < 1 || experts > 1024 || !ws_bytes) return MOE_EINVAL;
+  *ws_bytes = sort_ws_bytes(tokens * top_k, experts);
+  return MOE_OK;
+}
+
+int moe_sort(int64_t tokens, int32_t top_k, int32_t experts, int32_t first, const int32_t* topk_ids, int32_t* pos,
+             int32_t* src, int32_t* offsets, void* ws, void* stream) {
+  size_t bytes;
+  int rc = moe_sort_sizes(tokens, top_k, experts, &bytes);
+  if (rc) return rc;
+  if (first < 0 || !aligned_to(topk_ids, 4) || !aligned_to(pos, 4) || !aligned_to(src, 4) || !aligned_to(offsets, 4) ||
+      !aligned_to(ws, 256))
+    return MOE_EINVAL;
+  if (!offsets || (tokens > 0 && (!topk_ids || !pos)) || (bytes > 0 && !ws)) return MOE_EINVAL;
+  rc = prepare_device();
+  if (rc) return rc;
+  return hip_rc(launch_sort(tokens * top_k, experts, first, topk_ids, pos, src, offsets, ws, (hipStream_t)stream));
+}
+
+int moe_permute(const moe_rows_desc* desc, const void* x, const int32_t* pos, void* rows, void* stream) {
+  moe_rows_desc d;
+  int rc = check_rows(desc, pos, &d);
+  if (rc) return rc;
+  if (!row_buffer(d, x, d.tokens) || !row_buffer(d, rows, d.rows)) return MOE_EINVAL;
+  rc = prepare_device();
+  if (rc || d.tokens == 0 || d.rows == 0) return rc;
+  return hip_rc(launch_permute(d, x, pos, rows, (hipStream_t)stream));
+}
+
+int moe_unpermute(const moe_rows_desc* desc, const void* rows, const int32_t* pos, const float* topk_w, void* out,
+                  void* stream) {
+  moe_rows_desc d;
+  int rc = check_rows(desc, pos, &d);
+  if (rc) return rc;
+  if (!row_buffer(d, rows, d.rows) || !row_buffer(d, out, d.tokens) || !aligned_to(topk_w, 4)) return MOE_EINVAL;
+  rc = prepare_device();
+  if (rc || d.tokens == 0) return rc;
+  return hip_rc(launch_unpermute(d, rows, pos, topk_w, out, (hipStream_t)stream));
+}
+
+int moe_permute_backward(const moe_rows_desc* desc, const void* d_rows, const int32_t* pos, void* dx, void* stream) {
+  return moe_unpermute(desc, d_rows, pos, nullptr, dx, stream);   // the same sum, without weights
+}
+
+int moe_unpermute_backward(const moe_rows_desc* desc, const void* rows, const int32_t* pos, const float* topk_w,
+                           const void* d_out, void* d_rows, float* d_topk_w, void* stream) {
+  moe_rows_desc d;
+  int rc = check_rows(desc, pos, &d);
+  if (rc) return rc;
+  if (!d_rows && !d_topk_w) return MOE_EINVAL;
+  if (!row_buffer(d, d_out, d.tokens) || !row_buffer(d, d_rows, 0) || !row_buffer(d, rows, d_topk_w ? d.rows : 0) ||
+      !aligned_to(topk_w, 4) || !aligned_to(d_topk_w, 4))
+    return MOE_EINVAL;
+  rc = prepare_device();
+  if (rc || d.tokens == 0) return rc;
+  return hip_rc(launch_unpermute_backward(d, rows, pos, topk_w, d_out, d_rows, d_topk_w, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -40,6 +40,16 @@ void linear_cuts(const moe_linear_desc& d, int32_t cuts[6]);
 hipError_t launch_linear(const moe_linear_desc& d, const LinearBuffers& b, void* ws, hipStream_t s);
 hipError_t launch_linear_backward(const moe_linear_desc& d, const LinearGrads& b, void* ws, hipStream_t s);
 
+// rows sorted by expert (rows.hip); `d` has its row pitches filled in
+size_t sort_ws_bytes(int64_t pairs, int E);
+hipError_t launch_sort(int64_t pairs, int E, int first, const int32_t* ids, int32_t* pos, int32_t* src,
+                       int32_t* offsets, void* ws, hipStream_t s);
+hipError_t launch_permute(const moe_rows_desc& d, const void* x, const int32_t* pos, void* rows, hipStream_t s);
+hipError_t launch_unpermute(const moe_rows_desc& d, const void* rows, const int32_t* pos, const float* w, void* out,
+                            hipStream_t s);
+hipError_t launch_unpermute_backward(const moe_rows_desc& d, const void* rows, const int32_t* pos, const float* w,
+                                     const void* d_out, void* d_rows, float* dw, hipStream_t s);
+
 // the current device, checked to be a gfx950 (api.cpp); a moe_status
 int prepare_device();
 
