@@ -492,6 +492,70 @@ int moe_unpermute(const moe_rows_desc* desc, const void* rows, const int32_t* po
 int moe_unpermute_backward(const moe_rows_desc* desc, const void* rows, const int32_t* pos, const float* topk_w,
                            const void* d_out, void* d_rows, float* d_topk_w, void* stream);
 
+/*
+ * Microscaled 4-bit rows (MXFP4): elements of sign, two exponent bits and one
+ * fraction bit (+-0, 0.5, 1, 1.5, 2, 3, 4, 6), two a byte with the even one in the low
+ * half, and a scale byte s for each 32 of them along the row: element times
+ * 2^(s - 127); s = 255 makes its block NaN.  Packed rows are 16-byte aligned with
+ * pitches (bytes) that are multiples of 16, scales at any address and pitch.
+ * Row lengths are multiples of 32, up to 2^20.  Pitches are at most 2^21, 0 = packed.
+ */
+enum { MOE_MXFP4 = 3 };   /* beside moe_dtype, as the type of moe_mx_linear's x */
+
+/*
+ * moe_mx_quantize — the nearest microscaled rows of x: a block's scale is
+ * 2^(floor(log2 of its largest magnitude) - 2), 2^-127 at least; its elements are
+ * divided by it and rounded, ties to the even element, those above 6 to 6.
+ * A block with an infinity or a NaN becomes NaN (scale 255, elements 0).
+ *   x       device [rows, depth] of dtype (MOE_BF16, MOE_F16, MOE_F32), rows ld_x elements apart.
+ *   q       device [rows, depth / 2] bytes, rows ld_q bytes apart.
+ *   scale   device [rows, depth / 32] bytes, rows ld_scale bytes apart.
+ * rows <= 2^31 - 1.
+ */
+int moe_mx_quantize(int64_t rows, int32_t depth, const void* x, int32_t dtype, int64_t ld_x, uint8_t* q, int64_t ld_q,
+                    uint8_t* scale, int64_t ld_scale, void* stream);
+
+/* moe_mx_dequantize — what microscaled rows stand for, rounded to dtype (exact
+ * in it, but for values outside its range).  out: device [rows, depth]. */
+int moe_mx_dequantize(int64_t rows, int32_t depth, const uint8_t* q, int64_t ld_q, const uint8_t* scale,
+                      int64_t ld_scale, void* out, int32_t dtype, int64_t ld_out, void* stream);
+
+/* Sizes and types of moe_mx_linear.  n = 2 * cols under SWIGLU, else cols. */
+typedef struct moe_mx_linear_desc {
+  int64_t rows;            /* of x and out; 0..2^26 */
+  int32_t experts;         /* 1..1024 */
+  int32_t cols;            /* of out; 1..2^20 */
+  int32_t depth;           /* of x and w; a multiple of 32, 32..2^20 */
+  int32_t dtype;           /* of x: MOE_BF16, MOE_F16 or MOE_MXFP4 */
+  int32_t out_dtype;       /* of out and bias: x's or MOE_F32; any of moe_dtype if x is MOE_MXFP4 */
+  int32_t act;             /* MOE_ACT_* */
+  int64_t ld_x;            /* elements, a multiple of 8; MOE_MXFP4: bytes, a multiple of 16 */
+  int64_t ld_x_scale;      /* bytes */
+  int64_t ld_w;            /* bytes, a multiple of 16 */
+  int64_t ld_w_scale;      /* bytes */
+  int64_t expert_w;        /* bytes from one expert's weights to the next's, a multiple of 16; 0: n * ld_w */
+  int64_t expert_w_scale;  /* bytes; 0: n * ld_w_scale */
+  int64_t ld_out;          /* elements */
+} moe_mx_linear_desc;
+
+/*
+ * moe_mx_linear — out[r] = act(x[r] w[e]^T + bias[e]) for the rows r of each
+ * expert e, with weights in microscaled 4 bits and fp32 sums, rounded once.  With
+ * x in 16 bits the weights are taken in x's type: exactly in MOE_BF16; in
+ * MOE_F16 those of magnitude 65520 and above are infinite and bits below
+ * 2^-24 are rounded.  With x in MOE_MXFP4 the products are exact.
+ *   x         device [rows, depth], 16-byte aligned; MOE_MXFP4: packed rows [rows, depth / 2].
+ *   x_scale   device [rows, depth / 32] with MOE_MXFP4, else not read.
+ *   w         device [experts, n, depth / 2], 16-byte aligned;  w_scale  device [experts, n, depth / 32].
+ *   offsets   device int32 [experts + 1], ascending, e.g. from moe_sort: expert e's rows are offsets[e] ..
+ *             offsets[e + 1] - 1.  Rows outside all of them are neither read nor written.  NULL: one expert,
+ *             which has all rows.
+ *   bias      device [experts, n] of out_dtype, or NULL.
+ *   out       device [rows, cols] of out_dtype, no overlap with the inputs.
+ */
+int moe_mx_linear(const moe_mx_linear_desc* desc, const void* x, const uint8_t* x_scale, const uint8_t* w,
+                  const uint8_t* w_scale, const int32_t* offsets, const void* bias, void* out, void* stream);
+
 /* Synchronises `stream`, then returns the device error word of the plan
  * (MOE_OK, MOE_ETIMEOUT or MOE_EROUTING), or MOE_EHIP. */
 int moe_device_status(const void* plan_ws, void* stream);

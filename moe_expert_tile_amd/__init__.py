@@ -29,6 +29,7 @@ SIGNAL_TILE, SIGNAL_GROUP = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_SWIGLU = range(6)
+MXFP4, MX_BLOCK = 3, 32   # the type of packed 4-bit rows; elements that share a scale
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 HDR_FIELDS = ["error", "M", "bands", "remote_bands", "segments", "remote_segments",
@@ -89,6 +90,14 @@ class moe_rows_desc(ctypes.Structure):
                 ("ld_x", ctypes.c_int64), ("ld_rows", ctypes.c_int64), ("ld_d_rows", ctypes.c_int64)]
 
 
+class moe_mx_linear_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("experts", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("depth", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_x_scale", ctypes.c_int64),
+                ("ld_w", ctypes.c_int64), ("ld_w_scale", ctypes.c_int64), ("expert_w", ctypes.c_int64),
+                ("expert_w_scale", ctypes.c_int64), ("ld_out", ctypes.c_int64)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -125,6 +134,11 @@ def _load():
         "moe_permute_backward": (I, [P(moe_rows_desc), V, V, V, V]),
         "moe_unpermute": (I, [P(moe_rows_desc), V, V, V, V, V]),
         "moe_unpermute_backward": (I, [P(moe_rows_desc), V, V, V, V, V, V, V]),
+        "moe_mx_quantize": (I, [ctypes.c_int64, ctypes.c_int32, V, ctypes.c_int32, ctypes.c_int64, V, ctypes.c_int64, V,
+                                ctypes.c_int64, V]),
+        "moe_mx_dequantize": (I, [ctypes.c_int64, ctypes.c_int32, V, ctypes.c_int64, V, ctypes.c_int64, V,
+                                  ctypes.c_int32, ctypes.c_int64, V]),
+        "moe_mx_linear": (I, [P(moe_mx_linear_desc), V, V, V, V, V, V, V, V]),
         "moe_device_status": (I, [V, V]),
         "moe_device_cus": (I, []),
     }
@@ -140,7 +154,8 @@ EXPORTED = ["moe_status_string", "moe_query_sizes", "moe_plan_offsets", "moe_pla
             "moe_expert_combine", "moe_expert_combine_noalloc", "moe_scale", "moe_device_status",
             "moe_device_cus", "moe_scale_backward", "moe_route", "moe_route_backward", "moe_linear_sizes",
             "moe_linear", "moe_linear_backward", "moe_sort_sizes", "moe_sort", "moe_permute",
-            "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward"]
+            "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward", "moe_mx_quantize", "moe_mx_dequantize",
+            "moe_mx_linear"]
 
 
 def library_path() -> str:
@@ -585,6 +600,101 @@ def moe_unpermute_backward(pos, d_out, rows=None, topk_w=None, d_rows=None, d_to
     _launch(where, index, stream, _lib.moe_unpermute_backward, d, _ptr(rows), pos.data_ptr(),
             _packed(where, "topk_w", topk_w, pos.shape, torch.float32, index), d_out.data_ptr(), _ptr(d_rows),
             _packed(where, "d_topk_w", d_topk_w, pos.shape, torch.float32, index))
+
+
+# --- microscaled 4-bit rows -----------------------------------------------------
+
+# bytes, under torch's names for them where it has them
+_MX_ROWS = tuple(getattr(torch, n) for n in ("uint8", "float4_e2m1fn_x2") if hasattr(torch, n))
+_MX_SCALES = tuple(getattr(torch, n) for n in ("uint8", "float8_e8m0fnu") if hasattr(torch, n))
+
+
+def _mx(where, name, t, shape, dtypes, index) -> int:
+    """Checks a matrix of bytes; returns its row pitch, as _matrix does."""
+    if t.dtype not in dtypes:
+        raise _mismatch(where, name, t, shape, dtypes[0], index, "row-major")
+    return _matrix(where, name, t, shape, t.dtype, index)
+
+
+def _mx_rows(where, x, x_name, q, scale):
+    code = _DTYPES.get(x.dtype)
+    if code is None or x.dim() != 2 or x.shape[1] % MX_BLOCK or x.shape[1] == 0:
+        raise _invalid(where, f"{x_name} is a {x.dtype} tensor {tuple(x.shape)}, not a matrix of bfloat16, float16 or float32 "
+                              f"with a multiple of {MX_BLOCK} columns")
+    M, K = x.shape
+    index = x.get_device()
+    return (M, K, code, _matrix(where, x_name, x, x.shape, x.dtype, index),
+            _mx(where, "q", q, (M, K // 2), _MX_ROWS, index),
+            _mx(where, "scale", scale, (M, K // MX_BLOCK), _MX_SCALES, index), index)
+
+
+def moe_mx_quantize(x, q, scale, stream=None) -> None:
+    """x [M, K] -> its microscaled 4-bit rows: q [M, K / 2] and scale [M, K / 32],
+    bytes; see include/moe.h."""
+    where = "moe_mx_quantize"
+    M, K, code, ld_x, ld_q, ld_s, index = _mx_rows(where, x, "x", q, scale)
+    _launch(where, index, stream, _lib.moe_mx_quantize, M, K, x.data_ptr(), code, ld_x, q.data_ptr(), ld_q,
+            scale.data_ptr(), ld_s)
+
+
+def moe_mx_dequantize(q, scale, out, stream=None) -> None:
+    """What the microscaled rows stand for, in out's type: out [M, K]."""
+    where = "moe_mx_dequantize"
+    M, K, code, ld_out, ld_q, ld_s, index = _mx_rows(where, out, "out", q, scale)
+    _launch(where, index, stream, _lib.moe_mx_dequantize, M, K, q.data_ptr(), ld_q, scale.data_ptr(), ld_s,
+            out.data_ptr(), code, ld_out)
+
+
+def _experts(where, name, t, shape, dtypes, index):
+    """Checks the experts' matrices [E, rows, bytes] (one expert's: also
+    [rows, bytes]); returns (row pitch, bytes between experts), 0 where packed."""
+    E, rows, cols = shape
+    if t.dim() == 2 and E == 1:
+        return _mx(where, name, t, (rows, cols), dtypes, index), 0
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != index:
+        raise _mismatch(where, name, t, shape, dtypes[0], index, "row-major")
+    between, pitch, step = t.stride()
+    if step != 1 and cols > 1 or pitch < cols and rows > 1 or between < 1 and E > 1:
+        raise _mismatch(where, name, t, shape, dtypes[0], index, "row-major")
+    return pitch if rows > 1 else 0, between if E > 1 else 0
+
+
+def moe_mx_linear(x, w, w_scale, out, offsets=None, x_scale=None, bias=None, act: int = ACT_NONE, stream=None) -> None:
+    """out = act(x w^T + bias), expert by expert, with microscaled 4-bit weights
+    w [E, N, K / 2] and w_scale [E, N, K / 32] (SWIGLU: 2N rows each, gate then
+    up; without the first dimension for one expert).  x [M, K] is bfloat16 or float16,
+    or packed 4-bit rows [M, K / 2] with x_scale [M, K / 32].  offsets int32
+    [E + 1]: each expert's first row (moe_sort's), None for one expert.  out
+    [M, N] and bias [E, N] are of x's type or float32, any type with packed
+    rows; see include/moe.h."""
+    where = "moe_mx_linear"
+    if x.dim() != 2 or out.dim() != 2 or w.dim() not in (2, 3):
+        raise _invalid(where, "x and out are matrices, w [experts, n, depth / 2] or one expert's matrix")
+    index = x.get_device()
+    M, N = out.shape
+    E = 1 if w.dim() == 2 else w.shape[0]
+    n = 2 * N if act == ACT_SWIGLU else N
+    code = _DTYPES.get(out.dtype)
+    if x_scale is not None:
+        K, xt = 2 * x.shape[1], MXFP4
+        sound = code is not None
+        ld_x = _mx(where, "x", x, x.shape, _MX_ROWS, index)
+        ld_xs = _mx(where, "x_scale", x_scale, (M, K // MX_BLOCK), _MX_SCALES, index)
+    else:
+        K, xt = x.shape[1], _DTYPES.get(x.dtype)
+        sound = xt in (0, 1) and code in (xt, 2)
+        ld_x, ld_xs = _matrix(where, "x", x, x.shape, x.dtype, index), 0
+    if not sound or x.shape[0] != M or K % MX_BLOCK:
+        raise _invalid(where, f"x is {x.dtype} {tuple(x.shape)} and out {out.dtype} {tuple(out.shape)}: bfloat16 or float16 "
+                              f"with a multiple of {MX_BLOCK} columns and the same or float32, or packed rows with x_scale")
+    ld_w, expert_w = _experts(where, "w", w, (E, n, K // 2), _MX_ROWS, index)
+    ld_ws, expert_ws = _experts(where, "w_scale", w_scale, (E, n, K // MX_BLOCK), _MX_SCALES, index)
+    if bias is not None:
+        bias = _packed(where, "bias", bias, (E, n) if bias.dim() > 1 or E > 1 else (n,), out.dtype, index)
+    d = moe_mx_linear_desc(M, E, N, K, xt, code, act, ld_x, ld_xs, ld_w, ld_ws, expert_w, expert_ws,
+                           _matrix(where, "out", out, out.shape, out.dtype, index))
+    _launch(where, index, stream, _lib.moe_mx_linear, d, x.data_ptr(), _ptr(x_scale), w.data_ptr(), w_scale.data_ptr(),
+            _packed(where, "offsets", offsets, (E + 1,), torch.int32, index), bias, out.data_ptr())
 
 
 def moe_device_status(plan_ws, stream=None) -> int:

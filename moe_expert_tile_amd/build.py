@@ -18,7 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["plan.hip", "gemm.hip", "combine.hip", "scale.hip", "noalloc.hip", "route.hip", "linear.hip",
-           "rows.hip", "api.cpp", "layer_api.cpp"]
+           "rows.hip", "mx.hip", "api.cpp", "layer_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -1,7 +1,7 @@
 // C ABI of the operators around the experts (declared in include/moe.h):
 // routing, the dense product and the rows sorted by expert, with their
-// gradients.  Host-side validation; the launches are in route.hip, linear.hip
-// and rows.hip.
+// gradients, and microscaled 4-bit rows.  Host-side validation; the launches are
+// in route.hip, linear.hip, rows.hip and mx.hip.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -88,6 +88,50 @@ int check_rows(const moe_rows_desc* desc, const int32_t* pos, moe_rows_desc* d) 
 // whether a buffer of `count` rows is there and aligned to its elements
 bool row_buffer(const moe_rows_desc& d, const void* p, int64_t count) {
   return aligned_to(p, item(d.dtype)) && (p || count == 0);
+}
+
+// checks shared by the quantisation calls; fills in the pitches
+int check_mx_rows(int64_t rows, int32_t depth, const void* x, int32_t dtype, int64_t* ld_x, const uint8_t* q,
+                  int64_t* ld_q, const uint8_t* scale, int64_t* ld_s) {
+  if (rows < 0 || rows > INT32_MAX || depth < 32 || depth > (1 << 20) || depth % 32 != 0) return MOE_EINVAL;
+  if (dtype < MOE_BF16 || dtype > MOE_F32) return MOE_EINVAL;
+  if (*ld_x == 0) *ld_x = depth;
+  if (*ld_q == 0) *ld_q = depth / 2;
+  if (*ld_s == 0) *ld_s = depth / 32;
+  if (*ld_x < depth || *ld_x > kMaxPitch || *ld_q < depth / 2 || *ld_q > kMaxPitch || *ld_q % 16 != 0 ||
+      *ld_s < depth / 32 || *ld_s > kMaxPitch)
+    return MOE_EINVAL;
+  if (!aligned_to(x, item(dtype)) || !aligned_to(q, 16)) return MOE_EINVAL;
+  if (rows > 0 && (!x || !q || !scale)) return MOE_EINVAL;
+  return MOE_OK;
+}
+
+// checks a product's sizes and fills in its pitches
+int check_mx_linear(const moe_mx_linear_desc* desc, moe_mx_linear_desc* d) {
+  if (!desc) return MOE_EINVAL;
+  *d = *desc;
+  if (d->rows < 0 || d->rows > (1ll << 26) || d->experts < 1 || d->experts > 1024) return MOE_EINVAL;
+  if (d->cols < 1 || d->cols > (1 << 20)) return MOE_EINVAL;
+  if (d->depth < 32 || d->depth > (1 << 20) || d->depth % 32 != 0) return MOE_EINVAL;
+  const bool mx = d->dtype == MOE_MXFP4;
+  if (d->dtype != MOE_BF16 && d->dtype != MOE_F16 && !mx) return MOE_EINVAL;
+  if (d->out_dtype < MOE_BF16 || d->out_dtype > MOE_F32 || (!mx && d->out_dtype != d->dtype && d->out_dtype != MOE_F32))
+    return MOE_EINVAL;
+  if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_SWIGLU) return MOE_EINVAL;
+  const int64_t n = (int64_t)d->cols * (d->act == MOE_ACT_SWIGLU ? 2 : 1);
+  struct { int64_t* ld; int64_t least, unit; } pitches[] = {
+      {&d->ld_x, mx ? d->depth / 2 : d->depth, mx ? 16 : 8}, {&d->ld_x_scale, d->depth / 32, 1},
+      {&d->ld_w, d->depth / 2, 16}, {&d->ld_w_scale, d->depth / 32, 1}, {&d->ld_out, d->cols, 1}};
+  for (auto& p : pitches) {
+    if (*p.ld == 0) *p.ld = p.least;
+    if (*p.ld < p.least || *p.ld > kMaxPitch || *p.ld % p.unit != 0) return MOE_EINVAL;
+  }
+  if (d->expert_w == 0) d->expert_w = n * d->ld_w;
+  if (d->expert_w_scale == 0) d->expert_w_scale = n * d->ld_w_scale;
+  const int64_t most = 1ll << 42;
+  if (d->expert_w < 0 || d->expert_w > most || d->expert_w % 16 != 0 || d->expert_w_scale < 0 || d->expert_w_scale > most)
+    return MOE_EINVAL;
+  return MOE_OK;
 }
 
 }  // namespace
@@ -226,6 +270,37 @@ int moe_unpermute_backward(const moe_rows_desc* desc, const void* rows, const in
   rc = prepare_device();
   if (rc || d.tokens == 0) return rc;
   return hip_rc(launch_unpermute_backward(d, rows, pos, topk_w, d_out, d_rows, d_topk_w, (hipStream_t)stream));
+}
+
+int moe_mx_quantize(int64_t rows, int32_t depth, const void* x, int32_t dtype, int64_t ld_x, uint8_t* q, int64_t ld_q,
+                    uint8_t* scale, int64_t ld_scale, void* stream) {
+  int rc = check_mx_rows(rows, depth, x, dtype, &ld_x, q, &ld_q, scale, &ld_scale);
+  if (!rc) rc = prepare_device();
+  if (rc || rows == 0) return rc;
+  return hip_rc(launch_mx_quantize(rows, depth, x, dtype, ld_x, q, ld_q, scale, ld_scale, (hipStream_t)stream));
+}
+
+int moe_mx_dequantize(int64_t rows, int32_t depth, const uint8_t* q, int64_t ld_q, const uint8_t* scale,
+                      int64_t ld_scale, void* out, int32_t dtype, int64_t ld_out, void* stream) {
+  int rc = check_mx_rows(rows, depth, out, dtype, &ld_out, q, &ld_q, scale, &ld_scale);
+  if (!rc) rc = prepare_device();
+  if (rc || rows == 0) return rc;
+  return hip_rc(launch_mx_dequantize(rows, depth, q, ld_q, scale, ld_scale, out, dtype, ld_out, (hipStream_t)stream));
+}
+
+int moe_mx_linear(const moe_mx_linear_desc* desc, const void* x, const uint8_t* x_scale, const uint8_t* w,
+                  const uint8_t* w_scale, const int32_t* offsets, const void* bias, void* out, void* stream) {
+  moe_mx_linear_desc d;
+  int rc = check_mx_linear(desc, &d);
+  if (rc) return rc;
+  const size_t o = item(d.out_dtype);
+  if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(offsets, 4) || !aligned_to(bias, o) || !aligned_to(out, o))
+    return MOE_EINVAL;
+  if (!offsets && d.experts != 1) return MOE_EINVAL;
+  if (d.rows > 0 && (!x || !w || !w_scale || !out || (d.dtype == MOE_MXFP4 && !x_scale))) return MOE_EINVAL;
+  rc = prepare_device();
+  if (rc || d.rows == 0) return rc;
+  return hip_rc(launch_mx_linear(d, x, x_scale, w, w_scale, offsets, bias, out, (hipStream_t)stream));
 }
 
 }  // extern "C"

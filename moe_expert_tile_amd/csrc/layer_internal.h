@@ -50,6 +50,14 @@ hipError_t launch_unpermute(const moe_rows_desc& d, const void* rows, const int3
 hipError_t launch_unpermute_backward(const moe_rows_desc& d, const void* rows, const int32_t* pos, const float* w,
                                      const void* d_out, void* d_rows, float* dw, hipStream_t s);
 
+// microscaled 4-bit rows (mx.hip); pitches and `d` have their defaults filled in
+hipError_t launch_mx_quantize(int64_t rows, int depth, const void* x, int dtype, int64_t ld_x, uint8_t* q, int64_t ld_q,
+                              uint8_t* scale, int64_t ld_s, hipStream_t s);
+hipError_t launch_mx_dequantize(int64_t rows, int depth, const uint8_t* q, int64_t ld_q, const uint8_t* scale,
+                                int64_t ld_s, void* out, int dtype, int64_t ld_out, hipStream_t s);
+hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const uint8_t* x_scale, const uint8_t* w,
+                            const uint8_t* w_scale, const int32_t* offsets, const void* bias, void* out, hipStream_t s);
+
 // the current device, checked to be a gfx950 (api.cpp); a moe_status
 int prepare_device();
 
