@@ -191,6 +191,20 @@ struct RowTile {
   int64_t row;
 };
 
+// Row tiles of bm of all experts' rows.  Called by whole wavefronts.
+__device__ __forceinline__ int count_tiles(const MxArgs& a, int bm) {
+  const int rows = (int)a.rows;
+  if (!a.offsets) return (rows + bm - 1) / bm;
+  int n = 0;
+  for (int e = threadIdx.x & 63; e < a.E; e += 64) {
+    const int lo = min(max(a.offsets[e], 0), rows), hi = min(max(a.offsets[e + 1], 0), rows);
+    n += hi > lo ? (hi - lo + bm - 1) / bm : 0;
+  }
+#pragma unroll
+  for (int s = 32; s; s >>= 1) n += __shfl_xor(n, s);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
 // Row tile t of the experts' rows cut into pieces of bm, none of which holds
 // rows of two experts.  Offsets out of order or out of range give other rows, but
 // none outside [0, rows).  Called by whole wavefronts.
@@ -226,8 +240,9 @@ __device__ __forceinline__ RowTile find_tile(const MxArgs& a, int bm, int t) {
   return {0, 0, 0};
 }
 
-// Columns n .. n + 3 of a row and their bias, of which `left` exist
-__device__ __forceinline__ void load4(int type, const void* base, int64_t at, int left, float (&v)[4]) {
+// W columns of a row in the output's type, of which `left` exist
+template <int W>
+__device__ __forceinline__ void load_row(int type, const void* base, int64_t at, int left, float (&v)[W]) {
   if (type == MOE_F32) load32((const float*)base + at, left, v);
   else if (type == MOE_F16) load16<true>((const uint16_t*)base + at, left, v);
   else load16<false>((const uint16_t*)base + at, left, v);
@@ -374,11 +389,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(MxArgs a) {
     if (m >= rows || n >= a.N) continue;
     if (a.bias) {
       float add[4];
-      load4(a.out_type, a.bias, (int64_t)expert * G * a.N + n, a.N - n, add);
+      load_row(a.out_type, a.bias, (int64_t)expert * G * a.N + n, a.N - n, add);
 #pragma unroll
       for (int c = 0; c < 4; ++c) z[c] += add[c];
       if constexpr (GATED) {
-        load4(a.out_type, a.bias, (int64_t)expert * G * a.N + a.N + n, a.N - n, add);
+        load_row(a.out_type, a.bias, (int64_t)expert * G * a.N + a.N + n, a.N - n, add);
 #pragma unroll
         for (int c = 0; c < 4; ++c) u[c] += add[c];
       }
@@ -391,6 +406,268 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(MxArgs a) {
     }
     store_row(a.out_type, a.out, (row0 + m) * a.ld_out + n, a.N - n, y);
   }
+}
+
+// --- tiles ----------------------------------------------------------------------
+//
+// Many rows: tiles of BM rows of one expert x BN rows of w, staged through LDS by
+// direct-to-LDS buffer loads, v_mfma_*_32x32 out of it.  A stage is 128 bytes of
+// each row of x: 256 elements in 4 bits, 64 in 16, and as many elements of w.
+// Rows past an operand's end and blocks past K get an offset past the buffer
+// descriptor's bound, where loads return zeros.  Scales come through registers
+// (their rows may start at any byte), 32 bytes of a row at a time, into a table of
+// their own in LDS, ahead of the stages that need them.
+
+template <int BM_, int BN_, int WAVES_M, int WAVES_N>
+struct MxTile {
+  static constexpr int BM = BM_, BN = BN_;
+  static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64, WN_ = WAVES_N;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
+  static constexpr int FM = WM / 32, FN = WN / 32;
+  static constexpr int PITCH = FN * 32 + 4;       // floats of a row in the epilogue's staging
+  static constexpr int EPI = NW * 32 * PITCH * 4;
+};
+typedef MxTile<256, 256, 2, 4> Mx256;
+typedef MxTile<256, 256, 4, 2> Mx256G;   // gated: each wave's columns hold as many gate as up ones
+typedef MxTile<128, 128, 2, 2> Mx128;
+
+// 16 bytes of a row's scales from byte `at` on, zeros past its `bytes`
+__device__ __forceinline__ v4u32 load_scales(const uint8_t* row, int at, int bytes) {
+  if (at + 16 <= bytes) return ((const Loose<v4u32, 1>*)(row + at))->v;
+  v4u32 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < 15; ++c)
+    if (at + c < bytes) v[c / 4] |= (uint32_t)row[at + c] << (c % 4 * 8);
+  return v;
+}
+
+// A workgroup's tile: its place among the row and column tiles.  Workgroup i runs
+// on XCD i mod 8; each XCD gets a contiguous run, in which 8 row tiles x 4 column
+// tiles share their operands in its L2.
+struct Place {
+  RowTile rows;
+  int n0, cols;      // output columns
+};
+template <int BM, int HB>
+__device__ __forceinline__ Place place_of(const MxArgs& a) {
+  const int n_mt = count_tiles(a, BM), total = n_mt * a.n_nt;
+  if ((int)blockIdx.x >= total) return {{0, 0, 0}, 0, 0};
+  int t = xcd_order(blockIdx.x, total);
+  const int grp = t / (8 * a.n_nt), rows8 = min(8, n_mt - grp * 8);
+  t -= grp * 8 * a.n_nt;
+  RowTile r = find_tile(a, BM, grp * 8 + t % rows8);
+  const int n0 = (a.nt0 + t / rows8) * HB;
+  return {r, n0, min(HB, a.N - n0)};
+}
+
+// 32 rows of a wavefront's columns at a time go through LDS, so that lanes hold
+// neighbouring columns and every global access covers whole lines.
+template <class C, bool GATED>
+__device__ __forceinline__ void finish_tile(const MxArgs& a, const Place& p, f32x16 (&acc)[C::FN][C::FM], char* lds,
+                                            int wave, int lane) {
+  constexpr int FG = GATED ? C::FN / 2 : C::FN, CW = FG * 32, G = GATED ? 2 : 1;
+  float* stage = (float*)lds + wave * 32 * C::PITCH;
+  const int wave_m = wave / C::WN_, wave_n = wave % C::WN_;
+  constexpr int LPR = CW / 8, RPP = 64 / LPR;   // lanes a row (8 columns each), rows a pass
+  const int lrow = lane & 31, lhalf = lane >> 5;
+  const int er = lane / LPR, ec = (lane % LPR) * 8;
+  const int n = p.n0 + wave_n * CW + ec, left = a.N - n;
+  float bz[8], bu[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) bz[c] = bu[c] = 0.f;
+  if (a.bias && left > 0) {
+    const int64_t at = (int64_t)p.rows.expert * G * a.N + n;
+    load_row(a.out_type, a.bias, at, left, bz);
+    if constexpr (GATED) load_row(a.out_type, a.bias, at + a.N, left, bu);
+  }
+#pragma unroll
+  for (int j = 0; j < C::FM; ++j) {
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(float4*)(stage + lrow * C::PITCH + 32 * i + 8 * q + 4 * lhalf) =
+            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+    __builtin_amdgcn_wave_barrier();
+    auto staged8 = [&](int r, int col, float (&v)[8]) __attribute__((always_inline)) {
+      const float4 x = *(const float4*)(stage + r * C::PITCH + col), y = *(const float4*)(stage + r * C::PITCH + col + 4);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    };
+#pragma unroll 2
+    for (int r = er; r < 32; r += RPP) {
+      const int m = wave_m * C::WM + 32 * j + r;
+      float z[8], u[8], y[8];
+      staged8(r, ec, z);
+      if constexpr (GATED) staged8(r, CW + ec, u);
+      if (m >= p.rows.count || left <= 0) continue;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        z[c] += bz[c];
+        if constexpr (GATED) y[c] = z[c] * logistic(z[c]) * (u[c] + bu[c]);
+      }
+      if constexpr (!GATED) activate_all(a.act, z, y);
+      store_row(a.out_type, a.out, (p.rows.row + m) * a.ld_out + n, left, y);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// first row of w, inside the tile, of a wavefront's i-th block of 32
+template <class C, bool GATED>
+__device__ __forceinline__ int block_row(int wave_n, int i) {
+  if constexpr (GATED) return i < C::FN / 2 ? wave_n * (C::WN / 2) + 32 * i : C::BN / 2 + wave_n * (C::WN / 2) + 32 * (i - C::FN / 2);
+  else return wave_n * C::WN + 32 * i;
+}
+
+// Both operands in 4 bits.  A stage's 16-byte chunks (one block each) of row r lie
+// at c ^ (r / 2) % 8, free of bank conflicts.  Lane half h takes blocks 4 h + kk of
+// a stage in MFMA step kk, so that its four scales are one dword.
+template <class C, bool GATED>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
+void mx_both_kernel(MxArgs a) {
+  constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 128;
+  constexpr int SCALES = (C::BM + C::BN) * 32;              // four stages' scales
+  constexpr int A_LOADS = C::BM / 8 / C::NW, B_LOADS = C::BN / 8 / C::NW;
+  constexpr int S_LOADS = SCALES / 16 / C::NT;
+  constexpr int LDS = 2 * STAGE + 2 * SCALES;
+  static_assert(LDS >= C::EPI && LDS <= 160 * 1024 && C::NW % 2 == 0 && B_LOADS % 2 == 0, "tile");
+  __shared__ __attribute__((aligned(1024))) char lds[LDS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_m = wave / C::WN_, wave_n = wave % C::WN_;
+  constexpr int HB = GATED ? C::BN / 2 : C::BN;
+  Place p = place_of<C::BM, HB>(a);
+  p.rows.expert = __builtin_amdgcn_readfirstlane(p.rows.expert);
+  p.rows.count = __builtin_amdgcn_readfirstlane(p.rows.count);
+  p.rows.row = __builtin_amdgcn_readfirstlane((int)p.rows.row);
+  if (p.rows.count <= 0) return;
+  const int arows = p.rows.count, brows = p.cols;
+  const int kbytes = a.K / 2, kscales = a.K / 32;
+  const int KT = (kbytes + 127) / 128, tail = kbytes - (KT - 1) * 128;
+
+  const char* w = a.w + p.rows.expert * a.expert_w + p.n0 * a.ld_w;
+  const char* x = a.x + p.rows.row * a.ld_x;
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(x, (arows - 1) * a.ld_x + kbytes);
+  const __amdgpu_buffer_rsrc_t br = make_rsrc(w, (brows - 1) * a.ld_w + kbytes);
+  const __amdgpu_buffer_rsrc_t ur = GATED ? make_rsrc(w + a.N * a.ld_w, (brows - 1) * a.ld_w + kbytes) : br;
+  uint32_t aoff[A_LOADS], boff[B_LOADS];
+  const int chunk = (lane % 8) ^ ((wave * 4 + lane / 16) % 8);
+#pragma unroll
+  for (int i = 0; i < A_LOADS; ++i) {
+    const int r = (wave + i * C::NW) * 8 + lane / 8;
+    aoff[i] = r < arows ? (uint32_t)r * (uint32_t)a.ld_x + chunk * 16 : kPastEnd;
+  }
+#pragma unroll
+  for (int i = 0; i < B_LOADS; ++i) {
+    const int r = (wave + (GATED ? i % (B_LOADS / 2) : i) * C::NW) * 8 + lane / 8;   // the second half: up rows
+    boff[i] = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + chunk * 16 : kPastEnd;
+  }
+  auto issue = [&](int k, auto last_tag) __attribute__((always_inline)) {
+    constexpr bool LAST = decltype(last_tag)::value;
+    char* base = lds + (k & 1) * STAGE;
+    const bool on = !LAST || chunk * 16 < tail;
+#pragma unroll
+    for (int i = 0; i < A_LOADS; ++i)
+      load_lds(ar, base + (wave + i * C::NW) * 1024, on ? aoff[i] : kPastEnd, 128 * k);
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i)
+      load_lds(GATED && i >= B_LOADS / 2 ? ur : br, base + A_BYTES + (wave + i * C::NW) * 1024, on ? boff[i] : kPastEnd, 128 * k);
+  };
+  // scales of stages 4 s .. 4 s + 3: 32 bytes a row (x's rows, then w's), this thread's
+  // 16-byte halves; halves of rows 8 .. 15 of 16 swapped, against bank conflicts
+  v4u32 sc[S_LOADS];
+  auto fetch_scales = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < S_LOADS; ++i) {
+      const int id = i * C::NT + tid, r = id / 2;
+      const uint8_t* row;
+      bool on;
+      if (r < C::BM) {
+        row = a.xs + (p.rows.row + r) * a.ld_xs;
+        on = r < arows;
+      } else {
+        const int q = r - C::BM, up = GATED && q >= HB ? 1 : 0, b = q - up * HB;
+        row = a.ws + p.rows.expert * a.expert_ws + ((int64_t)up * a.N + p.n0 + b) * a.ld_ws;
+        on = b < brows;
+      }
+      sc[i] = load_scales(row, 32 * s + id % 2 * 16, on ? kscales : 0);
+    }
+  };
+  auto keep_scales = [&](int s) __attribute__((always_inline)) {
+    char* base = lds + 2 * STAGE + (s & 1) * SCALES;
+#pragma unroll
+    for (int i = 0; i < S_LOADS; ++i) {
+      const int id = i * C::NT + tid, r = id / 2;
+      *(v4u32*)(base + r * 32 + ((id % 2) ^ (r / 8 % 2)) * 16) = sc[i];
+    }
+  };
+
+  const int lrow = lane & 31, lhalf = lane >> 5, rsw = (lrow / 2) % 8, ssw = lrow / 8 % 2;
+  f32x16 acc[C::FN][C::FM];
+#pragma unroll
+  for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  auto step = [&](int k, auto next_tag) __attribute__((always_inline)) {
+    constexpr int NEXT = decltype(next_tag)::value;   // 0 nothing, 1 a whole stage, 2 the last one
+    __builtin_amdgcn_s_waitcnt(0x70);                 // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    const char* sa = lds + (k & 1) * STAGE;
+    const char* sb = sa + A_BYTES;
+    const char* ss = lds + 2 * STAGE + (k / 4 & 1) * SCALES + (((k / 2 & 1) ^ ssw) * 16 + (k & 1) * 8 + lhalf * 4);
+    int sw[C::FN], sx[C::FM];
+    v4u32 pw[2][C::FN], px[2][C::FM];
+    auto fetch = [&](int kk) __attribute__((always_inline)) {
+      const int phys = ((4 * lhalf + kk) ^ rsw) * 16;
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i) pw[kk & 1][i] = *(const v4u32*)(sb + (block_row<C, GATED>(wave_n, i) + lrow) * 128 + phys);
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j) px[kk & 1][j] = *(const v4u32*)(sa + (wave_m * C::WM + 32 * j + lrow) * 128 + phys);
+    };
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) sw[i] = *(const int*)(ss + (C::BM + block_row<C, GATED>(wave_n, i) + lrow) * 32);
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) sx[j] = *(const int*)(ss + (wave_m * C::WM + 32 * j + lrow) * 32);
+    fetch(0);
+    if constexpr (NEXT == 1) issue(k + 1, std::false_type{});
+    if constexpr (NEXT == 2) issue(k + 1, std::true_type{});
+    if ((k & 3) == 0 && k + 4 < KT) fetch_scales(k / 4 + 1);
+    if ((k & 3) == 1 && k + 3 < KT) keep_scales(k / 4 + 1);
+    auto multiply = [&](auto kt) __attribute__((always_inline)) {
+      constexpr int kk = decltype(kt)::value;
+      if constexpr (kk < 3) fetch(kk + 1);
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) {
+          const v4u32 q = pw[kk & 1][i], r = px[kk & 1][j];
+          const i32x8 wq = {(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
+          const i32x8 xq = {(int)r[0], (int)r[1], (int)r[2], (int)r[3], 0, 0, 0, 0};
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wq, xq, acc[i][j], 4, 4, kk, sw[i], kk, sx[j]);
+        }
+    };
+    multiply(std::integral_constant<int, 0>{});
+    multiply(std::integral_constant<int, 1>{});
+    multiply(std::integral_constant<int, 2>{});
+    multiply(std::integral_constant<int, 3>{});
+  };
+  fetch_scales(0);
+  if (KT > 1) issue(0, std::false_type{});
+  else issue(0, std::true_type{});
+  keep_scales(0);
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  int k = 0;
+  for (; k + 2 < KT; ++k) step(k, I1{});
+  if (k + 1 < KT) step(k++, I2{});
+  step(k, I0{});
+  __builtin_amdgcn_s_waitcnt(0x70);
+  __builtin_amdgcn_s_barrier();   // every wave is done with the operands
+  finish_tile<C, GATED>(a, p, acc, lds, wave, lane);
 }
 
 // --- host -------------------------------------------------------------------
@@ -462,10 +739,28 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
   a.ld_out = d.ld_out;
   a.rows = d.rows;
   a.E = d.experts; a.N = d.cols; a.K = d.depth; a.act = d.act; a.out_type = d.out_dtype;
+  const bool gated = d.act == MOE_ACT_SWIGLU;
+  const int64_t each = d.rows / d.experts;
+  if (d.dtype == MOE_MXFP4 && each >= 64) {
+    auto go = [&](auto tile, auto g) {
+      using C = decltype(tile);
+      constexpr bool G = decltype(g)::value;
+      launch_tiles(a, C::BM, G ? C::BN / 2 : C::BN, C::NT,
+                   [&](dim3 grid) { hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a); });
+    };
+    if (each >= 512) {
+      if (gated) go(Mx256G{}, std::true_type{});
+      else go(Mx256{}, std::false_type{});
+    } else {
+      if (gated) go(Mx128{}, std::true_type{});
+      else go(Mx128{}, std::false_type{});
+    }
+    return hipGetLastError();
+  }
   with_x(d.dtype, [&](auto xt) {
     constexpr int XT = decltype(xt)::value;
     launch_tiles(a, 16, 16, kFewWaves * 64, [&](dim3 grid) {
-      if (d.act == MOE_ACT_SWIGLU) hipLaunchKernelGGL((few_rows_kernel<XT, true, 1, 1, 4>), grid, dim3(kFewWaves * 64), 0, s, a);
+      if (gated) hipLaunchKernelGGL((few_rows_kernel<XT, true, 1, 1, 4>), grid, dim3(kFewWaves * 64), 0, s, a);
       else hipLaunchKernelGGL((few_rows_kernel<XT, false, 1, 1, 4>), grid, dim3(kFewWaves * 64), 0, s, a);
     });
   });

@@ -246,7 +246,8 @@ def _apart(t, more, at=0):
 TYPES = [("bf16", "bf16"), ("f16", "f32"), ("mx", "bf16")]
 SIZES = [(1, 1, 32, 1), (1, 64, 2048, 1), (1, 200, 7168, 3), (2, 17, 64, 2), (5, 40, 96, 8), (8, 130, 1024, 64), (16, 48, 256, 1),
          (17, 100, 160, 4), (33, 36, 544, 2), (64, 96, 512, 128), (100, 250, 288, 5), (300, 130, 1056, 7), (700, 70, 128, 130),
-         (513, 300, 224, 1), (1000, 260, 544, 3)]
+         (513, 300, 224, 1), (1000, 260, 544, 3), (600, 300, 2336, 1), (200, 200, 2848, 2), (1300, 390, 1056, 2),
+         (5000, 130, 96, 6)]
 
 
 @pytest.mark.parametrize("act", ["none", "swiglu"])
