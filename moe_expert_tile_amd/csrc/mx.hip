@@ -431,13 +431,13 @@ typedef MxTile<256, 256, 2, 4> Mx256;
 typedef MxTile<256, 256, 4, 2> Mx256G;   // gated: each wave's columns hold as many gate as up ones
 typedef MxTile<128, 128, 2, 2> Mx128;
 
-// 16 bytes of a row's scales from byte `at` on, zeros past its `bytes`
-__device__ __forceinline__ v4u32 load_scales(const uint8_t* row, int at, int bytes) {
-  if (at + 16 <= bytes) return ((const Loose<v4u32, 1>*)(row + at))->v;
+// 16 bytes of a row's scales, zeros from byte `left` on
+__device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int left) {
+  if (left >= 16) return ((const Loose<v4u32, 1>*)p)->v;
   v4u32 v = {0, 0, 0, 0};
 #pragma unroll
   for (int c = 0; c < 15; ++c)
-    if (at + c < bytes) v[c / 4] |= (uint32_t)row[at + c] << (c % 4 * 8);
+    if (c < left) v[c / 4] |= (uint32_t)p[c] << (c % 4 * 8);
   return v;
 }
 
@@ -576,21 +576,28 @@ void mx_both_kernel(MxArgs a) {
   // scales of stages 4 s .. 4 s + 3: 32 bytes a row (x's rows, then w's), this thread's
   // 16-byte halves; halves of rows 8 .. 15 of 16 swapped, against bank conflicts
   v4u32 sc[S_LOADS];
-  auto fetch_scales = [&](int s) __attribute__((always_inline)) {
+  const uint8_t* srow[S_LOADS];
 #pragma unroll
-    for (int i = 0; i < S_LOADS; ++i) {
-      const int id = i * C::NT + tid, r = id / 2;
-      const uint8_t* row;
-      bool on;
-      if (r < C::BM) {
-        row = a.xs + (p.rows.row + r) * a.ld_xs;
-        on = r < arows;
-      } else {
-        const int q = r - C::BM, up = GATED && q >= HB ? 1 : 0, b = q - up * HB;
-        row = a.ws + p.rows.expert * a.expert_ws + ((int64_t)up * a.N + p.n0 + b) * a.ld_ws;
-        on = b < brows;
+  for (int i = 0; i < S_LOADS; ++i) {
+    const int id = i * C::NT + tid, r = id / 2;
+    if (r < C::BM) {   // rows past the last one: any scales, their results are not stored
+      srow[i] = a.xs + (p.rows.row + min(r, arows - 1)) * a.ld_xs + id % 2 * 16;
+    } else {
+      const int q = r - C::BM, up = GATED && q >= HB ? 1 : 0, b = min(q - up * HB, brows - 1);
+      srow[i] = a.ws + p.rows.expert * a.expert_ws + ((int64_t)up * a.N + p.n0 + b) * a.ld_ws + id % 2 * 16;
+    }
+  }
+  auto fetch_scales = [&](int s) __attribute__((always_inline)) {
+    if (32 * s + 32 <= kscales) {
+#pragma unroll
+      for (int i = 0; i < S_LOADS; ++i) sc[i] = ((const Loose<v4u32, 1>*)(srow[i] + 32 * s))->v;
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < S_LOADS; ++i) {
+        const v4u32 v = load_scales(srow[i] + 32 * s, kscales - 32 * s - (i * C::NT + tid) % 2 * 16);
+#pragma unroll
+        for (int j = 0; j < S_LOADS; ++j) sc[j] = j == i ? v : sc[j];
       }
-      sc[i] = load_scales(row, 32 * s + id % 2 * 16, on ? kscales : 0);
     }
   };
   auto keep_scales = [&](int s) __attribute__((always_inline)) {
@@ -615,6 +622,8 @@ void mx_both_kernel(MxArgs a) {
     constexpr int NEXT = decltype(next_tag)::value;   // 0 nothing, 1 a whole stage, 2 the last one
     __builtin_amdgcn_s_waitcnt(0x70);                 // vmcnt(0) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
+    if ((k & 3) == 0 && k + 4 < KT) fetch_scales(k / 4 + 1);
+    if ((k & 3) == 1 && k + 3 < KT) keep_scales(k / 4 + 1);
     const char* sa = lds + (k & 1) * STAGE;
     const char* sb = sa + A_BYTES;
     const char* ss = lds + 2 * STAGE + (k / 4 & 1) * SCALES + (((k / 2 & 1) ^ ssw) * 16 + (k & 1) * 8 + lhalf * 4);
@@ -634,8 +643,7 @@ void mx_both_kernel(MxArgs a) {
     fetch(0);
     if constexpr (NEXT == 1) issue(k + 1, std::false_type{});
     if constexpr (NEXT == 2) issue(k + 1, std::true_type{});
-    if ((k & 3) == 0 && k + 4 < KT) fetch_scales(k / 4 + 1);
-    if ((k & 3) == 1 && k + 3 < KT) keep_scales(k / 4 + 1);
+    __builtin_amdgcn_sched_barrier(0);
     auto multiply = [&](auto kt) __attribute__((always_inline)) {
       constexpr int kk = decltype(kt)::value;
       if constexpr (kk < 3) fetch(kk + 1);
@@ -653,6 +661,12 @@ void mx_both_kernel(MxArgs a) {
     multiply(std::integral_constant<int, 1>{});
     multiply(std::integral_constant<int, 2>{});
     multiply(std::integral_constant<int, 3>{});
+    // each MFMA step's operand reads before the previous step's MFMAs
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      if (kk < 3) __builtin_amdgcn_sched_group_barrier(0x100, C::FN + C::FM, 0);
+      __builtin_amdgcn_sched_group_barrier(0x8, C::FN * C::FM, 0);
+    }
   };
   fetch_scales(0);
   if (KT > 1) issue(0, std::false_type{});
@@ -665,6 +679,143 @@ void mx_both_kernel(MxArgs a) {
   for (; k + 2 < KT; ++k) step(k, I1{});
   if (k + 1 < KT) step(k++, I2{});
   step(k, I0{});
+  __builtin_amdgcn_s_waitcnt(0x70);
+  __builtin_amdgcn_s_barrier();   // every wave is done with the operands
+  finish_tile<C, GATED>(a, p, acc, lds, wave, lane);
+}
+
+// Weights alone in 4 bits.  They lie in LDS as in memory, 32 bytes of a row a
+// stage, and become 16-bit operands on the way out of it: a lane's block of 32
+// gives the four MFMA steps' parts, element groups of 8, so that a stage's
+// weights cost one 16-byte read for 32 rows and 16 conversions.  x's 16-byte chunk
+// 4 h + kk of a stage belongs to lane half h in step kk.
+template <class C, bool F16, bool GATED>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
+void mx_weights_kernel(MxArgs a) {
+  typedef typename Elem<F16>::v8 v8;
+  constexpr int STAGES = 3;
+  constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 32;
+  constexpr int SCALES = C::BN * 16;                        // eight stages' scales
+  constexpr int A_LOADS = C::BM / 8 / C::NW;
+  constexpr int RING = STAGES * STAGE + 2 * SCALES, LDS = RING > C::EPI ? RING : C::EPI;
+  static_assert(LDS <= 160 * 1024 && C::NW % 2 == 0 && C::BN == 32 * C::NW, "tile");
+  __shared__ __attribute__((aligned(1024))) char lds[LDS];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_m = wave / C::WN_, wave_n = wave % C::WN_;
+  constexpr int HB = GATED ? C::BN / 2 : C::BN;
+  Place p = place_of<C::BM, HB>(a);
+  p.rows.expert = __builtin_amdgcn_readfirstlane(p.rows.expert);
+  p.rows.count = __builtin_amdgcn_readfirstlane(p.rows.count);
+  p.rows.row = __builtin_amdgcn_readfirstlane((int)p.rows.row);
+  if (p.rows.count <= 0) return;
+  const int arows = p.rows.count, brows = p.cols;
+  const int kscales = a.K / 32;
+  const int KT = (a.K + 63) / 64, tail = a.K - (KT - 1) * 64;   // 32 or 64 elements
+
+  // this wavefront's 32 rows of w, all of one half of a gated tile
+  const int up = GATED && wave * 32 >= HB ? 1 : 0;
+  const char* w = a.w + p.rows.expert * a.expert_w + ((int64_t)up * a.N + p.n0) * a.ld_w;
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.x + p.rows.row * a.ld_x, (arows - 1) * a.ld_x + 2 * a.K);
+  const __amdgpu_buffer_rsrc_t br = make_rsrc(w, (brows - 1) * a.ld_w + a.K / 2);
+  uint32_t aoff[A_LOADS], boff;
+  const int chunk = (lane % 8) ^ ((wave * 4 + lane / 16) % 8);
+#pragma unroll
+  for (int i = 0; i < A_LOADS; ++i) {
+    const int r = (wave + i * C::NW) * 8 + lane / 8;
+    aoff[i] = r < arows ? (uint32_t)r * (uint32_t)a.ld_x + chunk * 16 : kPastEnd;
+  }
+  const int block = (lane % 2) ^ (lane / 16 % 2);           // blocks of rows 8 .. 15 of 16 swapped
+  {
+    const int r = wave * 32 - up * HB + lane / 2;
+    boff = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + block * 16 : kPastEnd;
+  }
+  auto issue = [&](int k, auto last_tag) __attribute__((always_inline)) {
+    constexpr bool LAST = decltype(last_tag)::value;
+    char* base = lds + (k % STAGES) * STAGE;
+#pragma unroll
+    for (int i = 0; i < A_LOADS; ++i)
+      load_lds(ar, base + (wave + i * C::NW) * 1024, !LAST || chunk * 8 < tail ? aoff[i] : kPastEnd, 128 * k);
+    load_lds(br, base + A_BYTES + wave * 1024, !LAST || block * 32 < tail ? boff : kPastEnd, 32 * k);
+  };
+  // scales of stages 8 s .. 8 s + 7: 16 bytes of w's row tid
+  v4u32 sc = {0, 0, 0, 0};
+  const int sup = GATED && tid >= HB ? 1 : 0;
+  const uint8_t* srow = a.ws + p.rows.expert * a.expert_ws +
+                        ((int64_t)sup * a.N + p.n0 + min(tid - sup * HB, brows - 1)) * a.ld_ws;
+  auto fetch_scales = [&](int s) __attribute__((always_inline)) {
+    if (C::NT > C::BN && tid >= C::BN) return;
+    if (16 * s + 16 <= kscales) sc = ((const Loose<v4u32, 1>*)(srow + 16 * s))->v;
+    else sc = load_scales(srow + 16 * s, kscales - 16 * s);
+  };
+  auto keep_scales = [&](int s) __attribute__((always_inline)) {
+    if (C::NT > C::BN && tid >= C::BN) return;
+    *(v4u32*)(lds + STAGES * STAGE + (s & 1) * SCALES + tid * 16) = sc;
+  };
+
+  const int lrow = lane & 31, lhalf = lane >> 5, rsw = (lrow / 2) % 8;
+  const int bat = lrow * 32 + (lhalf ^ (lrow / 8 % 2)) * 16;
+  f32x16 acc[C::FN][C::FM];
+#pragma unroll
+  for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  auto step = [&](int k, auto next_tag, auto flying_tag) __attribute__((always_inline)) {
+    constexpr int NEXT = decltype(next_tag)::value;   // 0 nothing, 1 a whole stage, 2 the last one
+    constexpr int FLYING = decltype(flying_tag)::value ? A_LOADS + 1 : 0;   // the next stage's loads
+    __builtin_amdgcn_s_waitcnt(0x70 | FLYING);        // vmcnt(FLYING) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    if ((k & 7) == 0 && k + 8 < KT) fetch_scales(k / 8 + 1);
+    if ((k & 7) == 4 && k + 4 < KT) keep_scales(k / 8 + 1);
+    const char* sa = lds + (k % STAGES) * STAGE;
+    const char* sb = sa + A_BYTES;
+    const uint8_t* ss = (const uint8_t*)lds + STAGES * STAGE + (k / 8 & 1) * SCALES + (k & 7) * 2 + lhalf;
+    float scale[C::FN];
+    v4u32 q[C::FN];
+    v8 px[2][C::FM];
+    auto fetch = [&](int kk) __attribute__((always_inline)) {
+      const int phys = ((4 * lhalf + kk) ^ rsw) * 16;
+#pragma unroll
+      for (int j = 0; j < C::FM; ++j) px[kk & 1][j] = *(const v8*)(sa + (wave_m * C::WM + 32 * j + lrow) * 128 + phys);
+    };
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) {
+      q[i] = *(const v4u32*)(sb + block_row<C, GATED>(wave_n, i) * 32 + bat);
+      scale[i] = scale_of(ss[(block_row<C, GATED>(wave_n, i) + lrow) * 16]);
+    }
+    fetch(0);
+    if constexpr (NEXT == 1) issue(k + STAGES - 1, std::false_type{});
+    if constexpr (NEXT == 2) issue(k + STAGES - 1, std::true_type{});
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      if (kk < 3) fetch(kk + 1);
+#pragma unroll
+      for (int i = 0; i < C::FN; ++i) {
+        const v8 wide = __builtin_bit_cast(v8, widen<F16>(q[i][kk], scale[i]));
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j) acc[i][j] = Elem<F16>::mfma32(wide, px[kk & 1][j], acc[i][j]);
+      }
+    }
+  };
+  fetch_scales(0);
+#pragma unroll
+  for (int k = 0; k < STAGES - 1; ++k) {
+    if (k + 1 < KT) issue(k, std::false_type{});
+    else if (k + 1 == KT) issue(k, std::true_type{});
+  }
+  keep_scales(0);
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  int k = 0;
+  for (; k + STAGES < KT; ++k) step(k, I1{}, std::true_type{});
+  if (k + STAGES - 1 < KT) step(k++, I2{}, std::true_type{});
+  if (k + 1 < KT) step(k++, I0{}, std::true_type{});
+  step(k, I0{}, std::false_type{});
   __builtin_amdgcn_s_waitcnt(0x70);
   __builtin_amdgcn_s_barrier();   // every wave is done with the operands
   finish_tile<C, GATED>(a, p, acc, lds, wave, lane);
@@ -741,12 +892,15 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
   a.E = d.experts; a.N = d.cols; a.K = d.depth; a.act = d.act; a.out_type = d.out_dtype;
   const bool gated = d.act == MOE_ACT_SWIGLU;
   const int64_t each = d.rows / d.experts;
-  if (d.dtype == MOE_MXFP4 && each >= 64) {
+  if (each >= 64) {
     auto go = [&](auto tile, auto g) {
       using C = decltype(tile);
       constexpr bool G = decltype(g)::value;
-      launch_tiles(a, C::BM, G ? C::BN / 2 : C::BN, C::NT,
-                   [&](dim3 grid) { hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a); });
+      launch_tiles(a, C::BM, G ? C::BN / 2 : C::BN, C::NT, [&](dim3 grid) {
+        if (d.dtype == MOE_MXFP4) hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a);
+        else if (d.dtype == MOE_F16) hipLaunchKernelGGL((mx_weights_kernel<C, true, G>), grid, dim3(C::NT), 0, s, a);
+        else hipLaunchKernelGGL((mx_weights_kernel<C, false, G>), grid, dim3(C::NT), 0, s, a);
+      });
     };
     if (each >= 512) {
       if (gated) go(Mx256G{}, std::true_type{});
