@@ -191,6 +191,18 @@ struct RowTile {
   int64_t row;
 };
 
+// inclusive sum over the wavefront's lanes: shifts inside rows of 16, then the
+// rows' last lanes broadcast on
+__device__ __forceinline__ int lane_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);    // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);    // 2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);    // 4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);    // 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
 // Row tiles of bm of all experts' rows.  Called by whole wavefronts.
 __device__ __forceinline__ int count_tiles(const MxArgs& a, int bm) {
   const int rows = (int)a.rows;
@@ -200,9 +212,7 @@ __device__ __forceinline__ int count_tiles(const MxArgs& a, int bm) {
     const int lo = min(max(a.offsets[e], 0), rows), hi = min(max(a.offsets[e + 1], 0), rows);
     n += hi > lo ? (hi - lo + bm - 1) / bm : 0;
   }
-#pragma unroll
-  for (int s = 32; s; s >>= 1) n += __shfl_xor(n, s);
-  return __builtin_amdgcn_readfirstlane(n);
+  return __builtin_amdgcn_readlane(lane_scan(n), 63);
 }
 
 // Row tile t of the experts' rows cut into pieces of bm, none of which holds
@@ -221,18 +231,11 @@ __device__ __forceinline__ RowTile find_tile(const MxArgs& a, int bm, int t) {
     const int lo = e < a.E ? min(max(a.offsets[e], 0), rows) : 0;
     const int hi = e < a.E ? min(max(a.offsets[e + 1], 0), rows) : 0;
     const int n = hi > lo ? (hi - lo + bm - 1) / bm : 0;
-    int upto = n;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int o = __shfl_up(upto, s);
-      if (lane >= s) upto += o;
-    }
-    const int all = __shfl(upto, 63);
+    const int upto = lane_scan(n), all = __builtin_amdgcn_readlane(upto, 63);
     if (t < done + all) {
-      const uint64_t past = __ballot(t < done + upto);
-      const int l = __builtin_ctzll(past);
-      const int first = __shfl(lo, l), last = __shfl(hi, l), before = done + __shfl(upto - n, l);
-      const int row = first + (t - before) * bm;
+      const int l = __builtin_ctzll(__ballot(t < done + upto));
+      const int first = __builtin_amdgcn_readlane(lo, l), last = __builtin_amdgcn_readlane(hi, l);
+      const int row = first + (t - done - __builtin_amdgcn_readlane(upto - n, l)) * bm;
       return {e0 + l, min(bm, last - row), row};
     }
     done += all;
@@ -254,54 +257,63 @@ __device__ __forceinline__ void store_row(int type, char* base, int64_t at, int 
   else store16<false>((uint16_t*)base + at, left, v);
 }
 
+// 16 bytes of a row's scales, zeros from byte `left` on
+__device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int left) {
+  if (left >= 16) return ((const Loose<v4u32, 1>*)p)->v;
+  v4u32 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < 15; ++c)
+    if (c < left) v[c / 4] |= (uint32_t)p[c] << (c % 4 * 8);
+  return v;
+}
+
 // --- few rows -------------------------------------------------------------------
 //
 // Bound by reading the weights, which every (row tile, column tile) workgroup
 // does once, straight into operand registers.  A workgroup owns 16 TT rows of
 // one expert and 16 NB output columns (gated: 16 NB gate and up rows of w); its
-// wavefronts take K in steps of 128 in turn and join their sums in LDS.
-// Operand lane layout: row lane % 16, block lane / 16 of a step; with 16-bit
-// operands dword i of the block is the lane's part of the step's i-th
-// v_mfma_f32_16x16x32.  Result lane: row (of x) lane % 16, columns 4 (lane / 16) .. + 3.
-constexpr int kFewWaves = 8;
-
-template <int XT, bool GATED, int TT, int NB, int U>
-__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(MxArgs a) {
+// wavefronts take K in pieces of 512, 256 contiguous bytes of each weight row, in
+// turn and join their sums in LDS.  A piece is four steps of 128: a lane holds
+// row lane % 16, block lane / 16 of each; with 16-bit operands dword i of the
+// block is the lane's part of the step's i-th v_mfma_f32_16x16x32.  A row's 16
+// scales of a piece are one load, of which step s needs byte lane / 16 of dword s.
+// Result lane: row (of x) lane % 16, columns 4 (lane / 16) .. + 3.
+template <int XT, bool GATED, int TT, int NB, int W>
+__global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
   constexpr bool MX = XT == MOE_MXFP4, F16 = XT == MOE_F16;
   constexpr int G = GATED ? 2 : 1, XL = MX ? 1 : 4;      // 16-byte loads of a block of x
-  __shared__ float4 part[kFewWaves][G * NB][TT][64];
+  constexpr int AHEAD = MX ? 4 : 1;                      // steps of x in registers
+  __shared__ float4 part[W][G * NB][TT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int n_nt = a.n_nt;
-  const RowTile tile = find_tile(a, 16 * TT, blockIdx.x / n_nt);
+  const RowTile tile = find_tile(a, 16 * TT, blockIdx.x / a.n_nt);
   const int expert = __builtin_amdgcn_readfirstlane(tile.expert), rows = __builtin_amdgcn_readfirstlane(tile.count);
   const int64_t row0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)tile.row);
   if (rows <= 0) return;
-  const int n0 = (a.nt0 + (int)(blockIdx.x % n_nt)) * 16 * NB;
+  const int n0 = (a.nt0 + (int)(blockIdx.x % a.n_nt)) * 16 * NB;
   const int r = lane & 15, g = lane >> 4;
   const int cols = min(16 * NB, a.N - n0);
-  const char* w = a.w + expert * a.expert_w + n0 * a.ld_w;
-  const uint8_t* ws = a.ws + expert * a.expert_ws + n0 * a.ld_ws;
-  __amdgpu_buffer_rsrc_t wr[G], sr[G];
+  __amdgpu_buffer_rsrc_t wr[G];
+  const uint8_t* ws[G];
 #pragma unroll
   for (int h = 0; h < G; ++h) {
-    wr[h] = make_rsrc(w + (int64_t)h * a.N * a.ld_w, (cols - 1) * a.ld_w + a.K / 2);
-    sr[h] = make_rsrc(ws + (int64_t)h * a.N * a.ld_ws, (cols - 1) * a.ld_ws + a.K / 32);
+    const int64_t n = (int64_t)h * a.N + n0;
+    wr[h] = make_rsrc(a.w + expert * a.expert_w + n * a.ld_w, (cols - 1) * a.ld_w + a.K / 2);
+    ws[h] = a.ws + expert * a.expert_ws + n * a.ld_ws;
   }
   const int row_bytes = MX ? a.K / 2 : a.K * 2;
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + row0 * a.ld_x, (rows - 1) * a.ld_x + row_bytes);
-  const __amdgpu_buffer_rsrc_t xsr = make_rsrc(MX ? a.xs + row0 * a.ld_xs : nullptr, MX ? (rows - 1) * a.ld_xs + a.K / 32 : 0);
-  uint32_t w_off[NB], s_off[NB], x_off[TT], xs_off[TT];
+  const uint8_t* xs = MX ? a.xs + row0 * a.ld_xs : nullptr;
+  // rows past the last one: no data; any scales, their results are not stored
+  uint32_t w_off[NB], x_off[TT], s_off[NB], xs_off[TT];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const bool on = 16 * b + r < cols;
-    w_off[b] = on ? (uint32_t)(16 * b + r) * (uint32_t)a.ld_w + 16 * g : kPastEnd;
-    s_off[b] = on ? (uint32_t)(16 * b + r) * (uint32_t)a.ld_ws + g : kPastEnd;
+    w_off[b] = 16 * b + r < cols ? (uint32_t)(16 * b + r) * (uint32_t)a.ld_w + 16 * g : kPastEnd;
+    s_off[b] = (uint32_t)min(16 * b + r, cols - 1) * (uint32_t)a.ld_ws;
   }
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
-    const bool on = 16 * i + r < rows;
-    x_off[i] = on ? (uint32_t)(16 * i + r) * (uint32_t)a.ld_x + 16 * XL * g : kPastEnd;
-    xs_off[i] = on ? (uint32_t)(16 * i + r) * (uint32_t)a.ld_xs + g : kPastEnd;
+    x_off[i] = 16 * i + r < rows ? (uint32_t)(16 * i + r) * (uint32_t)a.ld_x + 16 * XL * g : kPastEnd;
+    xs_off[i] = MX ? (uint32_t)min(16 * i + r, rows - 1) * (uint32_t)a.ld_xs : 0;
   }
   f32x4 acc[G][NB][TT];
 #pragma unroll
@@ -310,60 +322,78 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(MxArgs a) {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < TT; ++i) acc[h][b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = wave * 128; k0 < a.K; k0 += kFewWaves * 128 * U) {
-    v4u32 wv[U][G][NB], xv[U][TT][XL];
-    uint32_t sv[U][G][NB], xsv[U][TT];
+  auto piece = [&](int k0, auto whole_tag) __attribute__((always_inline)) {
+    constexpr bool WHOLE = decltype(whole_tag)::value;
+    v4u32 wv[4][G][NB], xv[AHEAD][TT][XL], sv[G][NB], xsv[TT];
+    // scales of the piece; past K's end zeros, since a NaN there would count
+    auto scales = [&](const uint8_t* p) __attribute__((always_inline)) {
+      if constexpr (WHOLE) return ((const Loose<v4u32, 1>*)(p + k0 / 32))->v;
+      else return load_scales(p + k0 / 32, (a.K - k0) / 32);
+    };
 #pragma unroll
-    for (int s = 0; s < U; ++s) {
-      const int k = k0 + s * kFewWaves * 128;
-      const bool in = k + 32 * g < a.K;      // a lane's block is whole or absent
-      auto at = [&](uint32_t off, int step) __attribute__((always_inline)) {
-        return (int)(in && off != kPastEnd ? off + step : kPastEnd);
-      };
+    for (int h = 0; h < G; ++h)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) sv[h][b] = scales(ws[h] + s_off[b]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int k = k0 + s * 128;
+      const bool in = WHOLE || k + 32 * g < a.K;      // a lane's block is whole or absent
 #pragma unroll
       for (int h = 0; h < G; ++h)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          wv[s][h][b] = __builtin_amdgcn_raw_buffer_load_b128(wr[h], at(w_off[b], k / 2), 0, 0);
-          sv[s][h][b] = __builtin_amdgcn_raw_buffer_load_b8(sr[h], at(s_off[b], k / 32), 0, 0);
-        }
+        for (int b = 0; b < NB; ++b)
+          wv[s][h][b] = __builtin_amdgcn_raw_buffer_load_b128(wr[h], (int)(in ? w_off[b] + k / 2 : kPastEnd), 0, 0);
+    }
 #pragma unroll
-      for (int i = 0; i < TT; ++i) {
+    for (int i = 0; i < TT; ++i)
+      if constexpr (MX) xsv[i] = scales(xs + xs_off[i]);
+    auto rows_of = [&](int s) __attribute__((always_inline)) {
+      const int k = k0 + s * 128;
+      const bool in = WHOLE || k + 32 * g < a.K;
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
 #pragma unroll
         for (int c = 0; c < XL; ++c)
-          xv[s][i][c] = __builtin_amdgcn_raw_buffer_load_b128(xr, at(x_off[i], MX ? k / 2 : k * 2 + 16 * c), 0, 0);
-        xsv[s][i] = MX ? __builtin_amdgcn_raw_buffer_load_b8(xsr, at(xs_off[i], k / 32), 0, 0) : 0;
-      }
-    }
+          xv[s % AHEAD][i][c] = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(in ? x_off[i] + (MX ? k / 2 : k * 2) + 16 * c : kPastEnd), 0, 0);
+    };
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) rows_of(s);
     __builtin_amdgcn_sched_barrier(0);   // all of them, before the first is waited for
 #pragma unroll
-    for (int s = 0; s < U; ++s)
+    for (int s = 0; s < 4; ++s) {
 #pragma unroll
       for (int h = 0; h < G; ++h)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const v4u32 q = wv[s][h][b];
+          const uint32_t sw = sv[h][b][s] >> (8 * g) & 0xff;
           if constexpr (MX) {
             const i32x8 wq = {(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
-              const v4u32 p = xv[s][i][0];
+              const v4u32 p = xv[s % AHEAD][i][0];
               const i32x8 xq = {(int)p[0], (int)p[1], (int)p[2], (int)p[3], 0, 0, 0, 0};
-              acc[h][b][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wq, xq, acc[h][b][i], 4, 4, 0, (int)sv[s][h][b],
-                                                                               0, (int)xsv[s][i]);
+              acc[h][b][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wq, xq, acc[h][b][i], 4, 4, 0, (int)sw, 0,
+                                                                               (int)(xsv[i][s] >> (8 * g) & 0xff));
             }
           } else {
             typedef typename Elem<F16>::v8 v8;
-            const float scale = scale_of(sv[s][h][b]);
+            const float scale = scale_of(sw);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const v8 wide = __builtin_bit_cast(v8, widen<F16>(q[c], scale));
 #pragma unroll
               for (int i = 0; i < TT; ++i)
-                acc[h][b][i] = Elem<F16>::mfma16(wide, __builtin_bit_cast(v8, xv[s][i][c]), acc[h][b][i]);
+                acc[h][b][i] = Elem<F16>::mfma16(wide, __builtin_bit_cast(v8, xv[s % AHEAD][i][c]), acc[h][b][i]);
             }
           }
         }
+      if (s + AHEAD < 4) rows_of(s + AHEAD);
+    }
+  };
+  for (int k0 = wave * 512; k0 < a.K; k0 += W * 512) {
+    if (k0 + 512 <= a.K) piece(k0, std::true_type{});
+    else piece(k0, std::false_type{});
   }
 #pragma unroll
   for (int h = 0; h < G; ++h)
@@ -373,11 +403,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(MxArgs a) {
       for (int i = 0; i < TT; ++i)
         part[wave][h * NB + b][i][lane] = make_float4(acc[h][b][i][0], acc[h][b][i][1], acc[h][b][i][2], acc[h][b][i][3]);
   __syncthreads();
-  for (int j = wave; j < NB * TT; j += kFewWaves) {
+  for (int j = wave; j < NB * TT; j += W) {
     const int b = j / TT, i = j % TT;
     float z[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f}, y[4];
 #pragma unroll
-    for (int v = 0; v < kFewWaves; ++v) {
+    for (int v = 0; v < W; ++v) {
       const float4 p = part[v][b][i][lane];
       z[0] += p.x; z[1] += p.y; z[2] += p.z; z[3] += p.w;
       if constexpr (GATED) {
@@ -430,16 +460,7 @@ struct MxTile {
 typedef MxTile<256, 256, 2, 4> Mx256;
 typedef MxTile<256, 256, 4, 2> Mx256G;   // gated: each wave's columns hold as many gate as up ones
 typedef MxTile<128, 128, 2, 2> Mx128;
-
-// 16 bytes of a row's scales, zeros from byte `left` on
-__device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int left) {
-  if (left >= 16) return ((const Loose<v4u32, 1>*)p)->v;
-  v4u32 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int c = 0; c < 15; ++c)
-    if (c < left) v[c / 4] |= (uint32_t)p[c] << (c % 4 * 8);
-  return v;
-}
+typedef MxTile<64, 128, 2, 2> Mx64;
 
 // A workgroup's tile: its place among the row and column tiles.  Workgroup i runs
 // on XCD i mod 8; each XCD gets a contiguous run, in which 8 row tiles x 4 column
@@ -528,7 +549,7 @@ void mx_both_kernel(MxArgs a) {
   constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 128;
   constexpr int SCALES = (C::BM + C::BN) * 32;              // four stages' scales
   constexpr int A_LOADS = C::BM / 8 / C::NW, B_LOADS = C::BN / 8 / C::NW;
-  constexpr int S_LOADS = SCALES / 16 / C::NT;
+  constexpr int S_CHUNKS = SCALES / 16, S_LOADS = (S_CHUNKS + C::NT - 1) / C::NT;
   constexpr int LDS = 2 * STAGE + 2 * SCALES;
   static_assert(LDS >= C::EPI && LDS <= 160 * 1024 && C::NW % 2 == 0 && B_LOADS % 2 == 0, "tile");
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
@@ -579,7 +600,7 @@ void mx_both_kernel(MxArgs a) {
   const uint8_t* srow[S_LOADS];
 #pragma unroll
   for (int i = 0; i < S_LOADS; ++i) {
-    const int id = i * C::NT + tid, r = id / 2;
+    const int id = min(i * C::NT + tid, S_CHUNKS - 1), r = id / 2;
     if (r < C::BM) {   // rows past the last one: any scales, their results are not stored
       srow[i] = a.xs + (p.rows.row + min(r, arows - 1)) * a.ld_xs + id % 2 * 16;
     } else {
@@ -594,7 +615,7 @@ void mx_both_kernel(MxArgs a) {
     } else {
 #pragma unroll 1
       for (int i = 0; i < S_LOADS; ++i) {
-        const v4u32 v = load_scales(srow[i] + 32 * s, kscales - 32 * s - (i * C::NT + tid) % 2 * 16);
+        const v4u32 v = load_scales(srow[i] + 32 * s, kscales - 32 * s - min(i * C::NT + tid, S_CHUNKS - 1) % 2 * 16);
 #pragma unroll
         for (int j = 0; j < S_LOADS; ++j) sc[j] = j == i ? v : sc[j];
       }
@@ -604,7 +625,7 @@ void mx_both_kernel(MxArgs a) {
     char* base = lds + 2 * STAGE + (s & 1) * SCALES;
 #pragma unroll
     for (int i = 0; i < S_LOADS; ++i) {
-      const int id = i * C::NT + tid, r = id / 2;
+      const int id = min(i * C::NT + tid, S_CHUNKS - 1), r = id / 2;
       *(v4u32*)(base + r * 32 + ((id % 2) ^ (r / 8 % 2)) * 16) = sc[i];
     }
   };
@@ -843,6 +864,25 @@ QuantArgs quant_args(int64_t rows, int depth, const void* x, int size, int64_t l
   return a;
 }
 
+template <class F>
+void with_flag(bool b, F f) {
+  if (b) f(std::true_type{});
+  else f(std::false_type{});
+}
+
+enum MxKind { FEW, T64, T128, T256 };
+struct MxChoice {
+  MxKind kind;
+  int tt, nb, waves;   // FEW
+};
+
+MxChoice choose_mx(const moe_mx_linear_desc& d) {
+  const int64_t each = d.rows / d.experts;
+  if (each >= 512) return {T256, 0, 0, 0};
+  if (each >= 64) return {T128, 0, 0, 0};
+  return {FEW, 1, 1, 8};
+}
+
 // column tiles of `width` and row tiles of `bm` in launches of fewer than 2^31 threads
 template <class F>
 void launch_tiles(MxArgs& a, int bm, int width, int threads, F go) {
@@ -890,33 +930,44 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
   a.ld_out = d.ld_out;
   a.rows = d.rows;
   a.E = d.experts; a.N = d.cols; a.K = d.depth; a.act = d.act; a.out_type = d.out_dtype;
-  const bool gated = d.act == MOE_ACT_SWIGLU;
-  const int64_t each = d.rows / d.experts;
-  if (each >= 64) {
-    auto go = [&](auto tile, auto g) {
-      using C = decltype(tile);
-      constexpr bool G = decltype(g)::value;
-      launch_tiles(a, C::BM, G ? C::BN / 2 : C::BN, C::NT, [&](dim3 grid) {
-        if (d.dtype == MOE_MXFP4) hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a);
-        else if (d.dtype == MOE_F16) hipLaunchKernelGGL((mx_weights_kernel<C, true, G>), grid, dim3(C::NT), 0, s, a);
-        else hipLaunchKernelGGL((mx_weights_kernel<C, false, G>), grid, dim3(C::NT), 0, s, a);
+  const MxChoice c = choose_mx(d);
+  with_flag(d.act == MOE_ACT_SWIGLU, [&](auto g) {
+    constexpr bool G = decltype(g)::value;
+    if (c.kind == FEW) {
+      with_x(d.dtype, [&](auto xt) {
+        constexpr int XT = decltype(xt)::value;
+        auto go = [&](auto tt, auto nb, auto waves) {
+          constexpr int TT = decltype(tt)::value, NB = decltype(nb)::value, W = decltype(waves)::value;
+          launch_tiles(a, 16 * TT, 16 * NB, W * 64, [&](dim3 grid) {
+            hipLaunchKernelGGL((few_rows_kernel<XT, G, TT, NB, W>), grid, dim3(W * 64), 0, s, a);
+          });
+        };
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        using Four = std::integral_constant<int, 4>;
+        using Eight = std::integral_constant<int, 8>;
+        if (c.tt == 2) {
+          if (c.waves == 8) go(Two{}, One{}, Eight{});
+          else go(Two{}, One{}, Four{});
+        } else {
+          if (c.waves == 8) go(One{}, One{}, Eight{});
+          else if (c.nb == 2) go(One{}, Two{}, Four{});
+          else go(One{}, One{}, Four{});
+        }
       });
-    };
-    if (each >= 512) {
-      if (gated) go(Mx256G{}, std::true_type{});
-      else go(Mx256{}, std::false_type{});
     } else {
-      if (gated) go(Mx128{}, std::true_type{});
-      else go(Mx128{}, std::false_type{});
+      auto go = [&](auto tile) {
+        using C = decltype(tile);
+        launch_tiles(a, C::BM, G ? C::BN / 2 : C::BN, C::NT, [&](dim3 grid) {
+          if (d.dtype == MOE_MXFP4) hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a);
+          else if (d.dtype == MOE_F16) hipLaunchKernelGGL((mx_weights_kernel<C, true, G>), grid, dim3(C::NT), 0, s, a);
+          else hipLaunchKernelGGL((mx_weights_kernel<C, false, G>), grid, dim3(C::NT), 0, s, a);
+        });
+      };
+      if (c.kind == T64) go(Mx64{});
+      else if (c.kind == T128) go(Mx128{});
+      else go(std::conditional_t<G, Mx256G, Mx256>{});
     }
-    return hipGetLastError();
-  }
-  with_x(d.dtype, [&](auto xt) {
-    constexpr int XT = decltype(xt)::value;
-    launch_tiles(a, 16, 16, kFewWaves * 64, [&](dim3 grid) {
-      if (gated) hipLaunchKernelGGL((few_rows_kernel<XT, true, 1, 1, 4>), grid, dim3(kFewWaves * 64), 0, s, a);
-      else hipLaunchKernelGGL((few_rows_kernel<XT, false, 1, 1, 4>), grid, dim3(kFewWaves * 64), 0, s, a);
-    });
   });
   return hipGetLastError();
 }
