@@ -441,11 +441,11 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
 // --- tiles ----------------------------------------------------------------------
 //
 // Many rows: tiles of BM rows of one expert x BN rows of w, staged through LDS by
-// direct-to-LDS buffer loads, v_mfma_*_32x32 out of it.  A stage is 128 bytes of
+// direct-to-LDS buffer loads, MFMAs out of it.  A stage is 128 bytes of
 // each row of x: 256 elements in 4 bits, 64 in 16, and as many elements of w.
 // Rows past an operand's end and blocks past K get an offset past the buffer
 // descriptor's bound, where loads return zeros.  Scales come through registers
-// (their rows may start at any byte), 32 bytes of a row at a time, into a table of
+// (their rows may start at any byte), some stages' at a time, into a table of
 // their own in LDS, ahead of the stages that need them.
 
 template <int BM_, int BN_, int WAVES_M, int WAVES_N>
@@ -453,12 +453,10 @@ struct MxTile {
   static constexpr int BM = BM_, BN = BN_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64, WN_ = WAVES_N;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
-  static constexpr int FM = WM / 32, FN = WN / 32;
-  static constexpr int PITCH = FN * 32 + 4;       // floats of a row in the epilogue's staging
+  static constexpr int PITCH = WN + 4;            // floats of a row in the epilogue's staging
   static constexpr int EPI = NW * 32 * PITCH * 4;
 };
 typedef MxTile<256, 256, 2, 4> Mx256;
-typedef MxTile<256, 256, 4, 2> Mx256G;   // gated: each wave's columns hold as many gate as up ones
 typedef MxTile<128, 128, 2, 2> Mx128;
 typedef MxTile<64, 128, 2, 2> Mx64;
 
@@ -466,49 +464,54 @@ typedef MxTile<64, 128, 2, 2> Mx64;
 // on XCD i mod 8; each XCD gets a contiguous run, in which 8 row tiles x 4 column
 // tiles share their operands in its L2.
 struct Place {
-  RowTile rows;
-  int n0, cols;      // output columns
+  int expert, rows;     // rows: of the tile, 0 if there is none
+  int64_t row;
+  int n0, cols;         // output columns
 };
 template <int BM, int HB>
 __device__ __forceinline__ Place place_of(const MxArgs& a) {
   const int n_mt = count_tiles(a, BM), total = n_mt * a.n_nt;
-  if ((int)blockIdx.x >= total) return {{0, 0, 0}, 0, 0};
+  if ((int)blockIdx.x >= total) return {0, 0, 0, 0, 0};
   int t = xcd_order(blockIdx.x, total);
   const int grp = t / (8 * a.n_nt), rows8 = min(8, n_mt - grp * 8);
   t -= grp * 8 * a.n_nt;
-  RowTile r = find_tile(a, BM, grp * 8 + t % rows8);
+  const RowTile r = find_tile(a, BM, grp * 8 + t % rows8);
   const int n0 = (a.nt0 + t / rows8) * HB;
-  return {r, n0, min(HB, a.N - n0)};
+  return {__builtin_amdgcn_readfirstlane(r.expert), __builtin_amdgcn_readfirstlane(r.count),
+          __builtin_amdgcn_readfirstlane((int)r.row), n0, min(HB, a.N - n0)};
+}
+
+// first row of w, inside the tile, of a wavefront's i-th block of B; gated: the first
+// half of its blocks are gate rows, the others up rows
+template <class C, bool GATED, int B>
+__device__ __forceinline__ int block_row(int wave_n, int i) {
+  constexpr int HALF = C::WN / 2;
+  if constexpr (GATED) return B * i < HALF ? wave_n * HALF + B * i : C::BN / 2 + wave_n * HALF + B * i - HALF;
+  else return wave_n * C::WN + B * i;
 }
 
 // 32 rows of a wavefront's columns at a time go through LDS, so that lanes hold
 // neighbouring columns and every global access covers whole lines.
-template <class C, bool GATED>
-__device__ __forceinline__ void finish_tile(const MxArgs& a, const Place& p, f32x16 (&acc)[C::FN][C::FM], char* lds,
-                                            int wave, int lane) {
-  constexpr int FG = GATED ? C::FN / 2 : C::FN, CW = FG * 32, G = GATED ? 2 : 1;
+// put(j, to): the sums of rows 32 j .. + 31 to `to`, rows C::PITCH floats apart.
+template <class C, bool GATED, class Put>
+__device__ __forceinline__ void finish_tile(const MxArgs& a, const Place& p, char* lds, int wave, int lane, Put put) {
+  constexpr int CW = GATED ? C::WN / 2 : C::WN, G = GATED ? 2 : 1;
   float* stage = (float*)lds + wave * 32 * C::PITCH;
   const int wave_m = wave / C::WN_, wave_n = wave % C::WN_;
   constexpr int LPR = CW / 8, RPP = 64 / LPR;   // lanes a row (8 columns each), rows a pass
-  const int lrow = lane & 31, lhalf = lane >> 5;
   const int er = lane / LPR, ec = (lane % LPR) * 8;
   const int n = p.n0 + wave_n * CW + ec, left = a.N - n;
   float bz[8], bu[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) bz[c] = bu[c] = 0.f;
   if (a.bias && left > 0) {
-    const int64_t at = (int64_t)p.rows.expert * G * a.N + n;
+    const int64_t at = (int64_t)p.expert * G * a.N + n;
     load_row(a.out_type, a.bias, at, left, bz);
     if constexpr (GATED) load_row(a.out_type, a.bias, at + a.N, left, bu);
   }
 #pragma unroll
-  for (int j = 0; j < C::FM; ++j) {
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(float4*)(stage + lrow * C::PITCH + 32 * i + 8 * q + 4 * lhalf) =
-            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+  for (int j = 0; j < C::WM / 32; ++j) {
+    put(j, stage);
     __builtin_amdgcn_wave_barrier();
     auto staged8 = [&](int r, int col, float (&v)[8]) __attribute__((always_inline)) {
       const float4 x = *(const float4*)(stage + r * C::PITCH + col), y = *(const float4*)(stage + r * C::PITCH + col + 4);
@@ -520,24 +523,17 @@ __device__ __forceinline__ void finish_tile(const MxArgs& a, const Place& p, f32
       float z[8], u[8], y[8];
       staged8(r, ec, z);
       if constexpr (GATED) staged8(r, CW + ec, u);
-      if (m >= p.rows.count || left <= 0) continue;
+      if (m >= p.rows || left <= 0) continue;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         z[c] += bz[c];
         if constexpr (GATED) y[c] = z[c] * logistic(z[c]) * (u[c] + bu[c]);
       }
       if constexpr (!GATED) activate_all(a.act, z, y);
-      store_row(a.out_type, a.out, (p.rows.row + m) * a.ld_out + n, left, y);
+      store_row(a.out_type, a.out, (p.row + m) * a.ld_out + n, left, y);
     }
     __builtin_amdgcn_wave_barrier();
   }
-}
-
-// first row of w, inside the tile, of a wavefront's i-th block of 32
-template <class C, bool GATED>
-__device__ __forceinline__ int block_row(int wave_n, int i) {
-  if constexpr (GATED) return i < C::FN / 2 ? wave_n * (C::WN / 2) + 32 * i : C::BN / 2 + wave_n * (C::WN / 2) + 32 * (i - C::FN / 2);
-  else return wave_n * C::WN + 32 * i;
 }
 
 // Both operands in 4 bits.  A stage's 16-byte chunks (one block each) of row r lie
@@ -546,29 +542,26 @@ __device__ __forceinline__ int block_row(int wave_n, int i) {
 template <class C, bool GATED>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
 void mx_both_kernel(MxArgs a) {
+  constexpr int FM = C::WM / 32, FN = C::WN / 32;           // blocks of v_mfma_scale_f32_32x32x64
   constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 128;
   constexpr int SCALES = (C::BM + C::BN) * 32;              // four stages' scales
   constexpr int A_LOADS = C::BM / 8 / C::NW, B_LOADS = C::BN / 8 / C::NW;
   constexpr int S_CHUNKS = SCALES / 16, S_LOADS = (S_CHUNKS + C::NT - 1) / C::NT;
   constexpr int LDS = 2 * STAGE + 2 * SCALES;
-  static_assert(LDS >= C::EPI && LDS <= 160 * 1024 && C::NW % 2 == 0 && B_LOADS % 2 == 0, "tile");
+  static_assert(LDS >= C::EPI && LDS <= 160 * 1024 && C::NW % 2 == 0 && B_LOADS % 2 == 0 && FN % 2 == 0, "tile");
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wave_m = wave / C::WN_, wave_n = wave % C::WN_;
   constexpr int HB = GATED ? C::BN / 2 : C::BN;
-  Place p = place_of<C::BM, HB>(a);
-  p.rows.expert = __builtin_amdgcn_readfirstlane(p.rows.expert);
-  p.rows.count = __builtin_amdgcn_readfirstlane(p.rows.count);
-  p.rows.row = __builtin_amdgcn_readfirstlane((int)p.rows.row);
-  if (p.rows.count <= 0) return;
-  const int arows = p.rows.count, brows = p.cols;
+  const Place p = place_of<C::BM, HB>(a);
+  if (p.rows <= 0) return;
+  const int arows = p.rows, brows = p.cols;
   const int kbytes = a.K / 2, kscales = a.K / 32;
-  const int KT = (kbytes + 127) / 128, tail = kbytes - (KT - 1) * 128;
+  const int KT = (kbytes + 127) / 128;
 
-  const char* w = a.w + p.rows.expert * a.expert_w + p.n0 * a.ld_w;
-  const char* x = a.x + p.rows.row * a.ld_x;
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(x, (arows - 1) * a.ld_x + kbytes);
+  const char* w = a.w + p.expert * a.expert_w + p.n0 * a.ld_w;
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.x + p.row * a.ld_x, (arows - 1) * a.ld_x + kbytes);
   const __amdgpu_buffer_rsrc_t br = make_rsrc(w, (brows - 1) * a.ld_w + kbytes);
   const __amdgpu_buffer_rsrc_t ur = GATED ? make_rsrc(w + a.N * a.ld_w, (brows - 1) * a.ld_w + kbytes) : br;
   uint32_t aoff[A_LOADS], boff[B_LOADS];
@@ -583,10 +576,9 @@ void mx_both_kernel(MxArgs a) {
     const int r = (wave + (GATED ? i % (B_LOADS / 2) : i) * C::NW) * 8 + lane / 8;   // the second half: up rows
     boff[i] = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + chunk * 16 : kPastEnd;
   }
-  auto issue = [&](int k, auto last_tag) __attribute__((always_inline)) {
-    constexpr bool LAST = decltype(last_tag)::value;
+  auto issue = [&](int k) __attribute__((always_inline)) {
     char* base = lds + (k & 1) * STAGE;
-    const bool on = !LAST || chunk * 16 < tail;
+    const bool on = chunk * 16 < kbytes - 128 * k;     // past K's end: zeros
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i)
       load_lds(ar, base + (wave + i * C::NW) * 1024, on ? aoff[i] : kPastEnd, 128 * k);
@@ -602,10 +594,10 @@ void mx_both_kernel(MxArgs a) {
   for (int i = 0; i < S_LOADS; ++i) {
     const int id = min(i * C::NT + tid, S_CHUNKS - 1), r = id / 2;
     if (r < C::BM) {   // rows past the last one: any scales, their results are not stored
-      srow[i] = a.xs + (p.rows.row + min(r, arows - 1)) * a.ld_xs + id % 2 * 16;
+      srow[i] = a.xs + (p.row + min(r, arows - 1)) * a.ld_xs + id % 2 * 16;
     } else {
       const int q = r - C::BM, up = GATED && q >= HB ? 1 : 0, b = min(q - up * HB, brows - 1);
-      srow[i] = a.ws + p.rows.expert * a.expert_ws + ((int64_t)up * a.N + p.n0 + b) * a.ld_ws + id % 2 * 16;
+      srow[i] = a.ws + p.expert * a.expert_ws + ((int64_t)up * a.N + p.n0 + b) * a.ld_ws + id % 2 * 16;
     }
   }
   auto fetch_scales = [&](int s) __attribute__((always_inline)) {
@@ -631,16 +623,15 @@ void mx_both_kernel(MxArgs a) {
   };
 
   const int lrow = lane & 31, lhalf = lane >> 5, rsw = (lrow / 2) % 8, ssw = lrow / 8 % 2;
-  f32x16 acc[C::FN][C::FM];
+  f32x16 acc[FN][FM];
 #pragma unroll
-  for (int i = 0; i < C::FN; ++i)
+  for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j)
+    for (int j = 0; j < FM; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  auto step = [&](int k, auto next_tag) __attribute__((always_inline)) {
-    constexpr int NEXT = decltype(next_tag)::value;   // 0 nothing, 1 a whole stage, 2 the last one
+  auto step = [&](int k) __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(0x70);                 // vmcnt(0) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     if ((k & 3) == 0 && k + 4 < KT) fetch_scales(k / 4 + 1);
@@ -648,30 +639,29 @@ void mx_both_kernel(MxArgs a) {
     const char* sa = lds + (k & 1) * STAGE;
     const char* sb = sa + A_BYTES;
     const char* ss = lds + 2 * STAGE + (k / 4 & 1) * SCALES + (((k / 2 & 1) ^ ssw) * 16 + (k & 1) * 8 + lhalf * 4);
-    int sw[C::FN], sx[C::FM];
-    v4u32 pw[2][C::FN], px[2][C::FM];
+    int sw[FN], sx[FM];
+    v4u32 pw[2][FN], px[2][FM];
     auto fetch = [&](int kk) __attribute__((always_inline)) {
       const int phys = ((4 * lhalf + kk) ^ rsw) * 16;
 #pragma unroll
-      for (int i = 0; i < C::FN; ++i) pw[kk & 1][i] = *(const v4u32*)(sb + (block_row<C, GATED>(wave_n, i) + lrow) * 128 + phys);
+      for (int i = 0; i < FN; ++i) pw[kk & 1][i] = *(const v4u32*)(sb + (block_row<C, GATED, 32>(wave_n, i) + lrow) * 128 + phys);
 #pragma unroll
-      for (int j = 0; j < C::FM; ++j) px[kk & 1][j] = *(const v4u32*)(sa + (wave_m * C::WM + 32 * j + lrow) * 128 + phys);
+      for (int j = 0; j < FM; ++j) px[kk & 1][j] = *(const v4u32*)(sa + (wave_m * C::WM + 32 * j + lrow) * 128 + phys);
     };
 #pragma unroll
-    for (int i = 0; i < C::FN; ++i) sw[i] = *(const int*)(ss + (C::BM + block_row<C, GATED>(wave_n, i) + lrow) * 32);
+    for (int i = 0; i < FN; ++i) sw[i] = *(const int*)(ss + (C::BM + block_row<C, GATED, 32>(wave_n, i) + lrow) * 32);
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j) sx[j] = *(const int*)(ss + (wave_m * C::WM + 32 * j + lrow) * 32);
+    for (int j = 0; j < FM; ++j) sx[j] = *(const int*)(ss + (wave_m * C::WM + 32 * j + lrow) * 32);
     fetch(0);
-    if constexpr (NEXT == 1) issue(k + 1, std::false_type{});
-    if constexpr (NEXT == 2) issue(k + 1, std::true_type{});
+    issue(k + 1);
     __builtin_amdgcn_sched_barrier(0);
     auto multiply = [&](auto kt) __attribute__((always_inline)) {
       constexpr int kk = decltype(kt)::value;
       if constexpr (kk < 3) fetch(kk + 1);
 #pragma unroll
-      for (int i = 0; i < C::FN; ++i)
+      for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int j = 0; j < C::FM; ++j) {
+        for (int j = 0; j < FM; ++j) {
           const v4u32 q = pw[kk & 1][i], r = px[kk & 1][j];
           const i32x8 wq = {(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
           const i32x8 xq = {(int)r[0], (int)r[1], (int)r[2], (int)r[3], 0, 0, 0, 0};
@@ -685,35 +675,37 @@ void mx_both_kernel(MxArgs a) {
     // each MFMA step's operand reads before the previous step's MFMAs
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      if (kk < 3) __builtin_amdgcn_sched_group_barrier(0x100, C::FN + C::FM, 0);
-      __builtin_amdgcn_sched_group_barrier(0x8, C::FN * C::FM, 0);
+      if (kk < 3) __builtin_amdgcn_sched_group_barrier(0x100, FN + FM, 0);
+      __builtin_amdgcn_sched_group_barrier(0x8, FN * FM, 0);
     }
   };
   fetch_scales(0);
-  if (KT > 1) issue(0, std::false_type{});
-  else issue(0, std::true_type{});
+  issue(0);
   keep_scales(0);
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  int k = 0;
-  for (; k + 2 < KT; ++k) step(k, I1{});
-  if (k + 1 < KT) step(k++, I2{});
-  step(k, I0{});
+#pragma unroll 1
+  for (int k = 0; k < KT; ++k) step(k);
   __builtin_amdgcn_s_waitcnt(0x70);
   __builtin_amdgcn_s_barrier();   // every wave is done with the operands
-  finish_tile<C, GATED>(a, p, acc, lds, wave, lane);
+  finish_tile<C, GATED>(a, p, lds, wave, lane, [&](int j, float* to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(float4*)(to + lrow * C::PITCH + 32 * i + 8 * q + 4 * lhalf) =
+            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+  });
 }
 
 // Weights alone in 4 bits.  They lie in LDS as in memory, 32 bytes of a row a
-// stage, and become 16-bit operands on the way out of it: a lane's block of 32
-// gives the four MFMA steps' parts, element groups of 8, so that a stage's
-// weights cost one 16-byte read for 32 rows and 16 conversions.  x's 16-byte chunk
-// 4 h + kk of a stage belongs to lane half h in step kk.
+// stage, and become 16-bit operands on the way out of it: lane group g takes half
+// a block, elements 16 g .. + 15 of the stage, for the stage's two MFMA steps of 8 elements
+// each.  x's 16-byte chunk 2 g + c of a stage belongs to group g in step c.
 template <class C, bool F16, bool GATED>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
 void mx_weights_kernel(MxArgs a) {
   typedef typename Elem<F16>::v8 v8;
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  constexpr int FM = C::WM / 16, FN = C::WN / 16;           // blocks of v_mfma_f32_16x16x32
   constexpr int STAGES = 3;
   constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 32;
   constexpr int SCALES = C::BN * 16;                        // eight stages' scales
@@ -725,19 +717,16 @@ void mx_weights_kernel(MxArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wave_m = wave / C::WN_, wave_n = wave % C::WN_;
   constexpr int HB = GATED ? C::BN / 2 : C::BN;
-  Place p = place_of<C::BM, HB>(a);
-  p.rows.expert = __builtin_amdgcn_readfirstlane(p.rows.expert);
-  p.rows.count = __builtin_amdgcn_readfirstlane(p.rows.count);
-  p.rows.row = __builtin_amdgcn_readfirstlane((int)p.rows.row);
-  if (p.rows.count <= 0) return;
-  const int arows = p.rows.count, brows = p.cols;
+  const Place p = place_of<C::BM, HB>(a);
+  if (p.rows <= 0) return;
+  const int arows = p.rows, brows = p.cols;
   const int kscales = a.K / 32;
   const int KT = (a.K + 63) / 64, tail = a.K - (KT - 1) * 64;   // 32 or 64 elements
 
   // this wavefront's 32 rows of w, all of one half of a gated tile
   const int up = GATED && wave * 32 >= HB ? 1 : 0;
-  const char* w = a.w + p.rows.expert * a.expert_w + ((int64_t)up * a.N + p.n0) * a.ld_w;
-  const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.x + p.rows.row * a.ld_x, (arows - 1) * a.ld_x + 2 * a.K);
+  const char* w = a.w + p.expert * a.expert_w + ((int64_t)up * a.N + p.n0) * a.ld_w;
+  const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.x + p.row * a.ld_x, (arows - 1) * a.ld_x + 2 * a.K);
   const __amdgpu_buffer_rsrc_t br = make_rsrc(w, (brows - 1) * a.ld_w + a.K / 2);
   uint32_t aoff[A_LOADS], boff;
   const int chunk = (lane % 8) ^ ((wave * 4 + lane / 16) % 8);
@@ -746,7 +735,7 @@ void mx_weights_kernel(MxArgs a) {
     const int r = (wave + i * C::NW) * 8 + lane / 8;
     aoff[i] = r < arows ? (uint32_t)r * (uint32_t)a.ld_x + chunk * 16 : kPastEnd;
   }
-  const int block = (lane % 2) ^ (lane / 16 % 2);           // blocks of rows 8 .. 15 of 16 swapped
+  const int block = lane % 2;
   {
     const int r = wave * 32 - up * HB + lane / 2;
     boff = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + block * 16 : kPastEnd;
@@ -762,7 +751,7 @@ void mx_weights_kernel(MxArgs a) {
   // scales of stages 8 s .. 8 s + 7: 16 bytes of w's row tid
   v4u32 sc = {0, 0, 0, 0};
   const int sup = GATED && tid >= HB ? 1 : 0;
-  const uint8_t* srow = a.ws + p.rows.expert * a.expert_ws +
+  const uint8_t* srow = a.ws + p.expert * a.expert_ws +
                         ((int64_t)sup * a.N + p.n0 + min(tid - sup * HB, brows - 1)) * a.ld_ws;
   auto fetch_scales = [&](int s) __attribute__((always_inline)) {
     if (C::NT > C::BN && tid >= C::BN) return;
@@ -774,15 +763,12 @@ void mx_weights_kernel(MxArgs a) {
     *(v4u32*)(lds + STAGES * STAGE + (s & 1) * SCALES + tid * 16) = sc;
   };
 
-  const int lrow = lane & 31, lhalf = lane >> 5, rsw = (lrow / 2) % 8;
-  const int bat = lrow * 32 + (lhalf ^ (lrow / 8 % 2)) * 16;
-  f32x16 acc[C::FN][C::FM];
+  const int lrow = lane & 15, g = lane >> 4, rsw = (lrow / 2) % 8;
+  f32x4 acc[FN][FM];
 #pragma unroll
-  for (int i = 0; i < C::FN; ++i)
+  for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   auto step = [&](int k, auto next_tag, auto flying_tag) __attribute__((always_inline)) {
     constexpr int NEXT = decltype(next_tag)::value;   // 0 nothing, 1 a whole stage, 2 the last one
@@ -791,36 +777,34 @@ void mx_weights_kernel(MxArgs a) {
     __builtin_amdgcn_s_barrier();
     if ((k & 7) == 0 && k + 8 < KT) fetch_scales(k / 8 + 1);
     if ((k & 7) == 4 && k + 4 < KT) keep_scales(k / 8 + 1);
-    const char* sa = lds + (k % STAGES) * STAGE;
-    const char* sb = sa + A_BYTES;
-    const uint8_t* ss = (const uint8_t*)lds + STAGES * STAGE + (k / 8 & 1) * SCALES + (k & 7) * 2 + lhalf;
-    float scale[C::FN];
-    v4u32 q[C::FN];
-    v8 px[2][C::FM];
-    auto fetch = [&](int kk) __attribute__((always_inline)) {
-      const int phys = ((4 * lhalf + kk) ^ rsw) * 16;
+    const char* sa = lds + (k % STAGES) * STAGE + (wave_m * C::WM + lrow) * 128;
+    const char* sb = lds + (k % STAGES) * STAGE + A_BYTES + lrow * 32 + g * 8;
+    const uint8_t* ss = (const uint8_t*)lds + STAGES * STAGE + (k / 8 & 1) * SCALES + lrow * 16 + (k & 7) * 2 + g / 2;
+    float scale[FN];
+    u32x2 q[FN];
+    v8 px[2][FM];
 #pragma unroll
-      for (int j = 0; j < C::FM; ++j) px[kk & 1][j] = *(const v8*)(sa + (wave_m * C::WM + 32 * j + lrow) * 128 + phys);
-    };
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i) {
-      q[i] = *(const v4u32*)(sb + block_row<C, GATED>(wave_n, i) * 32 + bat);
-      scale[i] = scale_of(ss[(block_row<C, GATED>(wave_n, i) + lrow) * 16]);
+    for (int i = 0; i < FN; ++i) {
+      q[i] = *(const u32x2*)(sb + block_row<C, GATED, 16>(wave_n, i) * 32);
+      scale[i] = scale_of(ss[block_row<C, GATED, 16>(wave_n, i) * 16]);
     }
+    auto fetch = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < FM; ++j) px[c][j] = *(const v8*)(sa + 16 * j * 128 + ((2 * g + c) ^ rsw) * 16);
+    };
     fetch(0);
     if constexpr (NEXT == 1) issue(k + STAGES - 1, std::false_type{});
     if constexpr (NEXT == 2) issue(k + STAGES - 1, std::true_type{});
     __builtin_amdgcn_sched_barrier(0);
+    fetch(1);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      if (kk < 3) fetch(kk + 1);
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int i = 0; i < C::FN; ++i) {
-        const v8 wide = __builtin_bit_cast(v8, widen<F16>(q[i][kk], scale[i]));
+      for (int i = 0; i < FN; ++i) {
+        const v8 wide = __builtin_bit_cast(v8, widen<F16>(q[i][c], scale[i]));
 #pragma unroll
-        for (int j = 0; j < C::FM; ++j) acc[i][j] = Elem<F16>::mfma32(wide, px[kk & 1][j], acc[i][j]);
+        for (int j = 0; j < FM; ++j) acc[i][j] = Elem<F16>::mfma16(wide, px[c][j], acc[i][j]);
       }
-    }
   };
   fetch_scales(0);
 #pragma unroll
@@ -839,7 +823,13 @@ void mx_weights_kernel(MxArgs a) {
   step(k, I0{}, std::false_type{});
   __builtin_amdgcn_s_waitcnt(0x70);
   __builtin_amdgcn_s_barrier();   // every wave is done with the operands
-  finish_tile<C, GATED>(a, p, acc, lds, wave, lane);
+  finish_tile<C, GATED>(a, p, lds, wave, lane, [&](int j, float* to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+        *(f32x4*)(to + (16 * h + lrow) * C::PITCH + 16 * i + 4 * g) = acc[i][2 * j + h];
+  });
 }
 
 // --- host -------------------------------------------------------------------
@@ -966,7 +956,7 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
       };
       if (c.kind == T64) go(Mx64{});
       else if (c.kind == T128) go(Mx128{});
-      else go(std::conditional_t<G, Mx256G, Mx256>{});
+      else go(Mx256{});
     }
   });
   return hipGetLastError();
