@@ -16,6 +16,8 @@
 // a lane always takes whole blocks of 32: 16 bytes of a row, one scale.
 // The first MFMA operand is the weights', so a lane ends with 4 consecutive
 // output columns per accumulator quad.
+#include <math.h>
+
 #include "product.h"
 
 namespace moe {
@@ -271,19 +273,20 @@ __device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int left) {
 //
 // Bound by reading the weights, which every (row tile, column tile) workgroup
 // does once, straight into operand registers.  A workgroup owns 16 TT rows of
-// one expert and 16 NB output columns (gated: 16 NB gate and up rows of w); its
+// one expert and 16 BLOCKS rows of w (gated: half of them gate, half up rows); its
 // wavefronts take K in pieces of 512, 256 contiguous bytes of each weight row, in
 // turn and join their sums in LDS.  A piece is four steps of 128: a lane holds
 // row lane % 16, block lane / 16 of each; with 16-bit operands dword i of the
 // block is the lane's part of the step's i-th v_mfma_f32_16x16x32.  A row's 16
 // scales of a piece are one load, of which step s needs byte lane / 16 of dword s.
 // Result lane: row (of x) lane % 16, columns 4 (lane / 16) .. + 3.
-template <int XT, bool GATED, int TT, int NB, int W>
+template <int XT, bool GATED, int TT, int BLOCKS, int W>
 __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
   constexpr bool MX = XT == MOE_MXFP4, F16 = XT == MOE_F16;
-  constexpr int G = GATED ? 2 : 1, XL = MX ? 1 : 4;      // 16-byte loads of a block of x
+  constexpr int G = GATED ? 2 : 1, NB = BLOCKS / G;      // 16-row blocks of gate, and of up rows
+  constexpr int XL = MX ? 1 : 4;      // 16-byte loads of a block of x
   constexpr int AHEAD = MX ? 4 : 1;                      // steps of x in registers
-  __shared__ float4 part[W][G * NB][TT][64];
+  __shared__ float4 part[W][BLOCKS][TT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const RowTile tile = find_tile(a, 16 * TT, blockIdx.x / a.n_nt);
   const int expert = __builtin_amdgcn_readfirstlane(tile.expert), rows = __builtin_amdgcn_readfirstlane(tile.count);
@@ -448,17 +451,27 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
 // (their rows may start at any byte), some stages' at a time, into a table of
 // their own in LDS, ahead of the stages that need them.
 
-template <int BM_, int BN_, int WAVES_M, int WAVES_N>
+// STAGES16, STAGES4: stages in LDS with x in 16 and in 4 bits, all but one of them in
+// flight; B16: block of the matrix steps with x in 16 bits
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int STAGES16_, int STAGES4_, int B16_>
 struct MxTile {
-  static constexpr int BM = BM_, BN = BN_;
+  static constexpr int BM = BM_, BN = BN_, STAGES16 = STAGES16_, STAGES4 = STAGES4_, B16 = B16_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64, WN_ = WAVES_N;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int PITCH = WN + 4;            // floats of a row in the epilogue's staging
   static constexpr int EPI = NW * 32 * PITCH * 4;
 };
-typedef MxTile<256, 256, 2, 4> Mx256;
-typedef MxTile<128, 128, 2, 2> Mx128;
-typedef MxTile<64, 128, 2, 2> Mx64;
+typedef MxTile<256, 256, 2, 4, 3, 2, 16> Mx256;
+typedef MxTile<128, 128, 2, 2, 3, 2, 32> Mx128;
+typedef MxTile<64, 128, 2, 2, 3, 2, 32> Mx64;
+
+// vmcnt(flying) lgkmcnt(0) and the workgroup's barrier
+template <int FLYING>
+__device__ __forceinline__ void meet() {
+  static_assert(FLYING < 16, "vector memory counter's low bits");
+  __builtin_amdgcn_s_waitcnt(0x70 | FLYING);
+  __builtin_amdgcn_s_barrier();
+}
 
 // A workgroup's tile: its place among the row and column tiles.  Workgroup i runs
 // on XCD i mod 8; each XCD gets a contiguous run, in which 8 row tiles x 4 column
@@ -547,7 +560,8 @@ void mx_both_kernel(MxArgs a) {
   constexpr int SCALES = (C::BM + C::BN) * 32;              // four stages' scales
   constexpr int A_LOADS = C::BM / 8 / C::NW, B_LOADS = C::BN / 8 / C::NW;
   constexpr int S_CHUNKS = SCALES / 16, S_LOADS = (S_CHUNKS + C::NT - 1) / C::NT;
-  constexpr int LDS = 2 * STAGE + 2 * SCALES;
+  constexpr int STAGES = C::STAGES4, LDS = STAGES * STAGE + 2 * SCALES;
+  constexpr int KEEP_AT = STAGES > 2 ? 3 : 1;                // when the next table's scales have arrived
   static_assert(LDS >= C::EPI && LDS <= 160 * 1024 && C::NW % 2 == 0 && B_LOADS % 2 == 0 && FN % 2 == 0, "tile");
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -576,8 +590,8 @@ void mx_both_kernel(MxArgs a) {
     const int r = (wave + (GATED ? i % (B_LOADS / 2) : i) * C::NW) * 8 + lane / 8;   // the second half: up rows
     boff[i] = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + chunk * 16 : kPastEnd;
   }
-  auto issue = [&](int k) __attribute__((always_inline)) {
-    char* base = lds + (k & 1) * STAGE;
+  auto issue = [&](int k, int slot) __attribute__((always_inline)) {
+    char* base = lds + slot * STAGE;
     const bool on = chunk * 16 < kbytes - 128 * k;     // past K's end: zeros
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i)
@@ -614,7 +628,7 @@ void mx_both_kernel(MxArgs a) {
     }
   };
   auto keep_scales = [&](int s) __attribute__((always_inline)) {
-    char* base = lds + 2 * STAGE + (s & 1) * SCALES;
+    char* base = lds + STAGES * STAGE + (s & 1) * SCALES;
 #pragma unroll
     for (int i = 0; i < S_LOADS; ++i) {
       const int id = min(i * C::NT + tid, S_CHUNKS - 1), r = id / 2;
@@ -631,14 +645,14 @@ void mx_both_kernel(MxArgs a) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  auto step = [&](int k) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0x70);                 // vmcnt(0) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
+  // stage k in `slot`, the one STAGES - 1 ahead into `next`
+  auto step = [&](int k, int slot, int next) __attribute__((always_inline)) {
+    meet<(STAGES - 2) * (A_LOADS + B_LOADS)>();
     if ((k & 3) == 0 && k + 4 < KT) fetch_scales(k / 4 + 1);
-    if ((k & 3) == 1 && k + 3 < KT) keep_scales(k / 4 + 1);
-    const char* sa = lds + (k & 1) * STAGE;
+    if ((k & 3) == KEEP_AT && k + 4 - KEEP_AT < KT) keep_scales(k / 4 + 1);
+    const char* sa = lds + slot * STAGE;
     const char* sb = sa + A_BYTES;
-    const char* ss = lds + 2 * STAGE + (k / 4 & 1) * SCALES + (((k / 2 & 1) ^ ssw) * 16 + (k & 1) * 8 + lhalf * 4);
+    const char* ss = lds + STAGES * STAGE + (k / 4 & 1) * SCALES + (((k / 2 & 1) ^ ssw) * 16 + (k & 1) * 8 + lhalf * 4);
     int sw[FN], sx[FM];
     v4u32 pw[2][FN], px[2][FM];
     auto fetch = [&](int kk) __attribute__((always_inline)) {
@@ -653,7 +667,7 @@ void mx_both_kernel(MxArgs a) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) sx[j] = *(const int*)(ss + (wave_m * C::WM + 32 * j + lrow) * 32);
     fetch(0);
-    issue(k + 1);
+    issue(k + STAGES - 1, next);
     __builtin_amdgcn_sched_barrier(0);
     auto multiply = [&](auto kt) __attribute__((always_inline)) {
       constexpr int kk = decltype(kt)::value;
@@ -680,12 +694,17 @@ void mx_both_kernel(MxArgs a) {
     }
   };
   fetch_scales(0);
-  issue(0);
+#pragma unroll
+  for (int k = 0; k < STAGES - 1; ++k) issue(k, k);
   keep_scales(0);
+  int slot = 0, next = STAGES - 1;
 #pragma unroll 1
-  for (int k = 0; k < KT; ++k) step(k);
-  __builtin_amdgcn_s_waitcnt(0x70);
-  __builtin_amdgcn_s_barrier();   // every wave is done with the operands
+  for (int k = 0; k < KT; ++k) {
+    step(k, slot, next);
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+    next = next + 1 == STAGES ? 0 : next + 1;
+  }
+  meet<0>();   // every wave is done with the operands
   finish_tile<C, GATED>(a, p, lds, wave, lane, [&](int j, float* to) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < FN; ++i)
@@ -697,21 +716,23 @@ void mx_both_kernel(MxArgs a) {
 }
 
 // Weights alone in 4 bits.  They lie in LDS as in memory, 32 bytes of a row a
-// stage, and become 16-bit operands on the way out of it: lane group g takes half
-// a block, elements 16 g .. + 15 of the stage, for the stage's two MFMA steps of 8 elements
-// each.  x's 16-byte chunk 2 g + c of a stage belongs to group g in step c.
+// stage, and become 16-bit operands on the way out of it.  A lane group g (B lanes) takes
+// the stage's elements from 8 KK g on, 8 for each of the KK matrix steps: of w 4 KK
+// bytes, which are in one block, of x the 16-byte chunks KK g + kk.
 template <class C, bool F16, bool GATED>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
 void mx_weights_kernel(MxArgs a) {
   typedef typename Elem<F16>::v8 v8;
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  constexpr int FM = C::WM / 16, FN = C::WN / 16;           // blocks of v_mfma_f32_16x16x32
-  constexpr int STAGES = 3;
+  constexpr int B = C::B16, GROUPS = 64 / B, KK = 8 / GROUPS;
+  constexpr int FM = C::WM / B, FN = C::WN / B;
+  typedef uint32_t part_t __attribute__((ext_vector_type(KK)));
+  typedef std::conditional_t<B == 32, f32x16, f32x4> acc_t;
+  constexpr int STAGES = C::STAGES16;
   constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 32;
   constexpr int SCALES = C::BN * 16;                        // eight stages' scales
   constexpr int A_LOADS = C::BM / 8 / C::NW;
   constexpr int RING = STAGES * STAGE + 2 * SCALES, LDS = RING > C::EPI ? RING : C::EPI;
-  static_assert(LDS <= 160 * 1024 && C::NW % 2 == 0 && C::BN == 32 * C::NW, "tile");
+  static_assert(LDS <= 160 * 1024 && C::NW % 2 == 0 && C::BN == 32 * C::NW && STAGES <= 6, "tile");
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -721,7 +742,7 @@ void mx_weights_kernel(MxArgs a) {
   if (p.rows <= 0) return;
   const int arows = p.rows, brows = p.cols;
   const int kscales = a.K / 32;
-  const int KT = (a.K + 63) / 64, tail = a.K - (KT - 1) * 64;   // 32 or 64 elements
+  const int KT = (a.K + 63) / 64;
 
   // this wavefront's 32 rows of w, all of one half of a gated tile
   const int up = GATED && wave * 32 >= HB ? 1 : 0;
@@ -735,18 +756,18 @@ void mx_weights_kernel(MxArgs a) {
     const int r = (wave + i * C::NW) * 8 + lane / 8;
     aoff[i] = r < arows ? (uint32_t)r * (uint32_t)a.ld_x + chunk * 16 : kPastEnd;
   }
-  const int block = lane % 2;
+  const int block = (lane % 2) ^ (lane / 16 % 2);           // blocks of rows 8 .. 15 of 16 swapped
   {
     const int r = wave * 32 - up * HB + lane / 2;
     boff = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + block * 16 : kPastEnd;
   }
-  auto issue = [&](int k, auto last_tag) __attribute__((always_inline)) {
-    constexpr bool LAST = decltype(last_tag)::value;
-    char* base = lds + (k % STAGES) * STAGE;
+  auto issue = [&](int k, int slot) __attribute__((always_inline)) {
+    char* base = lds + slot * STAGE;
+    const int left = a.K - 64 * k;                           // past K's end: zeros
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i)
-      load_lds(ar, base + (wave + i * C::NW) * 1024, !LAST || chunk * 8 < tail ? aoff[i] : kPastEnd, 128 * k);
-    load_lds(br, base + A_BYTES + wave * 1024, !LAST || block * 32 < tail ? boff : kPastEnd, 32 * k);
+      load_lds(ar, base + (wave + i * C::NW) * 1024, chunk * 8 < left ? aoff[i] : kPastEnd, 128 * k);
+    load_lds(br, base + A_BYTES + wave * 1024, block * 32 < left ? boff : kPastEnd, 32 * k);
   };
   // scales of stages 8 s .. 8 s + 7: 16 bytes of w's row tid
   v4u32 sc = {0, 0, 0, 0};
@@ -763,72 +784,74 @@ void mx_weights_kernel(MxArgs a) {
     *(v4u32*)(lds + STAGES * STAGE + (s & 1) * SCALES + tid * 16) = sc;
   };
 
-  const int lrow = lane & 15, g = lane >> 4, rsw = (lrow / 2) % 8;
-  f32x4 acc[FN][FM];
+  const int lrow = lane % B, g = lane / B, rsw = (lrow / 2) % 8;
+  const int half = g * 2 / GROUPS;                           // this group's block of a stage
+  const int bat = lrow * 32 + (half ^ (lrow / 8 % 2)) * 16 + g % (GROUPS / 2) * 8;
+  acc_t acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FM; ++j) acc[i][j] = acc_t{};
 
-  auto step = [&](int k, auto next_tag, auto flying_tag) __attribute__((always_inline)) {
-    constexpr int NEXT = decltype(next_tag)::value;   // 0 nothing, 1 a whole stage, 2 the last one
-    constexpr int FLYING = decltype(flying_tag)::value ? A_LOADS + 1 : 0;   // the next stage's loads
-    __builtin_amdgcn_s_waitcnt(0x70 | FLYING);        // vmcnt(FLYING) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
+  // stage k in `slot`, the one STAGES - 1 ahead into `next`
+  auto step = [&](int k, int slot, int next) __attribute__((always_inline)) {
+    meet<(STAGES - 2) * (A_LOADS + 1)>();
     if ((k & 7) == 0 && k + 8 < KT) fetch_scales(k / 8 + 1);
     if ((k & 7) == 4 && k + 4 < KT) keep_scales(k / 8 + 1);
-    const char* sa = lds + (k % STAGES) * STAGE + (wave_m * C::WM + lrow) * 128;
-    const char* sb = lds + (k % STAGES) * STAGE + A_BYTES + lrow * 32 + g * 8;
-    const uint8_t* ss = (const uint8_t*)lds + STAGES * STAGE + (k / 8 & 1) * SCALES + lrow * 16 + (k & 7) * 2 + g / 2;
+    const char* sa = lds + slot * STAGE + (wave_m * C::WM + lrow) * 128;
+    const char* sb = lds + slot * STAGE + A_BYTES + bat;
+    const uint8_t* ss = (const uint8_t*)lds + STAGES * STAGE + (k / 8 & 1) * SCALES + lrow * 16 + (k & 7) * 2 + half;
     float scale[FN];
-    u32x2 q[FN];
+    part_t q[FN];
     v8 px[2][FM];
+    auto fetch = [&](int kk) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < FM; ++j) px[kk & 1][j] = *(const v8*)(sa + B * j * 128 + ((KK * g + kk) ^ rsw) * 16);
+    };
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
-      q[i] = *(const u32x2*)(sb + block_row<C, GATED, 16>(wave_n, i) * 32);
-      scale[i] = scale_of(ss[block_row<C, GATED, 16>(wave_n, i) * 16]);
+      q[i] = *(const part_t*)(sb + block_row<C, GATED, B>(wave_n, i) * 32);
+      scale[i] = scale_of(ss[block_row<C, GATED, B>(wave_n, i) * 16]);
     }
-    auto fetch = [&](int c) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < FM; ++j) px[c][j] = *(const v8*)(sa + 16 * j * 128 + ((2 * g + c) ^ rsw) * 16);
-    };
     fetch(0);
-    if constexpr (NEXT == 1) issue(k + STAGES - 1, std::false_type{});
-    if constexpr (NEXT == 2) issue(k + STAGES - 1, std::true_type{});
+    issue(k + STAGES - 1, next);
     __builtin_amdgcn_sched_barrier(0);
-    fetch(1);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int kk = 0; kk < KK; ++kk) {
+      if (kk + 1 < KK) fetch(kk + 1);
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
-        const v8 wide = __builtin_bit_cast(v8, widen<F16>(q[i][c], scale[i]));
+        const v8 wide = __builtin_bit_cast(v8, widen<F16>(q[i][kk], scale[i]));
 #pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = Elem<F16>::mfma16(wide, px[c][j], acc[i][j]);
+        for (int j = 0; j < FM; ++j) {
+          if constexpr (B == 32) acc[i][j] = Elem<F16>::mfma32(wide, px[kk & 1][j], acc[i][j]);
+          else acc[i][j] = Elem<F16>::mfma16(wide, px[kk & 1][j], acc[i][j]);
+        }
       }
+    }
   };
   fetch_scales(0);
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) {
-    if (k + 1 < KT) issue(k, std::false_type{});
-    else if (k + 1 == KT) issue(k, std::true_type{});
-  }
+  for (int k = 0; k < STAGES - 1; ++k) issue(k, k);
   keep_scales(0);
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  int k = 0;
-  for (; k + STAGES < KT; ++k) step(k, I1{}, std::true_type{});
-  if (k + STAGES - 1 < KT) step(k++, I2{}, std::true_type{});
-  if (k + 1 < KT) step(k++, I0{}, std::true_type{});
-  step(k, I0{}, std::false_type{});
-  __builtin_amdgcn_s_waitcnt(0x70);
-  __builtin_amdgcn_s_barrier();   // every wave is done with the operands
+  int slot = 0, next = STAGES - 1;
+#pragma unroll 1
+  for (int k = 0; k < KT; ++k) {
+    step(k, slot, next);
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+    next = next + 1 == STAGES ? 0 : next + 1;
+  }
+  meet<0>();   // every wave is done with the operands
   finish_tile<C, GATED>(a, p, lds, wave, lane, [&](int j, float* to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 32 / B; ++h)
 #pragma unroll
       for (int i = 0; i < FN; ++i)
-        *(f32x4*)(to + (16 * h + lrow) * C::PITCH + 16 * i + 4 * g) = acc[i][2 * j + h];
+#pragma unroll
+        for (int v = 0; v < (B == 32 ? 4 : 1); ++v) {
+          const acc_t& z = acc[i][32 / B * j + h];
+          *(float4*)(to + (16 * h + lrow) * C::PITCH + B * i + 8 * v + 4 * g) = make_float4(z[4 * v], z[4 * v + 1], z[4 * v + 2], z[4 * v + 3]);
+        }
   });
 }
 
@@ -860,17 +883,77 @@ void with_flag(bool b, F f) {
   else f(std::false_type{});
 }
 
+// How a product is cut: few rows (16 tt rows, `blocks` blocks of w's rows, `waves`
+// wavefronts a workgroup) or a tile.
 enum MxKind { FEW, T64, T128, T256 };
 struct MxChoice {
   MxKind kind;
-  int tt, nb, waves;   // FEW
+  int tt, blocks, waves;   // FEW
 };
 
+// Time of each choice, the smallest wins.  Rows are taken to be spread evenly over the
+// experts (the offsets are in device memory), half a row tile lost at each
+// expert's end.  A stage of a tile takes a load's latency, or what the
+// multiplications of the workgroups that share a CU take; a round of workgroups adds its
+// start and epilogue.  A few-row workgroup takes a fixed time and one for each piece of
+// K its wavefronts take in turn; all of them together what their reads take.  Neither is
+// faster than the weights' reading.  The constants are fitted to the times of every
+// choice over 198 products of each kind (1 to 32768 rows, 1 to 128 experts): the
+// choice costs 2.4% over the best one on average with x in 16 bits, 3.7% in 4.
+// Both sides of typical decisions, x in bf16, gated: 16 rows over 8 experts of 2 x
+// 2048 x 7168 take 31 us as few rows and 58 us in tiles of 64 rows; 1024 over 32 of them
+// 239 us as few rows, 196 in tiles of 64 and 215 in tiles of 128; 16384 over 16 of
+// 2 x 1536 x 4096 487 us in tiles of 64, 422 of 128 and 394 of 256.
 MxChoice choose_mx(const moe_mx_linear_desc& d) {
-  const int64_t each = d.rows / d.experts;
-  if (each >= 512) return {T256, 0, 0, 0};
-  if (each >= 64) return {T128, 0, 0, 0};
-  return {FEW, 1, 1, 8};
+  struct Fit { double latency, shared, round_us; };
+  struct Few { double fixed, piece, w_kb, x_kb; };
+  static const int bm[4] = {0, 64, 128, 256}, bn[4] = {0, 128, 128, 256};
+  static const int per_cu[2][4] = {{0, 3, 2, 1}, {0, 2, 2, 1}};
+  static const Fit fits[2][4] = {{{}, {0.412, 0.26, 1.8}, {0.547, 0.454, 3.9}, {1.45, 1.06, 7.73}},
+                                 {{}, {0.507, 0.538, 3.13}, {0.606, 0.588, 5.7}, {1.76, 0.96, 8.84}}};
+  static const Few few[2] = {{1.82, 2.92, 0.0783, 0.0097}, {2.01, 2.07, 0.0485, 0.0107}};
+  static const double tile_rate[2] = {3.15, 3.9}, few_rate[2] = {6.79, 3.97};   // MB/us of weights
+  static const MxChoice fews[] = {{FEW, 1, 2, 2}, {FEW, 1, 2, 4}, {FEW, 1, 4, 4}, {FEW, 2, 4, 4}};
+  constexpr double kCus = 256;
+  const int mx = d.dtype == MOE_MXFP4;
+  const double M = (double)(d.rows > 1 ? d.rows : 1), E = d.experts;
+  const double n = (double)d.cols * (d.act == MOE_ACT_SWIGLU ? 2 : 1), K = d.depth;
+  const double hit = M < E ? M : E, weights_mb = hit * n * K * 0.53e-6;
+  auto row_tiles = [&](int rows) {
+    if (d.experts == 1) return ceil(M / rows);
+    const double t = M / rows + hit * 0.5;
+    return t > hit ? t : hit;
+  };
+  MxChoice best = fews[0];
+  double best_us = 1e30;
+  auto take = [&](const MxChoice& c, double us) {
+    if (us < best_us) {
+      best_us = us;
+      best = c;
+    }
+  };
+  for (const MxChoice& c : fews) {
+    const Few& f = few[mx];
+    const double groups = row_tiles(16 * c.tt) * ceil(n / (16 * c.blocks)), pieces = ceil(K / 512);
+    const double each = M / hit, rows = each < 16 * c.tt ? each : 16 * c.tt;
+    const double rounds = groups / (kCus * (8 / c.waves) * 2);
+    const double wait = (rounds > 1 ? rounds : 1) * (f.fixed + ceil(pieces / c.waves) * f.piece);
+    const double read = f.fixed + groups * K / 512 * (16 * c.blocks * 0.266 * f.w_kb + rows * (mx ? 0.266 : 1) * f.x_kb) / kCus;
+    const double all = weights_mb / few_rate[mx];
+    take(c, wait > read ? (wait > all ? wait : all) : (read > all ? read : all));
+  }
+  for (int t = T64; t <= T256; ++t) {
+    const Fit& f = fits[mx][t];
+    const double tiles = row_tiles(bm[t]) * ceil(n / bn[t]), steps = ceil(K / (mx ? 256 : 64));
+    double share = ceil(tiles / kCus);
+    if (share > per_cu[mx][t]) share = per_cu[mx][t];
+    const double step = share * f.shared > f.latency ? share * f.shared : f.latency;
+    double rounds = tiles / (kCus * share);
+    rounds = rounds < 4 ? (rounds > 1 ? ceil(rounds - 0.02) : 1) : rounds + 0.4;
+    const double us = rounds * (steps * step + f.round_us), all = weights_mb / tile_rate[mx];
+    take({(MxKind)t, 0, 0, 0}, us > all ? us : all);
+  }
+  return best;
 }
 
 // column tiles of `width` and row tiles of `bm` in launches of fewer than 2^31 threads
@@ -926,24 +1009,19 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
     if (c.kind == FEW) {
       with_x(d.dtype, [&](auto xt) {
         constexpr int XT = decltype(xt)::value;
-        auto go = [&](auto tt, auto nb, auto waves) {
-          constexpr int TT = decltype(tt)::value, NB = decltype(nb)::value, W = decltype(waves)::value;
-          launch_tiles(a, 16 * TT, 16 * NB, W * 64, [&](dim3 grid) {
-            hipLaunchKernelGGL((few_rows_kernel<XT, G, TT, NB, W>), grid, dim3(W * 64), 0, s, a);
+        auto go = [&](auto tt, auto blocks, auto waves) {
+          constexpr int TT = decltype(tt)::value, BLOCKS = decltype(blocks)::value, W = decltype(waves)::value;
+          launch_tiles(a, 16 * TT, 16 * BLOCKS / (G ? 2 : 1), W * 64, [&](dim3 grid) {
+            hipLaunchKernelGGL((few_rows_kernel<XT, G, TT, BLOCKS, W>), grid, dim3(W * 64), 0, s, a);
           });
         };
         using One = std::integral_constant<int, 1>;
         using Two = std::integral_constant<int, 2>;
         using Four = std::integral_constant<int, 4>;
-        using Eight = std::integral_constant<int, 8>;
-        if (c.tt == 2) {
-          if (c.waves == 8) go(Two{}, One{}, Eight{});
-          else go(Two{}, One{}, Four{});
-        } else {
-          if (c.waves == 8) go(One{}, One{}, Eight{});
-          else if (c.nb == 2) go(One{}, Two{}, Four{});
-          else go(One{}, One{}, Four{});
-        }
+        if (c.tt == 2) go(Two{}, Four{}, Four{});
+        else if (c.blocks == 4) go(One{}, Four{}, Four{});
+        else if (c.waves == 4) go(One{}, Two{}, Four{});
+        else go(One{}, Two{}, Two{});
       });
     } else {
       auto go = [&](auto tile) {

@@ -16,7 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kSortWaves = 16, kSortThreads = kSortWaves * 64;
-constexpr int kSortCached = 4;     // groups of 64 pairs a wavefront keeps in registers between the walks
+constexpr int kSortUnroll = 8;     // groups of 64 pairs whose keys a wavefront loads together
 
 struct SortArgs {
   const int32_t* ids;
@@ -65,9 +65,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   const int64_t run = a.per / kSortWaves;
   const int64_t lo = min(a.pairs, blockIdx.x * a.per + wave * run), hi = min(a.pairs, lo + run);
   int* mine = table[wave];
-  uint32_t kept[kSortCached];
+  uint32_t kept[kSortUnroll];      // the first ones stay for the second walk
 #pragma unroll
-  for (int u = 0; u < kSortCached; ++u) kept[u] = local_of(a, lo + 64 * u + lane, hi);
+  for (int u = 0; u < kSortUnroll; ++u) kept[u] = local_of(a, lo + 64 * u + lane, hi);
   for (int e = lane; e < a.E; e += 64) mine[e] = 0;
   int total = 0, earlier = 0;
   if constexpr (MULTI) {
@@ -85,10 +85,17 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     before[tid] = earlier;
   }
   auto walk = [&](auto step) __attribute__((always_inline)) {
+    uint32_t e[kSortUnroll];
 #pragma unroll
-    for (int u = 0; u < kSortCached; ++u)
-      if (lo + 64 * u < hi) step(lo + 64 * u + lane, kept[u]);
-    for (int64_t i = lo + 64 * kSortCached; i < hi; i += 64) step(i + lane, local_of(a, i + lane, hi));
+    for (int u = 0; u < kSortUnroll; ++u) e[u] = kept[u];
+    for (int64_t i = lo; i < hi;) {
+#pragma unroll
+      for (int u = 0; u < kSortUnroll; ++u)
+        if (i + 64 * u < hi) step(i + 64 * u + lane, e[u]);
+      i += 64 * kSortUnroll;
+#pragma unroll
+      for (int u = 0; u < kSortUnroll; ++u) e[u] = local_of(a, i + 64 * u + lane, hi);
+    }
   };
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   walk([&](int64_t, uint32_t e) __attribute__((always_inline)) {
@@ -184,7 +191,7 @@ struct Type {                      // MOE_BF16, MOE_F16, MOE_F32
 // 16 bytes of a row from byte `at` on.  WHOLE: rows are 16-byte aligned and a
 // multiple of 16 bytes long; a buffer descriptor of the row gives zeros past its end.
 // Otherwise whole accesses at the elements' alignment, and the last ones by element.
-template <int SIZE, bool WHOLE>
+template <int SIZE, bool WHOLE, int POLICY = 0>
 struct Row {
   char* p;
   __amdgpu_buffer_rsrc_t rsrc;
@@ -195,7 +202,7 @@ struct Row {
     if constexpr (WHOLE) rsrc = make_rsrc(p, bytes);
   }
   __device__ __forceinline__ v4u32 load(int at) const {
-    if constexpr (WHOLE) return __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
+    if constexpr (WHOLE) return __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, POLICY);
     v4u32 x = {0, 0, 0, 0};
     if (at + 16 <= bytes) {
       x = ((const Loose<v4u32, SIZE>*)(p + at))->v;
@@ -211,7 +218,7 @@ struct Row {
   }
   __device__ __forceinline__ void store(int at, v4u32 x) const {
     if constexpr (WHOLE) {
-      __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, at, 0, POLICY);
     } else if (at + 16 <= bytes) {
       ((Loose<v4u32, SIZE>*)(p + at))->v = x;
     } else if (at < bytes) {
@@ -229,7 +236,7 @@ __device__ __forceinline__ bool held(const RowArgs& a, int p) { return (uint64_t
 
 // Each wavefront takes U KB of a token's row at a time, reads it once and writes
 // it to the token's rows.
-template <int SIZE, bool WHOLE, int U>
+template <int SIZE, bool WHOLE, int POLICY, int U>
 __global__ __launch_bounds__(256) void permute_kernel(RowArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -245,7 +252,7 @@ __global__ __launch_bounds__(256) void permute_kernel(RowArgs a) {
     for (int j = 0; j < a.k; ++j) {
       const int p = a.pos[t * a.k + j];
       if (!held(a, p)) continue;
-      const Row<SIZE, WHOLE> to(a.out, p, a.ld_out, a.bytes, true);
+      const Row<SIZE, WHOLE, POLICY> to(a.out, p, a.ld_out, a.bytes, true);
 #pragma unroll
       for (int u = 0; u < U; ++u) to.store(at + 1024 * u, x[u]);
     }
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(256) void permute_kernel(RowArgs a) {
 
 // Sum of a token's rows, weighted or not, in slot order in fp32: a wavefront
 // takes U KB of a token's row and has the loads of four slots in flight.
-template <int T, bool WEIGHTED, bool WHOLE, int U>
+template <int T, bool WEIGHTED, bool WHOLE, int POLICY, int U>
 __global__ __launch_bounds__(256) void unpermute_kernel(RowArgs a) {
   typedef Type<T> E;
   const int lane = threadIdx.x & 63;
@@ -280,7 +287,7 @@ __global__ __launch_bounds__(256) void unpermute_kernel(RowArgs a) {
         const int p = a.pos[j];
         on[c] = j0 + c < a.k && held(a, p);
         w[c] = WEIGHTED ? a.w[j] : 1.f;
-        const Row<E::SIZE, WHOLE> from(a.in, p, a.ld_in, a.bytes, on[c]);
+        const Row<E::SIZE, WHOLE, POLICY> from(a.in, p, a.ld_in, a.bytes, on[c]);
 #pragma unroll
         for (int u = 0; u < U; ++u) x[c][u] = from.load(at + 1024 * u);
       }
@@ -306,7 +313,7 @@ __global__ __launch_bounds__(256) void unpermute_kernel(RowArgs a) {
 // the weight's, the slot's row, writes the row's gradient and reduces the product
 // in fp32.  A token's slots are neighbouring wavefronts, so its gradient comes
 // from the caches after the first of them.
-template <int T, bool DROWS, bool DW, bool WHOLE>
+template <int T, bool DROWS, bool DW, bool WHOLE, int POLICY>
 __global__ __launch_bounds__(256) void unpermute_back_kernel(RowArgs a) {
   typedef Type<T> E;
   const int lane = threadIdx.x & 63;
@@ -320,8 +327,8 @@ __global__ __launch_bounds__(256) void unpermute_back_kernel(RowArgs a) {
       continue;
     }
     const float w = DROWS && a.w ? a.w[i] : 1.f;
-    const Row<E::SIZE, WHOLE> grad(a.in, t, a.ld_in, a.bytes, true), row(a.in2, p, a.ld_in2, a.bytes, DW),
-        to(a.out, p, a.ld_out, a.bytes, DROWS);
+    const Row<E::SIZE, WHOLE> grad(a.in, t, a.ld_in, a.bytes, true);
+    const Row<E::SIZE, WHOLE, POLICY> row(a.in2, p, a.ld_in2, a.bytes, DW), to(a.out, p, a.ld_out, a.bytes, DROWS);
     float sum = 0.f;
     constexpr int U = 4;
     for (int at = lane * 16; at < a.bytes; at += 1024 * U) {
@@ -357,10 +364,14 @@ __global__ __launch_bounds__(256) void unpermute_back_kernel(RowArgs a) {
 
 // --- host -------------------------------------------------------------------
 
+// Pairs of a workgroup.  A short batch is one workgroup's, whose 16 wavefronts share it
+// out: 4096 pairs over 128 experts 8.2 us so and 9.5 us in two launches, 8192 11.2 and 9.3 us
+// (replayed from a graph).  Beyond that up to 256 workgroups, which each read all
+// histograms: 32768 pairs over 256 experts 9.7 us with 1024 pairs each and 11.0 with 2048,
+// 262144 14.8 and 12.7 us, 13.1 with 4096.
 int64_t sort_per(int64_t pairs) {
-  if (pairs <= 4096) return 4096;
-  const int64_t per = (pairs + 255) / 256;
-  return per <= 4096 ? 4096 : (per + kSortThreads - 1) / kSortThreads * kSortThreads;
+  const int64_t least = pairs <= 4096 ? (pairs > 0 ? pairs : 1) : pairs <= 131072 ? 1024 : 2048, per = (pairs + 255) / 256;
+  return ((per > least ? per : least) + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 
 unsigned row_grid(int64_t waves) {
@@ -378,6 +389,18 @@ template <class F>
 void with_flag(bool b, F f) {
   if (b) f(std::true_type{});
   else f(std::false_type{});
+}
+
+// The sorted rows' accesses: what is larger than the last-level cache (256 MB) is
+// read and written past it, 8192 x 8 rows of 4096 bf16 columns 122 -> 103 us; smaller
+// ones may still be there, or be wanted from there by the experts' products.
+template <class F>
+void with_access(bool whole, int64_t bytes, F f) {
+  using Ordinary = std::integral_constant<int, 0>;
+  using Nontemporal = std::integral_constant<int, 2>;
+  if (whole && bytes > (256ll << 20)) f(std::true_type{}, Nontemporal{});
+  else if (whole) f(std::true_type{}, Ordinary{});
+  else f(std::false_type{}, Ordinary{});
 }
 
 bool whole(const void* p, int64_t ld, int64_t bytes) { return !p || (aligned_to(p, 16) && ld % 16 == 0 && bytes % 16 == 0); }
@@ -415,11 +438,11 @@ hipError_t launch_permute(const moe_rows_desc& d, const void* x, const int32_t* 
   const bool few = long_runs < 2048;     // short runs, so that few tokens spread over the CUs
   const dim3 grid(row_grid(few ? short_runs : long_runs)), block(256);
   with_flag(size == 2, [&](auto two) {
-    with_flag(all, [&](auto w) {
-      constexpr int SIZE = decltype(two)::value ? 2 : 4;
+    with_access(all, d.tokens * d.top_k * a.bytes, [&](auto w, auto policy) {
+      constexpr int SIZE = decltype(two)::value ? 2 : 4, P = decltype(policy)::value;
       constexpr bool W = decltype(w)::value;
-      if (few) hipLaunchKernelGGL((permute_kernel<SIZE, W, 1>), grid, block, 0, s, a);
-      else hipLaunchKernelGGL((permute_kernel<SIZE, W, 4>), grid, block, 0, s, a);
+      if (few) hipLaunchKernelGGL((permute_kernel<SIZE, W, P, 1>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((permute_kernel<SIZE, W, P, 4>), grid, block, 0, s, a);
     });
   });
   return hipGetLastError();
@@ -439,11 +462,11 @@ hipError_t launch_unpermute(const moe_rows_desc& d, const void* rows, const int3
   const dim3 grid(row_grid(few ? short_runs : long_runs)), block(256);
   with_type(d.dtype, [&](auto t) {
     with_flag(w != nullptr, [&](auto weighted) {
-      with_flag(all, [&](auto wh) {
-        constexpr int T = decltype(t)::value;
+      with_access(all, d.tokens * d.top_k * a.bytes, [&](auto wh, auto policy) {
+        constexpr int T = decltype(t)::value, P = decltype(policy)::value;
         constexpr bool G = decltype(weighted)::value, W = decltype(wh)::value;
-        if (few) hipLaunchKernelGGL((unpermute_kernel<T, G, W, 1>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((unpermute_kernel<T, G, W, 4>), grid, block, 0, s, a);
+        if (few) hipLaunchKernelGGL((unpermute_kernel<T, G, W, P, 1>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((unpermute_kernel<T, G, W, P, 4>), grid, block, 0, s, a);
       });
     });
   });
@@ -462,12 +485,12 @@ hipError_t launch_unpermute_backward(const moe_rows_desc& d, const void* rows, c
                    whole(d_rows, a.ld_out, a.bytes);
   const dim3 grid(row_grid(d.tokens * d.top_k)), block(256);
   with_type(d.dtype, [&](auto t) {
-    with_flag(all, [&](auto wh) {
-      constexpr int T = decltype(t)::value;
+    with_access(all, d.tokens * d.top_k * a.bytes, [&](auto wh, auto policy) {
+      constexpr int T = decltype(t)::value, P = decltype(policy)::value;
       constexpr bool W = decltype(wh)::value;
-      if (d_rows && dw) hipLaunchKernelGGL((unpermute_back_kernel<T, true, true, W>), grid, block, 0, s, a);
-      else if (d_rows) hipLaunchKernelGGL((unpermute_back_kernel<T, true, false, W>), grid, block, 0, s, a);
-      else hipLaunchKernelGGL((unpermute_back_kernel<T, false, true, W>), grid, block, 0, s, a);
+      if (d_rows && dw) hipLaunchKernelGGL((unpermute_back_kernel<T, true, true, W, P>), grid, block, 0, s, a);
+      else if (d_rows) hipLaunchKernelGGL((unpermute_back_kernel<T, true, false, W, P>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((unpermute_back_kernel<T, false, true, W, P>), grid, block, 0, s, a);
     });
   });
   return hipGetLastError();
