@@ -451,19 +451,20 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
 // (their rows may start at any byte), some stages' at a time, into a table of
 // their own in LDS, ahead of the stages that need them.
 
-// STAGES16, STAGES4: stages in LDS with x in 16 and in 4 bits, all but one of them in
-// flight; B16: block of the matrix steps with x in 16 bits
-template <int BM_, int BN_, int WAVES_M, int WAVES_N, int STAGES16_, int STAGES4_, int B16_>
+// WAVES_SIMD: wavefronts a SIMD that the registers are limited for; B16: block of the matrix
+// steps with x in 16 bits
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int WAVES_SIMD_, int B16_>
 struct MxTile {
-  static constexpr int BM = BM_, BN = BN_, STAGES16 = STAGES16_, STAGES4 = STAGES4_, B16 = B16_;
+  static constexpr int BM = BM_, BN = BN_, WAVES_SIMD = WAVES_SIMD_, B16 = B16_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64, WN_ = WAVES_N;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int PITCH = WN + 4;            // floats of a row in the epilogue's staging
   static constexpr int EPI = NW * 32 * PITCH * 4;
 };
-typedef MxTile<256, 256, 2, 4, 3, 2, 16> Mx256;
-typedef MxTile<128, 128, 2, 2, 3, 2, 32> Mx128;
-typedef MxTile<64, 128, 2, 2, 3, 2, 32> Mx64;
+typedef MxTile<256, 256, 2, 4, 2, 16> Mx256;     // x in 4 bits
+typedef MxTile<128, 256, 2, 4, 4, 16> MxWide;    // x in 16 bits: two workgroups a CU
+typedef MxTile<128, 128, 2, 2, 1, 32> Mx128;
+typedef MxTile<64, 128, 2, 2, 1, 32> Mx64;
 
 // vmcnt(flying) lgkmcnt(0) and the workgroup's barrier
 template <int FLYING>
@@ -550,18 +551,17 @@ __device__ __forceinline__ void finish_tile(const MxArgs& a, const Place& p, cha
 }
 
 // Both operands in 4 bits.  A stage's 16-byte chunks (one block each) of row r lie
-// at c ^ (r / 2) % 8, free of bank conflicts.  Lane half h takes blocks 4 h + kk of
+// at c ^ (r / 2) % 8, free of bank conflicts.  Lane half h takes chunks 4 h + kk of
 // a stage in MFMA step kk, so that its four scales are one dword.
 template <class C, bool GATED>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WAVES_SIMD)))
 void mx_both_kernel(MxArgs a) {
   constexpr int FM = C::WM / 32, FN = C::WN / 32;           // blocks of v_mfma_scale_f32_32x32x64
   constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 128;
   constexpr int SCALES = (C::BM + C::BN) * 32;              // four stages' scales
   constexpr int A_LOADS = C::BM / 8 / C::NW, B_LOADS = C::BN / 8 / C::NW;
   constexpr int S_CHUNKS = SCALES / 16, S_LOADS = (S_CHUNKS + C::NT - 1) / C::NT;
-  constexpr int STAGES = C::STAGES4, LDS = STAGES * STAGE + 2 * SCALES;
-  constexpr int KEEP_AT = STAGES > 2 ? 3 : 1;                // when the next table's scales have arrived
+  constexpr int LDS = 2 * STAGE + 2 * SCALES;
   static_assert(LDS >= C::EPI && LDS <= 160 * 1024 && C::NW % 2 == 0 && B_LOADS % 2 == 0 && FN % 2 == 0, "tile");
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -579,7 +579,7 @@ void mx_both_kernel(MxArgs a) {
   const __amdgpu_buffer_rsrc_t br = make_rsrc(w, (brows - 1) * a.ld_w + kbytes);
   const __amdgpu_buffer_rsrc_t ur = GATED ? make_rsrc(w + a.N * a.ld_w, (brows - 1) * a.ld_w + kbytes) : br;
   uint32_t aoff[A_LOADS], boff[B_LOADS];
-  const int chunk = (lane % 8) ^ ((wave * 4 + lane / 16) % 8);
+  const int chunk = (lane % 8) ^ ((wave * 4 + lane / 16) % 8);   // of a row in memory, the same in all of this lane's loads
 #pragma unroll
   for (int i = 0; i < A_LOADS; ++i) {
     const int r = (wave + i * C::NW) * 8 + lane / 8;
@@ -590,8 +590,8 @@ void mx_both_kernel(MxArgs a) {
     const int r = (wave + (GATED ? i % (B_LOADS / 2) : i) * C::NW) * 8 + lane / 8;   // the second half: up rows
     boff[i] = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + chunk * 16 : kPastEnd;
   }
-  auto issue = [&](int k, int slot) __attribute__((always_inline)) {
-    char* base = lds + slot * STAGE;
+  auto issue = [&](int k) __attribute__((always_inline)) {
+    char* base = lds + (k & 1) * STAGE;
     const bool on = chunk * 16 < kbytes - 128 * k;     // past K's end: zeros
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i)
@@ -628,7 +628,7 @@ void mx_both_kernel(MxArgs a) {
     }
   };
   auto keep_scales = [&](int s) __attribute__((always_inline)) {
-    char* base = lds + STAGES * STAGE + (s & 1) * SCALES;
+    char* base = lds + 2 * STAGE + (s & 1) * SCALES;
 #pragma unroll
     for (int i = 0; i < S_LOADS; ++i) {
       const int id = min(i * C::NT + tid, S_CHUNKS - 1), r = id / 2;
@@ -636,7 +636,7 @@ void mx_both_kernel(MxArgs a) {
     }
   };
 
-  const int lrow = lane & 31, lhalf = lane >> 5, rsw = (lrow / 2) % 8, ssw = lrow / 8 % 2;
+  const int lrow = lane & 31, lhalf = lane >> 5, rsw = lrow / 2 % 8, ssw = lrow / 8 % 2;
   f32x16 acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
@@ -645,14 +645,13 @@ void mx_both_kernel(MxArgs a) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  // stage k in `slot`, the one STAGES - 1 ahead into `next`
-  auto step = [&](int k, int slot, int next) __attribute__((always_inline)) {
-    meet<(STAGES - 2) * (A_LOADS + B_LOADS)>();
+  auto step = [&](int k) __attribute__((always_inline)) {
+    meet<0>();
     if ((k & 3) == 0 && k + 4 < KT) fetch_scales(k / 4 + 1);
-    if ((k & 3) == KEEP_AT && k + 4 - KEEP_AT < KT) keep_scales(k / 4 + 1);
-    const char* sa = lds + slot * STAGE;
+    if ((k & 3) == 1 && k + 3 < KT) keep_scales(k / 4 + 1);
+    const char* sa = lds + (k & 1) * STAGE;
     const char* sb = sa + A_BYTES;
-    const char* ss = lds + STAGES * STAGE + (k / 4 & 1) * SCALES + (((k / 2 & 1) ^ ssw) * 16 + (k & 1) * 8 + lhalf * 4);
+    const char* ss = lds + 2 * STAGE + (k / 4 & 1) * SCALES + (((k / 2 & 1) ^ ssw) * 16 + (k & 1) * 8 + lhalf * 4);
     int sw[FN], sx[FM];
     v4u32 pw[2][FN], px[2][FM];
     auto fetch = [&](int kk) __attribute__((always_inline)) {
@@ -667,7 +666,7 @@ void mx_both_kernel(MxArgs a) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) sx[j] = *(const int*)(ss + (wave_m * C::WM + 32 * j + lrow) * 32);
     fetch(0);
-    issue(k + STAGES - 1, next);
+    issue(k + 1);
     __builtin_amdgcn_sched_barrier(0);
     auto multiply = [&](auto kt) __attribute__((always_inline)) {
       constexpr int kk = decltype(kt)::value;
@@ -694,16 +693,10 @@ void mx_both_kernel(MxArgs a) {
     }
   };
   fetch_scales(0);
-#pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) issue(k, k);
+  issue(0);
   keep_scales(0);
-  int slot = 0, next = STAGES - 1;
 #pragma unroll 1
-  for (int k = 0; k < KT; ++k) {
-    step(k, slot, next);
-    slot = slot + 1 == STAGES ? 0 : slot + 1;
-    next = next + 1 == STAGES ? 0 : next + 1;
-  }
+  for (int k = 0; k < KT; ++k) step(k);
   meet<0>();   // every wave is done with the operands
   finish_tile<C, GATED>(a, p, lds, wave, lane, [&](int j, float* to) __attribute__((always_inline)) {
 #pragma unroll
@@ -720,14 +713,14 @@ void mx_both_kernel(MxArgs a) {
 // the stage's elements from 8 KK g on, 8 for each of the KK matrix steps: of w 4 KK
 // bytes, which are in one block, of x the 16-byte chunks KK g + kk.
 template <class C, bool F16, bool GATED>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::NW == 8 ? 2 : 1)))
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WAVES_SIMD)))
 void mx_weights_kernel(MxArgs a) {
   typedef typename Elem<F16>::v8 v8;
   constexpr int B = C::B16, GROUPS = 64 / B, KK = 8 / GROUPS;
   constexpr int FM = C::WM / B, FN = C::WN / B;
   typedef uint32_t part_t __attribute__((ext_vector_type(KK)));
   typedef std::conditional_t<B == 32, f32x16, f32x4> acc_t;
-  constexpr int STAGES = C::STAGES16;
+  constexpr int STAGES = 3;
   constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 32;
   constexpr int SCALES = C::BN * 16;                        // eight stages' scales
   constexpr int A_LOADS = C::BM / 8 / C::NW;
@@ -885,7 +878,7 @@ void with_flag(bool b, F f) {
 
 // How a product is cut: few rows (16 tt rows, `blocks` blocks of w's rows, `waves`
 // wavefronts a workgroup) or a tile.
-enum MxKind { FEW, T64, T128, T256 };
+enum MxKind { FEW, T64, T128, T256, WIDE };
 struct MxChoice {
   MxKind kind;
   int tt, blocks, waves;   // FEW
@@ -899,18 +892,18 @@ struct MxChoice {
 // K its wavefronts take in turn; all of them together what their reads take.  Neither is
 // faster than the weights' reading.  The constants are fitted to the times of every
 // choice over 198 products of each kind (1 to 32768 rows, 1 to 128 experts): the
-// choice costs 2.4% over the best one on average with x in 16 bits, 3.7% in 4.
-// Both sides of typical decisions, x in bf16, gated: 16 rows over 8 experts of 2 x
-// 2048 x 7168 take 31 us as few rows and 58 us in tiles of 64 rows; 1024 over 32 of them
-// 239 us as few rows, 196 in tiles of 64 and 215 in tiles of 128; 16384 over 16 of
-// 2 x 1536 x 4096 487 us in tiles of 64, 422 of 128 and 394 of 256.
+// choice costs 2.6% over the best one on average with x in 16 bits, 3.7% in 4.
+// Both sides of typical decisions, gated products with x in bf16: 8 rows over 8 experts of
+// 2 x 2048 x 7168 take 31 us as few rows and 58 us in tiles of 64 rows; 1024 over 32 of them
+// 239 us as few rows, 196 in 64 x 128 tiles and 215 in 128 x 128; 16384 over 16 of 2 x 1536
+// x 4096 487 us in 64 x 128, 422 in 128 x 128, 366 in 128 x 256 and 391 in 256 x 256 ones.
 MxChoice choose_mx(const moe_mx_linear_desc& d) {
   struct Fit { double latency, shared, round_us; };
   struct Few { double fixed, piece, w_kb, x_kb; };
-  static const int bm[4] = {0, 64, 128, 256}, bn[4] = {0, 128, 128, 256};
-  static const int per_cu[2][4] = {{0, 3, 2, 1}, {0, 2, 2, 1}};
-  static const Fit fits[2][4] = {{{}, {0.412, 0.26, 1.8}, {0.547, 0.454, 3.9}, {1.45, 1.06, 7.73}},
-                                 {{}, {0.507, 0.538, 3.13}, {0.606, 0.588, 5.7}, {1.76, 0.96, 8.84}}};
+  static const int bm[5] = {0, 64, 128, 256, 128}, bn[5] = {0, 128, 128, 256, 256};
+  static const int per_cu[2][5] = {{0, 3, 2, 1, 2}, {0, 2, 2, 1, 0}};
+  static const Fit fits[2][5] = {{{}, {0.412, 0.26, 1.8}, {0.547, 0.454, 3.9}, {}, {0.75, 0.6, 7.0}},
+                                 {{}, {0.507, 0.538, 3.13}, {0.606, 0.588, 5.7}, {1.76, 0.96, 8.84}, {}}};
   static const Few few[2] = {{1.82, 2.92, 0.0783, 0.0097}, {2.01, 2.07, 0.0485, 0.0107}};
   static const double tile_rate[2] = {3.15, 3.9}, few_rate[2] = {6.79, 3.97};   // MB/us of weights
   static const MxChoice fews[] = {{FEW, 1, 2, 2}, {FEW, 1, 2, 4}, {FEW, 1, 4, 4}, {FEW, 2, 4, 4}};
@@ -936,13 +929,13 @@ MxChoice choose_mx(const moe_mx_linear_desc& d) {
     const Few& f = few[mx];
     const double groups = row_tiles(16 * c.tt) * ceil(n / (16 * c.blocks)), pieces = ceil(K / 512);
     const double each = M / hit, rows = each < 16 * c.tt ? each : 16 * c.tt;
-    const double rounds = groups / (kCus * (8 / c.waves) * 2);
-    const double wait = (rounds > 1 ? rounds : 1) * (f.fixed + ceil(pieces / c.waves) * f.piece);
+    const double rounds = groups / (kCus * (8 / c.waves) * 2), near = weights_mb < 0.3 ? 0.5 : 1;   // (in the L2)
+    const double wait = (rounds > 1 ? rounds : 1) * (f.fixed + ceil(pieces / c.waves) * f.piece * near);
     const double read = f.fixed + groups * K / 512 * (16 * c.blocks * 0.266 * f.w_kb + rows * (mx ? 0.266 : 1) * f.x_kb) / kCus;
     const double all = weights_mb / few_rate[mx];
     take(c, wait > read ? (wait > all ? wait : all) : (read > all ? read : all));
   }
-  for (int t = T64; t <= T256; ++t) {
+  for (int t : {(int)T64, (int)T128, mx ? (int)T256 : (int)WIDE}) {
     const Fit& f = fits[mx][t];
     const double tiles = row_tiles(bm[t]) * ceil(n / bn[t]), steps = ceil(K / (mx ? 256 : 64));
     double share = ceil(tiles / kCus);
@@ -992,6 +985,14 @@ hipError_t launch_mx_dequantize(int64_t rows, int depth, const uint8_t* q, int64
   return hipGetLastError();
 }
 
+void mx_choice(const moe_mx_linear_desc& d, int32_t out[4]) {
+  const MxChoice c = choose_mx(d);
+  out[0] = c.kind;
+  out[1] = c.tt;
+  out[2] = c.blocks;
+  out[3] = c.waves;
+}
+
 hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const uint8_t* x_scale, const uint8_t* w,
                             const uint8_t* w_scale, const int32_t* offsets, const void* bias, void* out, hipStream_t s) {
   MxArgs a = {};
@@ -1027,13 +1028,17 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
       auto go = [&](auto tile) {
         using C = decltype(tile);
         launch_tiles(a, C::BM, G ? C::BN / 2 : C::BN, C::NT, [&](dim3 grid) {
-          if (d.dtype == MOE_MXFP4) hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a);
-          else if (d.dtype == MOE_F16) hipLaunchKernelGGL((mx_weights_kernel<C, true, G>), grid, dim3(C::NT), 0, s, a);
-          else hipLaunchKernelGGL((mx_weights_kernel<C, false, G>), grid, dim3(C::NT), 0, s, a);
+          if constexpr (!std::is_same_v<C, MxWide>)
+            if (d.dtype == MOE_MXFP4) hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a);
+          if constexpr (!std::is_same_v<C, Mx256>) {
+            if (d.dtype == MOE_F16) hipLaunchKernelGGL((mx_weights_kernel<C, true, G>), grid, dim3(C::NT), 0, s, a);
+            else if (d.dtype == MOE_BF16) hipLaunchKernelGGL((mx_weights_kernel<C, false, G>), grid, dim3(C::NT), 0, s, a);
+          }
         });
       };
       if (c.kind == T64) go(Mx64{});
       else if (c.kind == T128) go(Mx128{});
+      else if (c.kind == WIDE) go(MxWide{});
       else go(Mx256{});
     }
   });

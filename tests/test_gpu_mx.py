@@ -16,6 +16,7 @@ from test_gpu_linear import _forward_error
 
 pytestmark = pytest.mark.gpu
 
+U = 2.0 ** -24
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 
 
@@ -255,6 +256,59 @@ SIZES = [(1, 1, 32, 1), (1, 64, 2048, 1), (1, 200, 7168, 3), (2, 17, 64, 2), (5,
 def test_product(M, N, K, E, act):
     for i, (xt, out_t) in enumerate(TYPES):
         _check(M, N, K, E, act, xt, out_t, kind=["even", "loud", "few"][(i + M) % 3], bias=(i + M) % 2 == 0)
+
+
+# sizes that between them take every way of cutting a product, with sums over several tables of scales
+CUTS = [(25, 2060, 1184, 8), (700, 130, 1184, 1), (601, 130, 672, 2), (97, 700, 1184, 32), (2001, 30, 1184, 2), (193, 390, 672, 64),
+        (2500, 30, 2336, 1), (1281, 390, 1184, 64), (6401, 130, 672, 32), (22401, 30, 672, 32), (64001, 30, 672, 16), (9601, 130, 672, 64),
+        (40001, 30, 1184, 16), (32001, 130, 672, 32), (22401, 130, 1184, 32), (2561, 700, 672, 64), (32001, 130, 1184, 64)]
+
+
+def _values64(q, s):
+    """What packed rows stand for, in float64 on the GPU (powers of two from a table: exact)."""
+    power = torch.from_numpy(np.ldexp(1.0, np.arange(256) - 127)).cuda()[s.long()]
+    return torch.from_numpy(OM.ELEMENTS).cuda()[torch.stack([q & 15, q >> 4], -1).flatten(-2).long()] * power.repeat_interleave(32, -1)
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("M,N,K,E", CUTS)
+def test_every_cut(M, N, K, E, act):
+    """The same bound, with the float64 sums taken on the GPU: sizes too long for the oracle."""
+    m = _m()
+    gen = torch.Generator(device="cuda").manual_seed(M + N)
+    n = 2 * N if act == "swiglu" else N
+    off = _offsets(M, E, "loud" if M % 2 else "even", np.random.default_rng(M))
+    q, s = _weights(E, n, K, gen)
+    x = torch.randn(M, K, generator=gen, device="cuda")
+    b = torch.randn(E, n, generator=gen, device="cuda")
+    for xt in ("bf16", "f16", "mx"):
+        say(f"[mx linear] {M}x{N}x{K} E={E} {act} {xt}")
+        out = torch.full((M, N), 9.0, device="cuda")
+        if xt == "mx":
+            xq, xs = _quantize(x)
+            args, xr = dict(x=xq, x_scale=xs), _values64(xq, xs)
+        else:
+            args = dict(x=x.to(DT[xt]))
+            xr = args["x"].double()
+        # (fp16 holds these weights exactly: scales of 2^-9 to 2^-6)
+        m.moe_mx_linear(w=q, w_scale=s, out=out, offsets=torch.from_numpy(off).cuda(), bias=b, act=getattr(m, "ACT_" + act.upper()), **args)
+        for e in range(E):
+            lo, hi = int(off[e]), int(off[e + 1])
+            if lo == hi:
+                continue
+            w = _values64(q[e], s[e])
+            z = torch.mm(xr[lo:hi], w.t().contiguous()) + b[e].double()
+            ez = (K + 2) * U * (torch.mm(xr[lo:hi].abs(), w.t().contiguous().abs()) + b[e].double().abs())
+            if act == "swiglu":
+                g, u = z[:, :N], z[:, N:]
+                y = g * torch.sigmoid(g) * u
+                sg = (g * torch.sigmoid(g)).abs()
+                ez = (1.13 * ez[:, :N] * u.abs() + sg * ez[:, N:] + 1.13 * ez[:, :N] * ez[:, N:] +
+                      (16 * U + 64 * U * g.abs()) * sg * u.abs())
+            else:
+                y = z
+            err = (out[lo:hi].double() - y).abs()
+            assert bool((err <= ez * (1 + U) + U * y.abs()).all()), (xt, e, float((err - ez).max()))
 
 
 @pytest.mark.parametrize("kind", ["even", "loud", "few", "ends"])
