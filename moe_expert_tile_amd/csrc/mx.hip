@@ -708,6 +708,12 @@ void mx_both_kernel(MxArgs a) {
   });
 }
 
+// Where the 16-byte chunks of a pair of rows (p of 8) lie: c ^ spread(p).  A 16-byte LDS
+// read serves lanes 0-3, 12-15, 20-23 and 24-27 together, then the others of 32: with
+// blocks of 16 rows pairs 0, 1, 6, 7 at one chunk and pairs 2-5 at the chunk two further, so
+// that the latter's places have to be closed under that step.
+__device__ __forceinline__ int spread(int p) { return (p & 4) | (p & 1) << 1 | ((p >> 2 ^ p >> 1) & 1); }
+
 // Weights alone in 4 bits.  They lie in LDS as in memory, 32 bytes of a row a
 // stage, and become 16-bit operands on the way out of it.  A lane group g (B lanes) takes
 // the stage's elements from 8 KK g on, 8 for each of the KK matrix steps: of w 4 KK
@@ -743,7 +749,7 @@ void mx_weights_kernel(MxArgs a) {
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.x + p.row * a.ld_x, (arows - 1) * a.ld_x + 2 * a.K);
   const __amdgpu_buffer_rsrc_t br = make_rsrc(w, (brows - 1) * a.ld_w + a.K / 2);
   uint32_t aoff[A_LOADS], boff;
-  const int chunk = (lane % 8) ^ ((wave * 4 + lane / 16) % 8);
+  const int chunk = (lane % 8) ^ spread((wave * 4 + lane / 16) % 8);   // of a row in memory, the same in all of this lane's loads
 #pragma unroll
   for (int i = 0; i < A_LOADS; ++i) {
     const int r = (wave + i * C::NW) * 8 + lane / 8;
@@ -777,7 +783,7 @@ void mx_weights_kernel(MxArgs a) {
     *(v4u32*)(lds + STAGES * STAGE + (s & 1) * SCALES + tid * 16) = sc;
   };
 
-  const int lrow = lane % B, g = lane / B, rsw = (lrow / 2) % 8;
+  const int lrow = lane % B, g = lane / B, rsw = spread(lrow / 2 % 8);
   const int half = g * 2 / GROUPS;                           // this group's block of a stage
   const int bat = lrow * 32 + (half ^ (lrow / 8 % 2)) * 16 + g % (GROUPS / 2) * 8;
   acc_t acc[FN][FM];
