@@ -14,8 +14,8 @@
  *   - Device pointers are plain device addresses (hipMalloc or a torch
  *     tensor's data_ptr()).  bf16 tensors are passed as uint16_t bit patterns
  *     and must be 16-byte aligned; int32/uint32/float tensors 4-byte aligned
- *     (moe_route, moe_linear and their gradients: to their elements, where
- *     nothing else is said).
+ *     (moe_route, moe_linear, the calls on sorted rows and on 4-bit ones, and
+ *     their gradients: to their elements, where nothing else is said).
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *     Every call is asynchronous on it; nothing synchronises with the host
  *     except moe_device_status.
@@ -25,7 +25,9 @@
  *     cache of the compute-unit count, the LDS limit and that array's
  *     address.
  *   - The routing and dense-product calls (moe_route, moe_linear and their
- *     gradients) stand on their own: they take no plan and no moe_shape.
+ *     gradients), the calls on rows sorted by expert (moe_sort, moe_permute,
+ *     moe_unpermute) and on 4-bit rows (moe_mx_*) stand on their own: they take
+ *     no plan and no moe_shape.
  *   - Errors the device detects (an expert id out of range, a received-row
  *     count that disagrees with the routing, a consumer wait that timed out)
  *     are written to an error word inside the plan workspace and reported by

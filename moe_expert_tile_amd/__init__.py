@@ -1,7 +1,8 @@
 """Python binding of libmoe.so: one expert-parallel rank's share of an MoE
 layer on one MI355X (owner-aligned layout, remote-first schedule, grouped
 SwiGLU FFN with flagged epilogue, consumer copy, gate-weighted scale), and the
-operators around it (routing, dense product, their gradients and the scale's).
+operators around it (routing, dense product, their gradients and the scale's;
+rows sorted by expert and back; products with microscaled 4-bit weights).
 
 Argument marshalling only: every step runs in the HIP kernels of libmoe.so.
 Tensors are torch CUDA tensors (bf16 tensors may be torch.bfloat16 or

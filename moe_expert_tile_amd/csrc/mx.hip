@@ -55,7 +55,10 @@ __device__ __forceinline__ v4u32 widen(uint32_t q, float scale) {
 // Four neighbouring lanes share a block, eight elements each.  The largest
 // magnitude is found among bit patterns (infinities and NaN are above all
 // numbers that way), across the lanes by two DPP moves.  v_cvt_scalef32_pk_fp4_*
-// round to the nearest element, ties to the even one, and saturate at 6.
+// round to the nearest element, ties to the even one, and saturate at 6.  A thread
+// has four groups of eight in flight.  Bound by HBM: 16384 x 7168 from bf16, 297 MB, 51.7 us
+// (5.75 TB/s, a large copy 4.98), and back 56.4 us (5.27); 64 x 2048 take a launch.
+// A packed matrix is taken as one long row, without divisions.
 
 struct QuantArgs {
   const char* x;
@@ -280,6 +283,12 @@ __device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int left) {
 // block is the lane's part of the step's i-th v_mfma_f32_16x16x32.  A row's 16
 // scales of a piece are one load, of which step s needs byte lane / 16 of dword s.
 // Result lane: row (of x) lane % 16, columns 4 (lane / 16) .. + 3.
+// Measured with the weights in no cache (a call among others): 8 rows over 8 experts of 2 x
+// 2048 x 7168, 125 MB, 30.4 us (4.1 TB/s); 512 over 128 of 2 x 768 x 2048, 217 MB, 51 us
+// (4.3 TB/s).  With pieces of 128 elements and 8 wavefronts a workgroup they took 46 and
+// 133 us: 64 contiguous bytes a row and load, four times the loads of scales, and half as many
+// workgroups a CU.  x's operands are read a step ahead alone (all four steps' cost the
+// registers of a second workgroup: 62 instead of 57 us).
 template <int XT, bool GATED, int TT, int BLOCKS, int W>
 __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
   constexpr bool MX = XT == MOE_MXFP4, F16 = XT == MOE_F16;
@@ -450,6 +459,21 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
 // descriptor's bound, where loads return zeros.  Scales come through registers
 // (their rows may start at any byte), some stages' at a time, into a table of
 // their own in LDS, ahead of the stages that need them.
+//
+// Rates (gated, bf16 out, a call among others).  x in 16 bits: 8192 x 2 x 2048 x 7168 363 us,
+// 1.33 PFLOP/s; 16384 rows over 16 uneven experts of 2 x 1536 x 4096 366 us, 1.13.  x in 4
+// bits: 46451 over 32 of 2 x 2048 x 7168 841 us, 3.24 PFLOP/s; 8192 x 8192 x 8192 plain
+// 296 us, 3.72; 8192 x 4096 x 28672 465 us, 4.13.  Both are limited by power first: with
+// random operands in registers alone the card reaches 1.91 PFLOP/s in v_mfma_f32_32x32x16_bf16, 2.25 in
+// 16x16x32 and 6.8 in v_mfma_scale_f32_32x32x64 of 4 bits (9.4 with constant operands).
+// Of the 1.99 us a stage of the 256 x 256 tile takes with x in 4 bits, 1.66 remain without its loads and
+// 1.56 without its LDS reads either; a tile adds 13 us (start 3, epilogue 10, its stores being
+// two thirds of that), a fifth of the time at K = 7168.  Measured beside it: four wavefronts
+// of 128 x 128 4-10% slower; 128 x 256 tiles of 128-element stages, two workgroups a CU, 0-20%
+// slower; 16 x 16 steps 40-80% slower (registers).  With x in 16 bits 128 x 256 tiles, whose
+// two workgroups a CU overlap one's epilogue with the other's sums, take 366 us where 256 x 256
+// ones take 391, and 193 us for 8192 x 7168 x 2048 (211); where tiles fit the CUs
+// exactly and sums are long they are 3% slower.
 
 // WAVES_SIMD: wavefronts a SIMD that the registers are limited for; B16: block of the matrix
 // steps with x in 16 bits
@@ -464,7 +488,7 @@ struct MxTile {
 typedef MxTile<256, 256, 2, 4, 2, 16> Mx256;     // x in 4 bits
 typedef MxTile<128, 256, 2, 4, 4, 16> MxWide;    // x in 16 bits: two workgroups a CU
 typedef MxTile<128, 128, 2, 2, 1, 32> Mx128;
-typedef MxTile<64, 128, 2, 2, 1, 32> Mx64;
+typedef MxTile<64, 128, 2, 2, 1, 32> Mx64;       // (16 x 16 steps: 4096 rows over 128 experts of 2 x 768 x 2048 84 us instead of 79)
 
 // vmcnt(flying) lgkmcnt(0) and the workgroup's barrier
 template <int FLYING>
@@ -871,8 +895,8 @@ QuantArgs quant_args(int64_t rows, int depth, const void* x, int size, int64_t l
     a.rows = 1;
   }
   const int64_t per = 256 * kQuantUnroll, across = (a.n8 + per - 1) / per;
-  *grid = dim3((unsigned)(across < (1 << 16) ? across : 1 << 16), (unsigned)(a.rows < 4096 ? a.rows : 4096));
-  if (across * a.rows > (1 << 20)) grid->x = (unsigned)(across < 256 ? across : 256);
+  const int64_t gx = across < (1 << 16) ? across : 1 << 16, gy = (1 << 20) / gx;
+  *grid = dim3((unsigned)gx, (unsigned)(a.rows < gy ? a.rows : (gy < 65535 ? gy : 65535)));
   return a;
 }
 

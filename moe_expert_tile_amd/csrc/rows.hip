@@ -9,7 +9,9 @@
 // lanes with its key, found with one ballot per key bit.  Long batches take two
 // launches: per-workgroup histograms, then the same walk, in which every
 // workgroup sums the histograms of those before it.  Integer sums only, so the
-// result is the same in any order of the atomics.
+// result is the same in any order of the atomics.  Bound by latency: 64 x 8 ids over
+// 128 experts 3.8 us (the kernel), 32768 x 8 over 256 11 us a call, 2.6 + 9.3 us in its two kernels (its
+// bytes, 3.1 MB, would take 0.6); 8 million pairs take 97 us.
 #include "product.h"
 
 namespace moe {
@@ -235,7 +237,8 @@ struct Row {
 __device__ __forceinline__ bool held(const RowArgs& a, int p) { return (uint64_t)(int64_t)p < (uint64_t)a.rows; }
 
 // Each wavefront takes U KB of a token's row at a time, reads it once and writes
-// it to the token's rows.
+// it to the token's rows.  Bound by HBM: 8192 x 8 rows of 4096 bf16 columns, 604 MB,
+// 106 us (5.7 TB/s); few tokens take 1 KB a wavefront, so that they spread over the CUs.
 template <int SIZE, bool WHOLE, int POLICY, int U>
 __global__ __launch_bounds__(256) void permute_kernel(RowArgs a) {
   const int lane = threadIdx.x & 63;
@@ -260,7 +263,8 @@ __global__ __launch_bounds__(256) void permute_kernel(RowArgs a) {
 }
 
 // Sum of a token's rows, weighted or not, in slot order in fp32: a wavefront
-// takes U KB of a token's row and has the loads of four slots in flight.
+// takes U KB of a token's row and has the loads of four slots in flight.  Bound by HBM:
+// the same size 103 us (5.8 TB/s); a decode step of 64 x 8 x 2048 4.4 us, a launch.
 template <int T, bool WEIGHTED, bool WHOLE, int POLICY, int U>
 __global__ __launch_bounds__(256) void unpermute_kernel(RowArgs a) {
   typedef Type<T> E;
@@ -312,7 +316,8 @@ __global__ __launch_bounds__(256) void unpermute_kernel(RowArgs a) {
 // Gradients of the sum: a wavefront per slot reads the token's gradient and, for
 // the weight's, the slot's row, writes the row's gradient and reduces the product
 // in fp32.  A token's slots are neighbouring wavefronts, so its gradient comes
-// from the caches after the first of them.
+// from the caches after the first of them.  Bound by HBM: 4097 x 8 x 7168, 1.0 GB, 190 us
+// (5.2 TB/s), 202 with ordinary accesses.
 template <int T, bool DROWS, bool DW, bool WHOLE, int POLICY>
 __global__ __launch_bounds__(256) void unpermute_back_kernel(RowArgs a) {
   typedef Type<T> E;
