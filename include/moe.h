@@ -444,7 +444,7 @@ int moe_sort_sizes(int64_t tokens, int32_t top_k, int32_t experts, size_t* ws_by
  *   offsets   device int32 [experts + 1]: rows offsets[e] .. offsets[e + 1] - 1 are expert first + e's.
  *   ws        device workspace, 256-byte aligned, of moe_sort_sizes' bytes (NULL if that is 0); calls that
  *             overlap on the device need one each.
- * tokens <= 2^26, experts <= 1024, top_k <= 32, tokens * top_k < 2^31, first >= 0.
+ * tokens <= 2^26, experts <= 1024, top_k <= 32, tokens * top_k < 2^31, 0 <= first <= 2^31 - experts.
  */
 int moe_sort(int64_t tokens, int32_t top_k, int32_t experts, int32_t first, const int32_t* topk_ids, int32_t* pos,
              int32_t* src, int32_t* offsets, void* ws, void* stream);
@@ -543,9 +543,9 @@ typedef struct moe_mx_linear_desc {
 /*
  * moe_mx_linear — out[r] = act(x[r] w[e]^T + bias[e]) for the rows r of each
  * expert e, with weights in microscaled 4 bits and fp32 sums, rounded once.  With
- * x in 16 bits the weights are taken in x's type: exactly in MOE_BF16; in
- * MOE_F16 those of magnitude 65520 and above are infinite and bits below
- * 2^-24 are rounded.  With x in MOE_MXFP4 the products are exact.
+ * x in 16 bits the weights are taken in x's type: exactly in MOE_BF16, those of
+ * magnitude 2^128 and above infinite; in MOE_F16 those of 65520 and above are infinite
+ * and bits below 2^-24 are rounded.  With x in MOE_MXFP4 the products are exact.
  *   x         device [rows, depth], 16-byte aligned; MOE_MXFP4: packed rows [rows, depth / 2].
  *   x_scale   device [rows, depth / 32] with MOE_MXFP4, else not read.
  *   w         device [experts, n, depth / 2], 16-byte aligned;  w_scale  device [experts, n, depth / 32].

@@ -224,7 +224,7 @@ int moe_sort(int64_t tokens, int32_t top_k, int32_t experts, int32_t first, cons
   size_t bytes;
   int rc = moe_sort_sizes(tokens, top_k, experts, &bytes);
   if (rc) return rc;
-  if (first < 0 || !aligned_to(topk_ids, 4) || !aligned_to(pos, 4) || !aligned_to(src, 4) || !aligned_to(offsets, 4) ||
+  if (first < 0 || first > INT32_MAX - experts + 1 || !aligned_to(topk_ids, 4) || !aligned_to(pos, 4) || !aligned_to(src, 4) || !aligned_to(offsets, 4) ||
       !aligned_to(ws, 256))
     return MOE_EINVAL;
   if (!offsets || (tokens > 0 && (!topk_ids || !pos)) || (bytes > 0 && !ws)) return MOE_EINVAL;

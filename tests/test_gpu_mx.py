@@ -341,6 +341,59 @@ def test_scales_over_a_wide_range(xt):
         _check(M, N, K, 2, "none", xt, "f32", spread=30)
 
 
+@pytest.mark.parametrize("M", [6, 300])
+@pytest.mark.parametrize("xt", ["bf16", "f16", "mx"])
+def test_scales_at_both_ends(M, xt):
+    """One element a row of w, of every code over scales from 2^-127 to 2^127, times rows of a power of two each: every
+    sum is one product, exact but for the ends of the types."""
+    m = _m()
+    K = 128
+    scales = [0, 1, 2, 60, 101, 103, 112, 127, 141, 142, 190, 252, 253, 254]
+    rows = [(c, s) for s in scales for c in range(1, 16) if c != 8]
+    q, s = np.zeros((len(rows), K // 2), np.uint8), np.full((len(rows), K // 32), 254, np.uint8)
+    for n, (c, sc) in enumerate(rows):
+        at = (37 * n) % K
+        q[n, at // 2] = c << (at % 2 * 4)
+        s[n, at // 32] = sc
+    w = OM.values(q, s)
+    low, high = {"bf16": (-133, 127), "f16": (-24, 15), "mx": (-127, 127)}[xt]
+    power = np.linspace(low, high, M).astype(np.int64)
+    out = torch.empty(M, len(rows), device="cuda")
+    qg, sg = torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda()
+    if xt == "mx":
+        x = torch.full((M, K // 2), 0x22, dtype=torch.uint8, device="cuda")           # 1 and 1
+        xs = torch.from_numpy(np.repeat((power + 127).astype(np.uint8)[:, None], K // 32, 1)).cuda()
+        m.moe_mx_linear(x, qg, sg, out, x_scale=xs)
+    else:
+        x = torch.from_numpy(np.repeat(np.ldexp(1.0, power)[:, None], K, 1)).to(DT[xt]).cuda()
+        m.moe_mx_linear(x, qg, sg, out)
+        w = _np(torch.from_numpy(w).float().to(DT[xt]))
+    w = w.sum(1)                                       # the row's element (the others are zeros)
+    with np.errstate(over="ignore"):
+        want = (np.ldexp(1.0, power)[:, None] * w[None]).astype(np.float32)
+    got = out.cpu().numpy()
+    assert np.array_equal(got, want), [(int(power[i]), rows[j], got[i, j], want[i, j]) for i, j in np.argwhere(got != want)[:6]]
+
+
+@pytest.mark.skipif(not (hasattr(torch, "float4_e2m1fn_x2") and hasattr(torch, "float8_e8m0fnu")), reason="no such types")
+def test_bytes_under_their_own_types():
+    m = _m()
+    x = torch.randn(40, 128, device="cuda").bfloat16()
+    q, s = _quantize(x)
+    q4, s8 = q.view(torch.float4_e2m1fn_x2), s.view(torch.float8_e8m0fnu)
+    q2, s2 = torch.zeros_like(q), torch.zeros_like(s)
+    m.moe_mx_quantize(x, q2.view(torch.float4_e2m1fn_x2), s2.view(torch.float8_e8m0fnu))
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    back, back2 = torch.empty_like(x), torch.empty_like(x)
+    m.moe_mx_dequantize(q, s, back)
+    m.moe_mx_dequantize(q4, s8, back2)
+    assert torch.equal(back, back2)
+    y, y2 = torch.empty(40, 40, device="cuda"), torch.empty(40, 40, device="cuda")
+    m.moe_mx_linear(q, q, s, y, x_scale=s)
+    m.moe_mx_linear(q4, q4[None], s8[None], y2, x_scale=s8)
+    assert torch.equal(y, y2)
+
+
 def test_one_expert_without_offsets():
     for xt, out_t in TYPES:
         _check(40, 50, 96, 1, "none", xt, out_t, offsets=False)

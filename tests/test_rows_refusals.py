@@ -24,7 +24,7 @@ def _m():
 @built
 @pytest.mark.parametrize("bad", [
     dict(tokens=-1), dict(tokens=(1 << 26) + 1), dict(top_k=0), dict(top_k=33), dict(experts=0), dict(experts=1025),
-    dict(tokens=1 << 26, top_k=32), dict(first=-1), dict(ids=0), dict(ids=GOOD + 2), dict(pos=0), dict(pos=GOOD + 1),
+    dict(tokens=1 << 26, top_k=32), dict(first=-1), dict(first=2 ** 31 - 15), dict(ids=0), dict(ids=GOOD + 2), dict(pos=0), dict(pos=GOOD + 1),
     dict(src=GOOD + 2), dict(offsets=0), dict(offsets=GOOD + 2), dict(ws=GOOD + 128), dict(tokens=32768, ws=0)])
 def test_bad_sorts_are_rejected(bad):
     m = _m()
