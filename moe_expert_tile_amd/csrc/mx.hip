@@ -528,6 +528,14 @@ __device__ __forceinline__ int block_row(int wave_n, int i) {
   else return wave_n * C::WN + B * i;
 }
 
+// whether any of a wavefront's part of the tile exists: at an expert's or w's end the
+// others only load, and leave the matrix cores to those that share theirs (2048 rows over 32
+// experts of 2 x 2048 x 7168, x in 4 bits, 152 -> 150 us; 4096 over 128 of 2 x 768 x 2048, bf16, 78 -> 76)
+template <class C, bool GATED>
+__device__ __forceinline__ bool has_results(const Place& p, int wave_m, int wave_n) {
+  return wave_m * C::WM < p.rows && wave_n * (GATED ? C::WN / 2 : C::WN) < p.cols;
+}
+
 // 32 rows of a wavefront's columns at a time go through LDS, so that lanes hold
 // neighbouring columns and every global access covers whole lines.
 // put(j, to): the sums of rows 32 j .. + 31 to `to`, rows C::PITCH floats apart.
@@ -669,10 +677,13 @@ void mx_both_kernel(MxArgs a) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  auto step = [&](int k) __attribute__((always_inline)) {
+  auto ready = [&](int k) __attribute__((always_inline)) {   // stage k is there, the next ones under way
     meet<0>();
     if ((k & 3) == 0 && k + 4 < KT) fetch_scales(k / 4 + 1);
     if ((k & 3) == 1 && k + 3 < KT) keep_scales(k / 4 + 1);
+  };
+  auto step = [&](int k) __attribute__((always_inline)) {
+    ready(k);
     const char* sa = lds + (k & 1) * STAGE;
     const char* sb = sa + A_BYTES;
     const char* ss = lds + 2 * STAGE + (k / 4 & 1) * SCALES + (((k / 2 & 1) ^ ssw) * 16 + (k & 1) * 8 + lhalf * 4);
@@ -719,8 +730,16 @@ void mx_both_kernel(MxArgs a) {
   fetch_scales(0);
   issue(0);
   keep_scales(0);
+  if (has_results<C, GATED>(p, wave_m, wave_n)) {
 #pragma unroll 1
-  for (int k = 0; k < KT; ++k) step(k);
+    for (int k = 0; k < KT; ++k) step(k);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < KT; ++k) {
+      ready(k);
+      issue(k + 1);
+    }
+  }
   meet<0>();   // every wave is done with the operands
   finish_tile<C, GATED>(a, p, lds, wave, lane, [&](int j, float* to) __attribute__((always_inline)) {
 #pragma unroll
@@ -817,10 +836,13 @@ void mx_weights_kernel(MxArgs a) {
     for (int j = 0; j < FM; ++j) acc[i][j] = acc_t{};
 
   // stage k in `slot`, the one STAGES - 1 ahead into `next`
-  auto step = [&](int k, int slot, int next) __attribute__((always_inline)) {
+  auto ready = [&](int k) __attribute__((always_inline)) {
     meet<(STAGES - 2) * (A_LOADS + 1)>();
     if ((k & 7) == 0 && k + 8 < KT) fetch_scales(k / 8 + 1);
     if ((k & 7) == 4 && k + 4 < KT) keep_scales(k / 8 + 1);
+  };
+  auto step = [&](int k, int slot, int next) __attribute__((always_inline)) {
+    ready(k);
     const char* sa = lds + slot * STAGE + (wave_m * C::WM + lrow) * 128;
     const char* sb = lds + slot * STAGE + A_BYTES + bat;
     const uint8_t* ss = (const uint8_t*)lds + STAGES * STAGE + (k / 8 & 1) * SCALES + lrow * 16 + (k & 7) * 2 + half;
@@ -858,11 +880,21 @@ void mx_weights_kernel(MxArgs a) {
   for (int k = 0; k < STAGES - 1; ++k) issue(k, k);
   keep_scales(0);
   int slot = 0, next = STAGES - 1;
+  auto all_stages = [&](auto one) __attribute__((always_inline)) {
 #pragma unroll 1
-  for (int k = 0; k < KT; ++k) {
-    step(k, slot, next);
-    slot = slot + 1 == STAGES ? 0 : slot + 1;
-    next = next + 1 == STAGES ? 0 : next + 1;
+    for (int k = 0; k < KT; ++k) {
+      one(k);
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+      next = next + 1 == STAGES ? 0 : next + 1;
+    }
+  };
+  if (has_results<C, GATED>(p, wave_m, wave_n)) {
+    all_stages([&](int k) __attribute__((always_inline)) { step(k, slot, next); });
+  } else {
+    all_stages([&](int k) __attribute__((always_inline)) {
+      ready(k);
+      issue(k + STAGES - 1, next);
+    });
   }
   meet<0>();   // every wave is done with the operands
   finish_tile<C, GATED>(a, p, lds, wave, lane, [&](int j, float* to) __attribute__((always_inline)) {
