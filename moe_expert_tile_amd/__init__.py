@@ -551,16 +551,24 @@ def moe_sort(topk_ids, pos, offsets, src=None, first: int = 0, ws=None, stream=N
     _launch(where, index, stream, _lib.moe_sort, T, k, E, _int(first), *args, None if ws is None else ws.data_ptr())
 
 
-def _rows_desc(where, x, x_name, rows, rows_name, pos):
-    """The sizes of a call on sorted rows, and the GPU."""
+# the descriptors of sizes, which calls in a loop repeat: never written after they are made
+_rows_sizes = functools.lru_cache(maxsize=256, typed=True)(moe_rows_desc)
+_mx_sizes = functools.lru_cache(maxsize=256, typed=True)(moe_mx_linear_desc)
+
+
+def _rows_desc(where, x, x_name, rows, rows_name, pos, second=None):
+    """The sizes of a call on sorted rows, and the GPU.  second: a matrix like
+    rows under the name "rows", which then is the one of ld_rows."""
     (T, k), index = _pairs(where, "pos", pos)
     dtype = x.dtype
     code = _DTYPES.get(dtype)
     if code is None or x.dim() != 2 or rows.dim() != 2:
         raise _invalid(where, f"{x_name} and {rows_name} are matrices of bfloat16, float16 or float32")
     d, R = x.shape[1], rows.shape[0]
-    return moe_rows_desc(T, R, k, d, code, 0, _matrix(where, x_name, x, (T, d), dtype, index),
-                         _matrix(where, rows_name, rows, (R, d), dtype, index), 0), index
+    ld_x, ld_rows = _matrix(where, x_name, x, (T, d), dtype, index), _matrix(where, rows_name, rows, (R, d), dtype, index)
+    if second is None:
+        return _rows_sizes(T, R, k, d, code, 0, ld_x, ld_rows, ld_rows), index
+    return _rows_sizes(T, R, k, d, code, 0, ld_x, _matrix(where, "rows", second, (R, d), dtype, index), ld_rows), index
 
 
 def moe_permute(x, pos, rows, stream=None) -> None:
@@ -594,10 +602,7 @@ def moe_unpermute_backward(pos, d_out, rows=None, topk_w=None, d_rows=None, d_to
     given, name = (rows, "rows") if d_rows is None else (d_rows, "d_rows")
     if given is None:
         raise _invalid(where, "neither d_rows nor rows is given")
-    d, index = _rows_desc(where, d_out, "d_out", given, name, pos)
-    if d_rows is not None:
-        d.ld_d_rows = d.ld_rows
-        d.ld_rows = _matrix(where, "rows", rows, given.shape, d_out.dtype, index)
+    d, index = _rows_desc(where, d_out, "d_out", given, name, pos, None if d_rows is None else rows)
     _launch(where, index, stream, _lib.moe_unpermute_backward, d, _ptr(rows), pos.data_ptr(),
             _packed(where, "topk_w", topk_w, pos.shape, torch.float32, index), d_out.data_ptr(), _ptr(d_rows),
             _packed(where, "d_topk_w", d_topk_w, pos.shape, torch.float32, index))
@@ -692,8 +697,8 @@ def moe_mx_linear(x, w, w_scale, out, offsets=None, x_scale=None, bias=None, act
     ld_ws, expert_ws = _experts(where, "w_scale", w_scale, (E, n, K // MX_BLOCK), _MX_SCALES, index)
     if bias is not None:
         bias = _packed(where, "bias", bias, (E, n) if bias.dim() > 1 or E > 1 else (n,), out.dtype, index)
-    d = moe_mx_linear_desc(M, E, N, K, xt, code, act, ld_x, ld_xs, ld_w, ld_ws, expert_w, expert_ws,
-                           _matrix(where, "out", out, out.shape, out.dtype, index))
+    d = _mx_sizes(M, E, N, K, xt, code, act, ld_x, ld_xs, ld_w, ld_ws, expert_w, expert_ws,
+                  _matrix(where, "out", out, (M, N), out.dtype, index))
     _launch(where, index, stream, _lib.moe_mx_linear, d, x.data_ptr(), _ptr(x_scale), w.data_ptr(), w_scale.data_ptr(),
             _packed(where, "offsets", offsets, (E + 1,), torch.int32, index), bias, out.data_ptr())
 
