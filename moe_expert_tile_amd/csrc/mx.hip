@@ -475,11 +475,11 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
 // ones take 391, and 193 us for 8192 x 7168 x 2048 (211); where tiles fit the CUs
 // exactly and sums are long they are 3% slower.
 
-// WAVES_SIMD: wavefronts a SIMD that the registers are limited for; B16: block of the matrix
-// steps with x in 16 bits
-template <int BM_, int BN_, int WAVES_M, int WAVES_N, int WAVES_SIMD_, int B16_>
+// WAVES_SIMD: wavefronts a SIMD that the registers are limited for; B16, STAGES16: block of the
+// matrix steps and stages in LDS with x in 16 bits
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int WAVES_SIMD_, int B16_, int STAGES16_ = 3>
 struct MxTile {
-  static constexpr int BM = BM_, BN = BN_, WAVES_SIMD = WAVES_SIMD_, B16 = B16_;
+  static constexpr int BM = BM_, BN = BN_, WAVES_SIMD = WAVES_SIMD_, B16 = B16_, STAGES16 = STAGES16_;
   static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64, WN_ = WAVES_N;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int PITCH = WN + 4;            // floats of a row in the epilogue's staging
@@ -488,6 +488,7 @@ struct MxTile {
 typedef MxTile<256, 256, 2, 4, 2, 16> Mx256;     // x in 4 bits
 typedef MxTile<128, 256, 2, 4, 4, 16> MxWide;    // x in 16 bits: two workgroups a CU
 typedef MxTile<128, 128, 2, 2, 1, 32> Mx128;
+typedef MxTile<32, 256, 1, 4, 1, 32, 5> Mx32;    // x in 16 bits: 12 to 40 rows an expert
 typedef MxTile<64, 128, 2, 2, 1, 32> Mx64;       // (16 x 16 steps: 4096 rows over 128 experts of 2 x 768 x 2048 84 us instead of 79)
 
 // vmcnt(flying) lgkmcnt(0) and the workgroup's barrier
@@ -769,12 +770,12 @@ void mx_weights_kernel(MxArgs a) {
   constexpr int FM = C::WM / B, FN = C::WN / B;
   typedef uint32_t part_t __attribute__((ext_vector_type(KK)));
   typedef std::conditional_t<B == 32, f32x16, f32x4> acc_t;
-  constexpr int STAGES = 3;
+  constexpr int STAGES = C::STAGES16;
   constexpr int A_BYTES = C::BM * 128, STAGE = A_BYTES + C::BN * 32;
   constexpr int SCALES = C::BN * 16;                        // eight stages' scales
-  constexpr int A_LOADS = C::BM / 8 / C::NW;
+  constexpr int A_LOADS = C::BM / 8 / C::NW, B_LOADS = C::BN / 32 / C::NW;
   constexpr int RING = STAGES * STAGE + 2 * SCALES, LDS = RING > C::EPI ? RING : C::EPI;
-  static_assert(LDS <= 160 * 1024 && C::NW % 2 == 0 && C::BN == 32 * C::NW && STAGES <= 6, "tile");
+  static_assert(LDS <= 160 * 1024 && C::NW % 2 == 0 && C::BN % (32 * C::NW) == 0 && C::BN <= C::NT && STAGES <= 6, "tile");
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -786,12 +787,10 @@ void mx_weights_kernel(MxArgs a) {
   const int kscales = a.K / 32;
   const int KT = (a.K + 63) / 64;
 
-  // this wavefront's 32 rows of w, all of one half of a gated tile
-  const int up = GATED && wave * 32 >= HB ? 1 : 0;
-  const char* w = a.w + p.expert * a.expert_w + ((int64_t)up * a.N + p.n0) * a.ld_w;
+  const char* w = a.w + p.expert * a.expert_w + p.n0 * a.ld_w;
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(a.x + p.row * a.ld_x, (arows - 1) * a.ld_x + 2 * a.K);
-  const __amdgpu_buffer_rsrc_t br = make_rsrc(w, (brows - 1) * a.ld_w + a.K / 2);
-  uint32_t aoff[A_LOADS], boff;
+  __amdgpu_buffer_rsrc_t br[B_LOADS];
+  uint32_t aoff[A_LOADS], boff[B_LOADS];
   const int chunk = (lane % 8) ^ spread((wave * 4 + lane / 16) % 8);   // of a row in memory, the same in all of this lane's loads
 #pragma unroll
   for (int i = 0; i < A_LOADS; ++i) {
@@ -799,9 +798,12 @@ void mx_weights_kernel(MxArgs a) {
     aoff[i] = r < arows ? (uint32_t)r * (uint32_t)a.ld_x + chunk * 16 : kPastEnd;
   }
   const int block = (lane % 2) ^ (lane / 16 % 2);           // blocks of rows 8 .. 15 of 16 swapped
-  {
-    const int r = wave * 32 - up * HB + lane / 2;
-    boff = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + block * 16 : kPastEnd;
+#pragma unroll
+  for (int i = 0; i < B_LOADS; ++i) {                        // 32 rows of w, all of one half of a gated tile
+    const int first = (wave + i * C::NW) * 32, up = GATED && first >= HB ? 1 : 0;
+    const int r = first - up * HB + lane / 2;
+    br[i] = make_rsrc(w + (int64_t)up * a.N * a.ld_w, (brows - 1) * a.ld_w + a.K / 2);
+    boff[i] = r < brows ? (uint32_t)r * (uint32_t)a.ld_w + block * 16 : kPastEnd;
   }
   auto issue = [&](int k, int slot) __attribute__((always_inline)) {
     char* base = lds + slot * STAGE;
@@ -809,7 +811,9 @@ void mx_weights_kernel(MxArgs a) {
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i)
       load_lds(ar, base + (wave + i * C::NW) * 1024, chunk * 8 < left ? aoff[i] : kPastEnd, 128 * k);
-    load_lds(br, base + A_BYTES + wave * 1024, block * 32 < left ? boff : kPastEnd, 32 * k);
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i)
+      load_lds(br[i], base + A_BYTES + (wave + i * C::NW) * 1024, block * 32 < left ? boff[i] : kPastEnd, 32 * k);
   };
   // scales of stages 8 s .. 8 s + 7: 16 bytes of w's row tid
   v4u32 sc = {0, 0, 0, 0};
@@ -837,7 +841,7 @@ void mx_weights_kernel(MxArgs a) {
 
   // stage k in `slot`, the one STAGES - 1 ahead into `next`
   auto ready = [&](int k) __attribute__((always_inline)) {
-    meet<(STAGES - 2) * (A_LOADS + 1)>();
+    meet<(STAGES - 2) * (A_LOADS + B_LOADS)>();
     if ((k & 7) == 0 && k + 8 < KT) fetch_scales(k / 8 + 1);
     if ((k & 7) == 4 && k + 4 < KT) keep_scales(k / 8 + 1);
   };
@@ -940,7 +944,7 @@ void with_flag(bool b, F f) {
 
 // How a product is cut: few rows (16 tt rows, `blocks` blocks of w's rows, `waves`
 // wavefronts a workgroup) or a tile.
-enum MxKind { FEW, T64, T128, T256, WIDE };
+enum MxKind { FEW, T64, T128, T256, WIDE, T32 };
 struct MxChoice {
   MxKind kind;
   int tt, blocks, waves;   // FEW
@@ -953,21 +957,22 @@ struct MxChoice {
 // start and epilogue.  A few-row workgroup takes a fixed time and one for each piece of
 // K its wavefronts take in turn; all of them together what their reads take.  Neither is
 // faster than the weights' reading.  The constants are fitted to the times of every
-// choice over 198 products of each kind (1 to 32768 rows, 1 to 128 experts): the
-// choice costs 2.6% over the best one on average with x in 16 bits, 3.7% in 4.
+// choice over 252 products with x in 16 bits and 198 in 4 (1 to 32768 rows, 1 to 128
+// experts): the choice costs 2.9% over the best one on average, 3.7% in 4 bits.
 // Both sides of typical decisions, gated products with x in bf16: 8 rows over 8 experts of
 // 2 x 2048 x 7168 take 31 us as few rows and 58 us in tiles of 64 rows; 1024 over 32 of them
-// 239 us as few rows, 196 in 64 x 128 tiles and 215 in 128 x 128; 16384 over 16 of 2 x 1536
-// x 4096 487 us in 64 x 128, 422 in 128 x 128, 366 in 128 x 256 and 391 in 256 x 256 ones.
+// 239 us as few rows, 196 in 64 x 128 tiles and 187 in 128 x 256; 384 over 32 of 7168 x 2048 (no
+// gate) 76 us in 64 x 128 tiles and 67 in 32 x 256; 16384 over 16 of 2 x 1536 x 4096 487 us in
+// 64 x 128, 422 in 128 x 128, 355 in 128 x 256 and 391 in 256 x 256 ones.
 MxChoice choose_mx(const moe_mx_linear_desc& d) {
   struct Fit { double latency, shared, round_us; };
   struct Few { double fixed, piece, w_kb, x_kb; };
-  static const int bm[5] = {0, 64, 128, 256, 128}, bn[5] = {0, 128, 128, 256, 256};
-  static const int per_cu[2][5] = {{0, 3, 2, 1, 2}, {0, 2, 2, 1, 0}};
-  static const Fit fits[2][5] = {{{}, {0.412, 0.26, 1.8}, {0.547, 0.454, 3.9}, {}, {0.75, 0.6, 7.0}},
-                                 {{}, {0.507, 0.538, 3.13}, {0.606, 0.588, 5.7}, {1.76, 0.96, 8.84}, {}}};
-  static const Few few[2] = {{1.82, 2.92, 0.0783, 0.0097}, {2.01, 2.07, 0.0485, 0.0107}};
-  static const double tile_rate[2] = {3.15, 3.9}, few_rate[2] = {6.79, 3.97};   // MB/us of weights
+  static const int bm[6] = {0, 64, 128, 256, 128, 32}, bn[6] = {0, 128, 128, 256, 256, 256};
+  static const int per_cu[2][6] = {{0, 3, 2, 0, 2, 2}, {0, 2, 2, 1, 0, 0}};
+  static const Fit fits[2][6] = {{{}, {0.406, 0.284, 1.76}, {0.547, 0.436, 3.57}, {}, {0.673, 0.593, 7.72}, {0.467, 0.344, 3.56}},
+                                 {{}, {0.507, 0.538, 3.13}, {0.606, 0.588, 5.7}, {1.76, 0.96, 8.84}, {}, {}}};
+  static const Few few[2] = {{1.98, 2.83, 0.0778, 0.00733}, {2.01, 2.07, 0.0485, 0.0107}};
+  static const double tile_rate[2] = {3.15, 3.9}, few_rate[2] = {8.26, 3.97};   // MB/us of weights
   static const MxChoice fews[] = {{FEW, 1, 2, 2}, {FEW, 1, 2, 4}, {FEW, 1, 4, 4}, {FEW, 2, 4, 4}};
   constexpr double kCus = 256;
   const int mx = d.dtype == MOE_MXFP4;
@@ -997,7 +1002,8 @@ MxChoice choose_mx(const moe_mx_linear_desc& d) {
     const double all = weights_mb / few_rate[mx];
     take(c, wait > read ? (wait > all ? wait : all) : (read > all ? read : all));
   }
-  for (int t : {(int)T64, (int)T128, mx ? (int)T256 : (int)WIDE}) {
+  for (int t : {(int)T64, (int)T128, (int)T256, (int)WIDE, (int)T32}) {
+    if (per_cu[mx][t] == 0) continue;          // not with such an x
     const Fit& f = fits[mx][t];
     const double tiles = row_tiles(bm[t]) * ceil(n / bn[t]), steps = ceil(K / (mx ? 256 : 64));
     double share = ceil(tiles / kCus);
@@ -1090,7 +1096,7 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
       auto go = [&](auto tile) {
         using C = decltype(tile);
         launch_tiles(a, C::BM, G ? C::BN / 2 : C::BN, C::NT, [&](dim3 grid) {
-          if constexpr (!std::is_same_v<C, MxWide>)
+          if constexpr (!std::is_same_v<C, MxWide> && !std::is_same_v<C, Mx32>)
             if (d.dtype == MOE_MXFP4) hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a);
           if constexpr (!std::is_same_v<C, Mx256>) {
             if (d.dtype == MOE_F16) hipLaunchKernelGGL((mx_weights_kernel<C, true, G>), grid, dim3(C::NT), 0, s, a);
@@ -1098,7 +1104,8 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
           }
         });
       };
-      if (c.kind == T64) go(Mx64{});
+      if (c.kind == T32) go(Mx32{});
+      else if (c.kind == T64) go(Mx64{});
       else if (c.kind == T128) go(Mx128{});
       else if (c.kind == WIDE) go(MxWide{});
       else go(Mx256{});

@@ -261,7 +261,8 @@ def test_product(M, N, K, E, act):
 # sizes that between them take every way of cutting a product, with sums over several tables of scales
 CUTS = [(25, 2060, 1184, 8), (700, 130, 1184, 1), (601, 130, 672, 2), (97, 700, 1184, 32), (2001, 30, 1184, 2), (193, 390, 672, 64),
         (2500, 30, 2336, 1), (1281, 390, 1184, 64), (6401, 130, 672, 32), (22401, 30, 672, 32), (64001, 30, 672, 16), (9601, 130, 672, 64),
-        (40001, 30, 1184, 16), (32001, 130, 672, 32), (22401, 130, 1184, 32), (2561, 700, 672, 64), (32001, 130, 1184, 64)]
+        (40001, 30, 1184, 16), (32001, 130, 672, 32), (22401, 130, 1184, 32), (2561, 700, 672, 64), (32001, 130, 1184, 64),
+        (1601, 700, 1184, 64), (1600, 1030, 672, 64)]
 
 
 def _values64(q, s):
