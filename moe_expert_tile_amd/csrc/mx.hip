@@ -208,15 +208,33 @@ __device__ __forceinline__ int lane_scan(int v) {
   return v;
 }
 
+// Rows of four experts from the lane's on: their first rows and numbers of tiles of bm.
+// Four a lane, so that 256 experts' offsets are in flight together.
+struct Four {
+  int lo[4], hi[4], n[4], all;
+};
+__device__ __forceinline__ Four four_experts(const MxArgs& a, int bm, int e) {
+  const int rows = (int)a.rows;
+  int at[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) at[i] = a.offsets[min(e + i, a.E)];
+  Four f;
+  f.all = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {                 // past the last expert: no rows
+    f.lo[i] = min(max(at[i], 0), rows);
+    f.hi[i] = min(max(at[i + 1], 0), rows);
+    f.n[i] = f.hi[i] > f.lo[i] ? (f.hi[i] - f.lo[i] + bm - 1) / bm : 0;
+    f.all += f.n[i];
+  }
+  return f;
+}
+
 // Row tiles of bm of all experts' rows.  Called by whole wavefronts.
 __device__ __forceinline__ int count_tiles(const MxArgs& a, int bm) {
-  const int rows = (int)a.rows;
-  if (!a.offsets) return (rows + bm - 1) / bm;
+  if (!a.offsets) return ((int)a.rows + bm - 1) / bm;
   int n = 0;
-  for (int e = threadIdx.x & 63; e < a.E; e += 64) {
-    const int lo = min(max(a.offsets[e], 0), rows), hi = min(max(a.offsets[e + 1], 0), rows);
-    n += hi > lo ? (hi - lo + bm - 1) / bm : 0;
-  }
+  for (int e = (threadIdx.x & 63) * 4; e < a.E; e += 256) n += four_experts(a, bm, e).all;
   return __builtin_amdgcn_readlane(lane_scan(n), 63);
 }
 
@@ -224,26 +242,30 @@ __device__ __forceinline__ int count_tiles(const MxArgs& a, int bm) {
 // rows of two experts.  Offsets out of order or out of range give other rows, but
 // none outside [0, rows).  Called by whole wavefronts.
 __device__ __forceinline__ RowTile find_tile(const MxArgs& a, int bm, int t) {
-  const int rows = (int)a.rows;
   if (!a.offsets) {
     const int64_t row = (int64_t)t * bm;
-    return {0, row < rows ? min(bm, (int)(rows - row)) : 0, row};
+    return {0, row < a.rows ? min(bm, (int)(a.rows - row)) : 0, row};
   }
   const int lane = threadIdx.x & 63;
-  int done = 0;
-  for (int e0 = 0; e0 < a.E; e0 += 64) {
-    const int e = e0 + lane;
-    const int lo = e < a.E ? min(max(a.offsets[e], 0), rows) : 0;
-    const int hi = e < a.E ? min(max(a.offsets[e + 1], 0), rows) : 0;
-    const int n = hi > lo ? (hi - lo + bm - 1) / bm : 0;
-    const int upto = lane_scan(n), all = __builtin_amdgcn_readlane(upto, 63);
-    if (t < done + all) {
-      const int l = __builtin_ctzll(__ballot(t < done + upto));
-      const int first = __builtin_amdgcn_readlane(lo, l), last = __builtin_amdgcn_readlane(hi, l);
-      const int row = first + (t - done - __builtin_amdgcn_readlane(upto - n, l)) * bm;
-      return {e0 + l, min(bm, last - row), row};
+  for (int e0 = 0; e0 < a.E; e0 += 256) {
+    const Four f = four_experts(a, bm, e0 + 4 * lane);
+    const int upto = lane_scan(f.all), all = __builtin_amdgcn_readlane(upto, 63);
+    if (t < all) {
+      int before = upto - f.all, expert = -1, row = 0, last = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t >= before && t < before + f.n[i]) {
+          expert = e0 + 4 * lane + i;
+          row = f.lo[i] + (t - before) * bm;
+          last = f.hi[i];
+        }
+        before += f.n[i];
+      }
+      const int l = __builtin_ctzll(__ballot(expert >= 0));
+      const int first = __builtin_amdgcn_readlane(row, l);
+      return {__builtin_amdgcn_readlane(expert, l), min(bm, __builtin_amdgcn_readlane(last, l) - first), first};
     }
-    done += all;
+    t -= all;
   }
   return {0, 0, 0};
 }
@@ -262,10 +284,21 @@ __device__ __forceinline__ void store_row(int type, char* base, int64_t at, int 
   else store16<false>((uint16_t*)base + at, left, v);
 }
 
-// 16 bytes of a row's scales, zeros from byte `left` on
-__device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int left) {
+// 16 bytes of a row's scales, zeros from byte `left` on, where the row ends; `before` of its bytes
+// lie in front of p.  A row of 16 or more is read up to its end, in one load, and
+// shifted (byte by byte 1536 rows over 128 experts of 2048 x 768 took 82 us).
+__device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int before, int left) {
   if (left >= 16) return ((const Loose<v4u32, 1>*)p)->v;
   v4u32 v = {0, 0, 0, 0};
+  if (left <= 0) return v;
+  if (before + left >= 16) {
+    v = ((const Loose<v4u32, 1>*)(p + left - 16))->v;
+    uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+    const int bits = 8 * (16 - left);          // 8 .. 120
+    lo = bits >= 64 ? hi >> (bits - 64) : lo >> bits | hi << (64 - bits);
+    hi = bits >= 64 ? 0 : hi >> bits;
+    return v4u32{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
 #pragma unroll
   for (int c = 0; c < 15; ++c)
     if (c < left) v[c / 4] |= (uint32_t)p[c] << (c % 4 * 8);
@@ -340,7 +373,7 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
     // scales of the piece; past K's end zeros, since a NaN there would count
     auto scales = [&](const uint8_t* p) __attribute__((always_inline)) {
       if constexpr (WHOLE) return ((const Loose<v4u32, 1>*)(p + k0 / 32))->v;
-      else return load_scales(p + k0 / 32, (a.K - k0) / 32);
+      else return load_scales(p + k0 / 32, k0 / 32, (a.K - k0) / 32);
     };
 #pragma unroll
     for (int h = 0; h < G; ++h)
@@ -489,6 +522,7 @@ typedef MxTile<256, 256, 2, 4, 2, 16> Mx256;     // x in 4 bits
 typedef MxTile<128, 256, 2, 4, 4, 16> MxWide;    // x in 16 bits: two workgroups a CU
 typedef MxTile<128, 128, 2, 2, 1, 32> Mx128;
 typedef MxTile<32, 256, 1, 4, 1, 32, 5> Mx32;    // x in 16 bits: 12 to 40 rows an expert
+typedef MxTile<32, 128, 1, 2, 1, 32> Mx32Both;   // the same with x in 4 bits: two wavefronts, three workgroups a CU
 typedef MxTile<64, 128, 2, 2, 1, 32> Mx64;       // (16 x 16 steps: 4096 rows over 128 experts of 2 x 768 x 2048 84 us instead of 79)
 
 // vmcnt(flying) lgkmcnt(0) and the workgroup's barrier
@@ -654,7 +688,8 @@ void mx_both_kernel(MxArgs a) {
     } else {
 #pragma unroll 1
       for (int i = 0; i < S_LOADS; ++i) {
-        const v4u32 v = load_scales(srow[i] + 32 * s, kscales - 32 * s - min(i * C::NT + tid, S_CHUNKS - 1) % 2 * 16);
+        const int at = 32 * s + min(i * C::NT + tid, S_CHUNKS - 1) % 2 * 16;
+        const v4u32 v = load_scales(srow[i] + 32 * s, at, kscales - at);
 #pragma unroll
         for (int j = 0; j < S_LOADS; ++j) sc[j] = j == i ? v : sc[j];
       }
@@ -823,7 +858,7 @@ void mx_weights_kernel(MxArgs a) {
   auto fetch_scales = [&](int s) __attribute__((always_inline)) {
     if (C::NT > C::BN && tid >= C::BN) return;
     if (16 * s + 16 <= kscales) sc = ((const Loose<v4u32, 1>*)(srow + 16 * s))->v;
-    else sc = load_scales(srow + 16 * s, kscales - 16 * s);
+    else sc = load_scales(srow + 16 * s, 16 * s, kscales - 16 * s);
   };
   auto keep_scales = [&](int s) __attribute__((always_inline)) {
     if (C::NT > C::BN && tid >= C::BN) return;
@@ -967,10 +1002,11 @@ struct MxChoice {
 MxChoice choose_mx(const moe_mx_linear_desc& d) {
   struct Fit { double latency, shared, round_us; };
   struct Few { double fixed, piece, w_kb, x_kb; };
-  static const int bm[6] = {0, 64, 128, 256, 128, 32}, bn[6] = {0, 128, 128, 256, 256, 256};
-  static const int per_cu[2][6] = {{0, 3, 2, 0, 2, 2}, {0, 2, 2, 1, 0, 0}};
+  static const int bm[6] = {0, 64, 128, 256, 128, 32};
+  static const int bn[2][6] = {{0, 128, 128, 256, 256, 256}, {0, 128, 128, 256, 256, 128}};
+  static const int per_cu[2][6] = {{0, 3, 2, 0, 2, 2}, {0, 2, 2, 1, 0, 3}};
   static const Fit fits[2][6] = {{{}, {0.406, 0.284, 1.76}, {0.547, 0.436, 3.57}, {}, {0.673, 0.593, 7.72}, {0.467, 0.344, 3.56}},
-                                 {{}, {0.507, 0.538, 3.13}, {0.606, 0.588, 5.7}, {1.76, 0.96, 8.84}, {}, {}}};
+                                 {{}, {0.507, 0.538, 3.13}, {0.606, 0.588, 5.7}, {1.76, 0.96, 8.84}, {}, {0.6, 0.3, 3.0}}};
   static const Few few[2] = {{1.98, 2.83, 0.0778, 0.00733}, {2.01, 2.07, 0.0485, 0.0107}};
   static const double tile_rate[2] = {3.15, 3.9}, few_rate[2] = {8.26, 3.97};   // MB/us of weights
   static const MxChoice fews[] = {{FEW, 1, 2, 2}, {FEW, 1, 2, 4}, {FEW, 1, 4, 4}, {FEW, 2, 4, 4}};
@@ -1005,7 +1041,7 @@ MxChoice choose_mx(const moe_mx_linear_desc& d) {
   for (int t : {(int)T64, (int)T128, (int)T256, (int)WIDE, (int)T32}) {
     if (per_cu[mx][t] == 0) continue;          // not with such an x
     const Fit& f = fits[mx][t];
-    const double tiles = row_tiles(bm[t]) * ceil(n / bn[t]), steps = ceil(K / (mx ? 256 : 64));
+    const double tiles = row_tiles(bm[t]) * ceil(n / bn[mx][t]), steps = ceil(K / (mx ? 256 : 64));
     double share = ceil(tiles / kCus);
     if (share > per_cu[mx][t]) share = per_cu[mx][t];
     const double step = share * f.shared > f.latency ? share * f.shared : f.latency;
@@ -1098,13 +1134,14 @@ hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const ui
         launch_tiles(a, C::BM, G ? C::BN / 2 : C::BN, C::NT, [&](dim3 grid) {
           if constexpr (!std::is_same_v<C, MxWide> && !std::is_same_v<C, Mx32>)
             if (d.dtype == MOE_MXFP4) hipLaunchKernelGGL((mx_both_kernel<C, G>), grid, dim3(C::NT), 0, s, a);
-          if constexpr (!std::is_same_v<C, Mx256>) {
+          if constexpr (!std::is_same_v<C, Mx256> && !std::is_same_v<C, Mx32Both>) {
             if (d.dtype == MOE_F16) hipLaunchKernelGGL((mx_weights_kernel<C, true, G>), grid, dim3(C::NT), 0, s, a);
             else if (d.dtype == MOE_BF16) hipLaunchKernelGGL((mx_weights_kernel<C, false, G>), grid, dim3(C::NT), 0, s, a);
           }
         });
       };
-      if (c.kind == T32) go(Mx32{});
+      if (c.kind == T32 && d.dtype == MOE_MXFP4) go(Mx32Both{});
+      else if (c.kind == T32) go(Mx32{});
       else if (c.kind == T64) go(Mx64{});
       else if (c.kind == T128) go(Mx128{});
       else if (c.kind == WIDE) go(MxWide{});
