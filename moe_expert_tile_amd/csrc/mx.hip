@@ -989,11 +989,11 @@ struct MxChoice {
 // experts (the offsets are in device memory), half a row tile lost at each
 // expert's end.  A stage of a tile takes a load's latency, or what the
 // multiplications of the workgroups that share a CU take; a round of workgroups adds its
-// start and epilogue.  A few-row workgroup takes a fixed time and one for each piece of
-// K its wavefronts take in turn; all of them together what their reads take.  Neither is
+// start and epilogue.  A few-row workgroup takes a fixed time (another one in later
+// rounds) and one for each piece of K its wavefronts take in turn; all of them together what their reads take.  Neither is
 // faster than the weights' reading.  The constants are fitted to the times of every
-// choice over 252 products with x in 16 bits and 198 in 4 (1 to 32768 rows, 1 to 128
-// experts): the choice costs 2.9% over the best one on average, 3.7% in 4 bits.
+// choice over 252 products of each kind (1 to 32768 rows, 1 to 128 experts): the
+// choice costs 2.9% over the best one on average with x in 16 bits, 3.1% in 4.
 // Both sides of typical decisions, gated products with x in bf16: 8 rows over 8 experts of
 // 2 x 2048 x 7168 take 31 us as few rows and 58 us in tiles of 64 rows; 1024 over 32 of them
 // 239 us as few rows, 196 in 64 x 128 tiles and 187 in 128 x 256; 384 over 32 of 7168 x 2048 (no
@@ -1001,14 +1001,14 @@ struct MxChoice {
 // 64 x 128, 422 in 128 x 128, 355 in 128 x 256 and 391 in 256 x 256 ones.
 MxChoice choose_mx(const moe_mx_linear_desc& d) {
   struct Fit { double latency, shared, round_us; };
-  struct Few { double fixed, piece, w_kb, x_kb; };
+  struct Few { double fixed, next, piece, w_kb, x_kb; };
   static const int bm[6] = {0, 64, 128, 256, 128, 32};
   static const int bn[2][6] = {{0, 128, 128, 256, 256, 256}, {0, 128, 128, 256, 256, 128}};
   static const int per_cu[2][6] = {{0, 3, 2, 0, 2, 2}, {0, 2, 2, 1, 0, 3}};
   static const Fit fits[2][6] = {{{}, {0.406, 0.284, 1.76}, {0.547, 0.436, 3.57}, {}, {0.673, 0.593, 7.72}, {0.467, 0.344, 3.56}},
-                                 {{}, {0.507, 0.538, 3.13}, {0.606, 0.588, 5.7}, {1.76, 0.96, 8.84}, {}, {0.6, 0.3, 3.0}}};
-  static const Few few[2] = {{1.98, 2.83, 0.0778, 0.00733}, {2.01, 2.07, 0.0485, 0.0107}};
-  static const double tile_rate[2] = {3.15, 3.9}, few_rate[2] = {8.26, 3.97};   // MB/us of weights
+                                 {{}, {0.549, 0.539, 2.97}, {0.544, 0.492, 5.33}, {1.48, 0.665, 8.52}, {}, {0.364, 0.449, 3.53}}};
+  static const Few few[2] = {{1.98, 1.98, 2.83, 0.0778, 0.00733}, {1.98, 5.2, 1.98, 0.0467, 0.00993}};
+  static const double tile_rate[2] = {3.15, 4.54}, few_rate[2] = {8.26, 4.57};   // MB/us of weights
   static const MxChoice fews[] = {{FEW, 1, 2, 2}, {FEW, 1, 2, 4}, {FEW, 1, 4, 4}, {FEW, 2, 4, 4}};
   constexpr double kCus = 256;
   const int mx = d.dtype == MOE_MXFP4;
@@ -1033,7 +1033,8 @@ MxChoice choose_mx(const moe_mx_linear_desc& d) {
     const double groups = row_tiles(16 * c.tt) * ceil(n / (16 * c.blocks)), pieces = ceil(K / 512);
     const double each = M / hit, rows = each < 16 * c.tt ? each : 16 * c.tt;
     const double rounds = groups / (kCus * (8 / c.waves) * 2), near = weights_mb < 0.3 ? 0.5 : 1;   // (in the L2)
-    const double wait = (rounds > 1 ? rounds : 1) * (f.fixed + ceil(pieces / c.waves) * f.piece * near);
+    const double turns = ceil(pieces / c.waves) * f.piece;
+    const double wait = f.fixed + turns * near + (rounds > 1 ? (rounds - 1) * (f.next + turns) : 0);
     const double read = f.fixed + groups * K / 512 * (16 * c.blocks * 0.266 * f.w_kb + rows * (mx ? 0.266 : 1) * f.x_kb) / kCus;
     const double all = weights_mb / few_rate[mx];
     take(c, wait > read ? (wait > all ? wait : all) : (read > all ? read : all));
