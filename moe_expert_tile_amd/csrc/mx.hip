@@ -317,8 +317,8 @@ __device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int before, int l
 // scales of a piece are one load, of which step s needs byte lane / 16 of dword s.
 // Result lane: row (of x) lane % 16, columns 4 (lane / 16) .. + 3.
 // Measured with the weights in no cache (a call among others): 8 rows over 8 experts of 2 x
-// 2048 x 7168, 125 MB, 30.4 us (4.1 TB/s); 512 over 128 of 2 x 768 x 2048, 217 MB, 51 us
-// (4.3 TB/s).  With pieces of 128 elements and 8 wavefronts a workgroup they took 46 and
+// 2048 x 7168, 125 MB, 30.4 us (4.1 TB/s); 512 over 128 of 2 x 768 x 2048, 217 MB, 50 us
+// (4.4 TB/s).  With pieces of 128 elements and 8 wavefronts a workgroup they took 46 and
 // 133 us: 64 contiguous bytes a row and load, four times the loads of scales, and half as many
 // workgroups a CU.  x's operands are read a step ahead alone (all four steps' cost the
 // registers of a second workgroup: 62 instead of 57 us).
