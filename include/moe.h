@@ -489,7 +489,8 @@ int moe_unpermute(const moe_rows_desc* desc, const void* rows, const int32_t* po
  * stay as they were.
  *   rows      as given to moe_unpermute; may be NULL when d_topk_w is.
  *   topk_w    NULL: every weight is 1.
- *   d_rows, d_topk_w   no overlap with the inputs; either may be NULL, not both.
+ *   d_rows, d_topk_w   no overlap with the inputs; either may be NULL, not both unless
+ *             tokens or rows is 0.
  */
 int moe_unpermute_backward(const moe_rows_desc* desc, const void* rows, const int32_t* pos, const float* topk_w,
                            const void* d_out, void* d_rows, float* d_topk_w, void* stream);

@@ -599,6 +599,8 @@ def moe_unpermute_backward(pos, d_out, rows=None, topk_w=None, d_rows=None, d_to
     """The gradients of moe_unpermute that are given a tensor: d_rows [R, d] and
     d_topk_w float32 [T, k] (this one needs rows) from d_out [T, d]."""
     where = "moe_unpermute_backward"
+    if d_rows is None and d_topk_w is None:   # (the library sees addresses, and an empty tensor has none)
+        raise _invalid(where, "neither d_rows nor d_topk_w is given")
     given, name = (rows, "rows") if d_rows is None else (d_rows, "d_rows")
     if given is None:
         raise _invalid(where, "neither d_rows nor rows is given")

@@ -263,12 +263,14 @@ int moe_unpermute_backward(const moe_rows_desc* desc, const void* rows, const in
   moe_rows_desc d;
   int rc = check_rows(desc, pos, &d);
   if (rc) return rc;
-  if (!d_rows && !d_topk_w) return MOE_EINVAL;
+  // a gradient without elements may be null as well, and nothing be left to write
+  const bool none = !d_rows && !d_topk_w;
+  if (none && d.tokens > 0 && d.rows > 0) return MOE_EINVAL;
   if (!row_buffer(d, d_out, d.tokens) || !row_buffer(d, d_rows, 0) || !row_buffer(d, rows, d_topk_w ? d.rows : 0) ||
       !aligned_to(topk_w, 4) || !aligned_to(d_topk_w, 4))
     return MOE_EINVAL;
   rc = prepare_device();
-  if (rc || d.tokens == 0) return rc;
+  if (rc || d.tokens == 0 || none) return rc;
   return hip_rc(launch_unpermute_backward(d, rows, pos, topk_w, d_out, d_rows, d_topk_w, (hipStream_t)stream));
 }
 

@@ -177,6 +177,27 @@ def test_no_tokens_and_no_rows():
     assert bool((rows == 9).all())
 
 
+def test_one_gradient_alone_without_tokens_or_rows():
+    """An empty gradient is given, though its address is 0."""
+    m = _m()
+    pos = torch.full((3, 2), -1, dtype=torch.int32, device="cuda")
+    g, w, rows = torch.randn(3, 5, device="cuda"), torch.randn(3, 2, device="cuda"), torch.full((4, 5), 9.0, device="cuda")
+    none, no_w = torch.empty(0, 5, device="cuda"), torch.empty(0, 2, device="cuda")
+    for weights in (None, w):
+        m.moe_unpermute_backward(pos, g, topk_w=weights, d_rows=none)               # no expert of the rank got a row
+        m.moe_unpermute_backward(pos, g, none, weights, none)
+        d_w = torch.full((3, 2), 9.0, device="cuda")
+        m.moe_unpermute_backward(pos, g, none, weights, d_topk_w=d_w)
+        assert bool((d_w == 0).all())
+        no = None if weights is None else no_w
+        m.moe_unpermute_backward(pos[:0], none, rows, no, d_topk_w=no_w)            # no tokens
+        m.moe_unpermute_backward(pos[:0], none, topk_w=no, d_rows=rows)
+        m.moe_unpermute_backward(pos[:0], none, none, no, none, no_w)               # neither
+        m.moe_unpermute_backward(pos[:0], none, none, no, d_topk_w=no_w)
+        m.moe_unpermute_backward(pos[:0], none, topk_w=no, d_rows=none)
+    assert bool((rows == 9).all())
+
+
 def test_offsets_beyond_32_bits():
     """Rows 4 MB apart, so that the last ones lie 4.6 GB behind the first."""
     m = _m()

@@ -78,6 +78,26 @@ def test_bad_row_calls_are_rejected():
 
 
 @built
+def test_empty_gradients_are_no_refusal():
+    """Without tokens or without rows a gradient that was asked for may have no
+    address; with both, a call for neither is refused."""
+    m = _m()
+
+    def call(tokens, rows, d_rows, d_topk_w):
+        d = m.moe_rows_desc(tokens=tokens, rows=rows, top_k=2, cols=32, dtype=0)
+        return m._lib.moe_unpermute_backward(ctypes.byref(d), GOOD if rows and d_topk_w else None, GOOD if tokens else None, None,
+                                             GOOD if tokens else None, d_rows, d_topk_w, 0)
+
+    for sizes in ((3, 0), (0, 4), (0, 0)):       # nothing to write: no launch, and without a GPU no device
+        assert call(*sizes, None, None) in (m.MOE_OK, m.MOE_EHIP, m.MOE_EUNSUPPORTED), sizes
+    assert call(3, 4, None, None) == m.MOE_EINVAL
+    pos, g, rows = torch.zeros(0, 2, dtype=torch.int32), torch.zeros(0, 32), torch.zeros(0, 32)
+    with pytest.raises(m.MoEError) as ei:
+        m.moe_unpermute_backward(pos, g, rows)
+    assert ei.value.status == m.MOE_EINVAL and "neither d_rows nor d_topk_w" in str(ei.value)
+
+
+@built
 def test_bad_row_tensors_are_rejected():
     m = _m()
     ids, pos, offsets = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(9, dtype=torch.int32)
