@@ -415,7 +415,8 @@ int moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const 
  * vanish.  The residual's gradient is d_out.
  *   d_out   device [rows, cols] of out_dtype.
  *   pre     device [rows, n]; not read without an activation (may be NULL then).
- *   dx      device [rows, depth], dw device [n, depth], dbias device [n]: any may be NULL, not all.
+ *   dx      device [rows, depth], dw device [n, depth], dbias device [n]: any may be NULL, not all
+ *           unless rows is 0.
  *           dx and dw without overlap with the inputs.
  *   x       may be NULL without dw, w without dx.
  *   ws      as for moe_linear, backward_bytes.

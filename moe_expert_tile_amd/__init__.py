@@ -502,6 +502,8 @@ def moe_linear_backward(x, w, d_out, dx=None, dw=None, dbias=None, pre=None, act
     w, dbias [n], all of x's type) from d_out [M, N] and, under an activation,
     the forward call's pre; see include/moe.h."""
     where = "moe_linear_backward"
+    if dx is None and dw is None and dbias is None:
+        raise _invalid(where, "none of dx, dw and dbias is given")
     d, n, index = _linear_desc(where, x, w, d_out, act, "d_out")
     dtype = x.dtype
     d.ld_pre = _matrix(where, "pre", pre, (x.shape[0], n), dtype, index)

@@ -201,13 +201,14 @@ int moe_linear_backward(const moe_linear_desc* desc, const void* x, const void* 
   moe_linear_desc d;
   int rc = check_linear(desc, &d);
   if (rc) return rc;
-  if (!dx && !dw && !dbias) return MOE_EINVAL;
+  const bool none = !dx && !dw && !dbias;     // (without rows: perhaps dx, which then has no elements)
+  if (none && d.rows > 0) return MOE_EINVAL;
   if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(pre, 2) || !aligned_to(d_out, item(d.out_dtype)) ||
       !aligned_to(dx, 2) || !aligned_to(dw, 2) || !aligned_to(dbias, 2) || !ws || !aligned_to(ws, 256))
     return MOE_EINVAL;
   if (d.rows > 0 && (!d_out || (dw && !x) || (dx && !w) || (d.act != MOE_ACT_NONE && !pre))) return MOE_EINVAL;
   rc = prepare_device();
-  if (rc) return rc;
+  if (rc || none) return rc;
   LinearGrads b = {x, w, pre, d_out, dx, dw, dbias};
   return hip_rc(launch_linear_backward(d, b, ws, (hipStream_t)stream));
 }

@@ -202,6 +202,19 @@ def test_no_rows():
     assert not dw.any() and not db.any()
 
 
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_one_gradient_alone_without_rows(act):
+    """An empty dx is given, though its address is 0 (a frozen expert without rows)."""
+    m = _m()
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    n = 64 if act == "swiglu" else 32
+    x, w, g, pre = torch.empty(0, 64, **bf), torch.ones(n, 64, **bf), torch.empty(0, 32, **bf), torch.empty(0, n, **bf)
+    m.moe_linear_backward(x, w, g, dx=torch.empty_like(x), pre=pre, act=_act(act))
+    db = torch.full((n,), 5.0, **bf)
+    m.moe_linear_backward(x, w, g, dbias=db, pre=pre, act=_act(act))
+    assert not db.any()
+
+
 # --- gradients -------------------------------------------------------------------
 
 def _check_backward(a, act, want=("dx", "dw", "dbias"), place=None):

@@ -57,6 +57,24 @@ def test_scale_backward_on_the_cpu_is_rejected():
         m.moe_scale_backward(bad, **a)
 
 
+def test_an_empty_gradient_of_the_product_is_no_refusal():
+    """Without rows dx, asked for alone, has no address; with rows a call for no gradient is refused."""
+    import ctypes
+    m = _m()
+    some = 1 << 20   # an address, never read
+
+    def call(rows, d_out):
+        d = m.moe_linear_desc(rows, 32, 64, 0, 0, m.ACT_NONE, 0)
+        return m._lib.moe_linear_backward(ctypes.byref(d), None, some, None, d_out, None, None, None, some, 0)
+
+    assert call(0, None) in (m.MOE_OK, m.MOE_EHIP, m.MOE_EUNSUPPORTED)   # no launch; without a GPU no device
+    assert call(4, some) == m.MOE_EINVAL
+    x, w, g = (torch.zeros(s, dtype=torch.bfloat16) for s in ((0, 64), (32, 64), (0, 32)))
+    with pytest.raises(m.MoEError, match="none of dx, dw and dbias is given") as ei:
+        m.moe_linear_backward(x, w, g)
+    assert ei.value.status == m.MOE_EINVAL
+
+
 @pytest.mark.parametrize("stream", [None, 0, 1 << 20])
 def test_tensors_on_the_cpu_are_rejected_whatever_the_stream(stream):
     m = _m()
