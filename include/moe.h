@@ -302,7 +302,7 @@ int moe_scale(const moe_shape* shape, const void* plan_ws, const uint16_t* recv_
  *   topk_w     device float [T_r, k]; may be NULL when d_recv is.
  *   d_out      device bf16 [T_r, d].
  *   d_recv     device bf16 [T_r*k, d], no overlap with the inputs; NULL: not wanted.
- *   d_topk_w   device float [T_r, k]; NULL: not wanted (one of the two must be).
+ *   d_topk_w   device float [T_r, k]; NULL: not wanted (one of the two must be, unless T_r is 0).
  */
 int moe_scale_backward(const moe_shape* shape, const void* plan_ws, const uint16_t* recv_self,
                        const float* topk_w, const uint16_t* d_out, uint16_t* d_recv, float* d_topk_w,

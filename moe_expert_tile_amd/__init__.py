@@ -348,6 +348,8 @@ def moe_scale_backward(shape: Shape, plan_ws, recv_self, topk_w, d_out, d_recv=N
     recv_self and d_out) and d_topk_w float32 [T_r, k]; tensors may have more
     rows, which stay as they are.  See include/moe.h."""
     where = "moe_scale_backward"
+    if d_recv is None and d_topk_w is None:
+        raise _invalid(where, "neither d_recv nor d_topk_w is given")
     c = shape.c
     d, k, r = c.hidden, c.top_k, c.rank
     tokens = shape.tokens

@@ -465,7 +465,7 @@ int moe_scale_backward(const moe_shape* s, const void* plan_ws, const uint16_t* 
   int rc = valid_shape(s);
   if (rc) return rc;
   if (!plan_ws || !aligned(plan_ws, 256)) return MOE_EINVAL;
-  if (!d_recv && !d_topk_w) return MOE_EINVAL;
+  if (!d_recv && !d_topk_w && s->tokens[s->rank] > 0) return MOE_EINVAL;   // (without tokens both are empty)
   if (!aligned(recv_self, 16) || !aligned(topk_w, 4) || !aligned(d_out, 16) || !aligned(d_recv, 16) ||
       !aligned(d_topk_w, 4))
     return MOE_EINVAL;

@@ -82,6 +82,16 @@ def test_scale_backward(tokens, rank, E, k, d):
     assert torch.equal(a, d_recv) and torch.equal(b, d_w)
 
 
+def test_one_scale_gradient_alone_without_tokens():
+    """An empty gradient is given, though its address is 0."""
+    m = _m()
+    sh, _, _ = _share(0, 4, 2, 256, tokens=[0, 5], rank=0, W=2)
+    rows, w = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 2, device="cuda")
+    m.moe_scale_backward(sh.shape, sh.plan_ws, rows, w, rows, d_recv=torch.empty_like(rows))
+    m.moe_scale_backward(sh.shape, sh.plan_ws, rows, w, rows, d_topk_w=torch.empty_like(w))
+    assert sh.status() == m.MOE_OK
+
+
 def test_scale_backward_after_a_routing_error_does_nothing():
     m = _m()
     sh, ids, _ = _share(16, 8, 2, 256)

@@ -57,6 +57,20 @@ def test_scale_backward_on_the_cpu_is_rejected():
         m.moe_scale_backward(bad, **a)
 
 
+def test_empty_gradients_of_the_scale_step_are_no_refusal():
+    """A rank without tokens: either gradient, asked for alone, has no address; with tokens a call for neither is refused."""
+    m = _m()
+    some = 1 << 20   # an address, never read
+    for tokens in (0, 6):
+        s, a = _scale_args(m, T=tokens)
+        rc = m._lib.moe_scale_backward(s.ptr, some, None, some, some, None, None, 0)
+        assert (rc == m.MOE_EINVAL) == (tokens > 0) and rc in (m.MOE_OK, m.MOE_EINVAL, m.MOE_EHIP, m.MOE_EUNSUPPORTED)
+        a["d_recv"] = a["d_topk_w"] = None
+        with pytest.raises(m.MoEError, match="neither d_recv nor d_topk_w is given") as ei:
+            m.moe_scale_backward(s, **a)
+        assert ei.value.status == m.MOE_EINVAL
+
+
 def test_an_empty_gradient_of_the_product_is_no_refusal():
     """Without rows dx, asked for alone, has no address; with rows a call for no gradient is refused."""
     import ctypes
