@@ -446,6 +446,32 @@ def test_offsets_out_of_order_or_range_stay_inside_the_buffers():
             assert bool((big == 9).sum() >= 8 * 64)
 
 
+@pytest.mark.parametrize("M", [20, 700])
+@pytest.mark.parametrize("xt", ["bf16", "f16", "mx"])
+def test_rows_outside_every_experts_stay_as_they_were(M, xt):
+    """Also with offsets out of order or range: what no expert's offsets, cut to the buffer, enclose is not written."""
+    m = _m()
+    q, s = _weights(4, 64, 64, torch.Generator(device="cuda").manual_seed(0))
+    x = torch.randn(M, 64, device="cuda")
+    if xt == "mx":
+        xq, xs = _quantize(x)
+        args = dict(x=xq, x_scale=xs)
+    else:
+        args = dict(x=x.to(DT[xt]))
+    for off in ([0, 0, 0, 0, 0], [M, M, M, M, M], [M - 1, M - 1, M, M, M], [3, 3, M // 2, M // 2, M - 2], [0, 1, 1, 2, 2],
+                [-5, 3, 2, 2 ** 31 - 1, 10], [M + 4, 2, -2 ** 31, 5, 3 * M], [9, 7, 5, 3, 1]):
+        big = torch.full((M + 8, 64), 9.0, device="cuda")
+        m.moe_mx_linear(w=q, w_scale=s, out=big[4:4 + M], offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), **args)
+        touched = (big != 9).any(1).cpu().numpy()
+        cut = np.clip(np.array(off, np.int64), 0, M)
+        enclosed = np.zeros(M + 8, bool)
+        for lo, hi in zip(cut, cut[1:]):
+            enclosed[4 + lo:4 + max(hi, lo)] = True
+        assert not (touched & ~enclosed).any(), off
+        if (np.diff(off) >= 0).all():
+            assert np.array_equal(touched, enclosed), off       # (a result of 9 in all 64 columns aside)
+
+
 def test_no_rows():
     m = _m()
     q, s = _weights(2, 64, 64, torch.Generator(device="cuda").manual_seed(0))
