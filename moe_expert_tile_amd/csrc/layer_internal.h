@@ -56,7 +56,7 @@ hipError_t launch_mx_quantize(int64_t rows, int depth, const void* x, int dtype,
 hipError_t launch_mx_dequantize(int64_t rows, int depth, const uint8_t* q, int64_t ld_q, const uint8_t* scale,
                                 int64_t ld_s, void* out, int dtype, int64_t ld_out, hipStream_t s);
 // for tests: 0 few rows (then 16-row blocks of x, of w and wavefronts of a workgroup), 1 64 x 128, 2 128 x 128,
-// 3 256 x 256, 4 128 x 256
+// 3 256 x 256, 4 128 x 256, 5 32 x 256 (x in 4 bits: 32 x 128)
 void mx_choice(const moe_mx_linear_desc& d, int32_t out[4]);
 hipError_t launch_mx_linear(const moe_mx_linear_desc& d, const void* x, const uint8_t* x_scale, const uint8_t* w,
                             const uint8_t* w_scale, const int32_t* offsets, const void* bias, void* out, hipStream_t s);

@@ -56,8 +56,9 @@ __device__ __forceinline__ v4u32 widen(uint32_t q, float scale) {
 // magnitude is found among bit patterns (infinities and NaN are above all
 // numbers that way), across the lanes by two DPP moves.  v_cvt_scalef32_pk_fp4_*
 // round to the nearest element, ties to the even one, and saturate at 6.  A thread
-// has four groups of eight in flight.  Bound by HBM: 16384 x 7168 from bf16, 297 MB, 51.7 us
-// (5.75 TB/s, a large copy 4.98), and back 56.4 us (5.27); 64 x 2048 take a launch.
+// has four groups of eight in flight.  Bound by HBM: 16384 x 7168 from bf16 and back, 597 MB,
+// 129 us a pair of calls (4.6 TB/s, a large copy 4.98), 72 (60 at best) and 56 us in the profiler's
+// intervals; 64 x 2048 take a launch each.
 // A packed matrix is taken as one long row, without divisions.
 
 struct QuantArgs {
@@ -317,8 +318,9 @@ __device__ __forceinline__ v4u32 load_scales(const uint8_t* p, int before, int l
 // scales of a piece are one load, of which step s needs byte lane / 16 of dword s.
 // Result lane: row (of x) lane % 16, columns 4 (lane / 16) .. + 3.
 // Measured with the weights in no cache (a call among others): 8 rows over 8 experts of 2 x
-// 2048 x 7168, 125 MB, 30.4 us (4.1 TB/s); 512 over 128 of 2 x 768 x 2048, 217 MB, 50 us
-// (4.4 TB/s).  With pieces of 128 elements and 8 wavefronts a workgroup they took 46 and
+// 2048 x 7168, 125 MB, 30.3 us (4.1 TB/s); 512 over 128 of 2 x 768 x 2048, 217 MB, 50 us
+// (4.4 TB/s); replayed from a graph over 600 MB of weights 34 and 55 us, with x in 4 bits 26.7 and
+// 47.5.  With pieces of 128 elements and 8 wavefronts a workgroup they took 46 and
 // 133 us: 64 contiguous bytes a row and load, four times the loads of scales, and half as many
 // workgroups a CU.  x's operands are read a step ahead alone (all four steps' cost the
 // registers of a second workgroup: 62 instead of 57 us).
@@ -493,19 +495,21 @@ __global__ __launch_bounds__(W * 64) void few_rows_kernel(MxArgs a) {
 // (their rows may start at any byte), some stages' at a time, into a table of
 // their own in LDS, ahead of the stages that need them.
 //
-// Rates (gated, bf16 out, a call among others).  x in 16 bits: 8192 x 2 x 2048 x 7168 363 us,
-// 1.33 PFLOP/s; 16384 rows over 16 uneven experts of 2 x 1536 x 4096 366 us, 1.13.  x in 4
-// bits: 46451 over 32 of 2 x 2048 x 7168 841 us, 3.24 PFLOP/s; 8192 x 8192 x 8192 plain
-// 296 us, 3.72; 8192 x 4096 x 28672 465 us, 4.13.  Both are limited by power first: with
-// random operands in registers alone the card reaches 1.91 PFLOP/s in v_mfma_f32_32x32x16_bf16, 2.25 in
+// Rates (gated, bf16 out, replayed from a graph).  x in 16 bits: 8192 x 2 x 2048 x 7168 368 us,
+// 1.31 PFLOP/s; 16384 rows over 16 uneven experts of 2 x 1536 x 4096 366 us, 1.13.  x in 4
+// bits: 46451 over 32 of 2 x 2048 x 7168 835 us, 3.27 PFLOP/s; 8192 x 8192 x 8192 plain
+// 293 us, 3.75; 8192 x 2 x 4096 x 28672 899 us, 4.28.  The card's power limits both: with
+// random operands in registers alone it reaches 1.91 PFLOP/s in v_mfma_f32_32x32x16_bf16, 2.25 in
 // 16x16x32 and 6.8 in v_mfma_scale_f32_32x32x64 of 4 bits (9.4 with constant operands).
-// Of the 1.99 us a stage of the 256 x 256 tile takes with x in 4 bits, 1.66 remain without its loads and
-// 1.56 without its LDS reads either; a tile adds 13 us (start 3, epilogue 10, its stores being
-// two thirds of that), a fifth of the time at K = 7168.  Measured beside it: four wavefronts
+// With x in 4 bits there is more between: of the 1.99 us a stage of the 256 x 256 tile takes (1.26 at
+// 6.8 PFLOP/s) 1.66 remain without its loads and 1.56 without its LDS reads either, so that 0.3 us
+// are neither (all eight wavefronts meet at every stage; what else was not found); a tile adds 13 us (start 3,
+// epilogue 10, its stores being two thirds of that), a fifth of the time at K = 7168, in which its CU
+// multiplies nothing.  Measured beside it: four wavefronts
 // of 128 x 128 4-10% slower; 128 x 256 tiles of 128-element stages, two workgroups a CU, 0-20%
 // slower; 16 x 16 steps 40-80% slower (registers).  With x in 16 bits 128 x 256 tiles, whose
-// two workgroups a CU overlap one's epilogue with the other's sums, take 366 us where 256 x 256
-// ones take 391, and 193 us for 8192 x 7168 x 2048 (211); where tiles fit the CUs
+// two workgroups a CU overlap one's epilogue with the other's sums, take 366 us for 16384 rows where
+// 256 x 256 ones take 391, and 193 us for 8192 x 7168 x 2048 (211); where tiles fit the CUs
 // exactly and sums are long they are 3% slower.
 
 // WAVES_SIMD: wavefronts a SIMD that the registers are limited for; B16, STAGES16: block of the
@@ -992,13 +996,14 @@ struct MxChoice {
 // start and epilogue.  A few-row workgroup takes a fixed time (another one in later
 // rounds) and one for each piece of K its wavefronts take in turn; all of them together what their reads take.  Neither is
 // faster than the weights' reading.  The constants are fitted to the times of every
-// choice over 252 products of each kind (1 to 32768 rows, 1 to 128 experts): the
-// choice costs 2.9% over the best one on average with x in 16 bits, 3.1% in 4.
-// Both sides of typical decisions, gated products with x in bf16: 8 rows over 8 experts of
-// 2 x 2048 x 7168 take 31 us as few rows and 58 us in tiles of 64 rows; 1024 over 32 of them
-// 239 us as few rows, 196 in 64 x 128 tiles and 187 in 128 x 256; 384 over 32 of 7168 x 2048 (no
-// gate) 76 us in 64 x 128 tiles and 67 in 32 x 256; 16384 over 16 of 2 x 1536 x 4096 487 us in
-// 64 x 128, 422 in 128 x 128, 355 in 128 x 256 and 391 in 256 x 256 ones.
+// choice over 252 products of each kind (1 to 32768 rows, 1 to 128 experts;
+// profiles/mx_choice_times.txt): the choice costs 2.8% over the best one on average with x
+// in bf16, 3.5% in 4 bits, and more than a tenth for 29 and 35 of them.
+// Both sides of typical decisions, in one run of replayed graphs, gated products with x in bf16: 8 rows over 8
+// experts of 2 x 2048 x 7168 take 31 us as few rows (16 x 64) and 46 us in tiles of 64 rows; 1024 over 32 of them
+// 240 us as few rows, 187 in 64 x 128 tiles, 192 in 128 x 256 (the choice) and 173 in 32 x 256; 384 over 32 of
+// 7168 x 2048 (no gate) 77 us in 64 x 128 tiles and 66 in 32 x 256; 16384 over 16 of 2 x 1536 x 4096 493 us in
+// 64 x 128, 449 in 128 x 128 and 380 in 128 x 256 ones.
 MxChoice choose_mx(const moe_mx_linear_desc& d) {
   struct Fit { double latency, shared, round_us; };
   struct Few { double fixed, next, piece, w_kb, x_kb; };

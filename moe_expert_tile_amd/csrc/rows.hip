@@ -10,8 +10,8 @@
 // launches: per-workgroup histograms, then the same walk, in which every
 // workgroup sums the histograms of those before it.  Integer sums only, so the
 // result is the same in any order of the atomics.  Bound by latency: 64 x 8 ids over
-// 128 experts 3.8 us (the kernel), 32768 x 8 over 256 11 us a call, 2.6 + 9.3 us in its two kernels (its
-// bytes, 3.1 MB, would take 0.6); 8 million pairs take 97 us.
+// 128 experts 3.8 us (the kernel), 32768 x 8 over 256 2.7 + 9.3 us in its two kernels (its
+// bytes, 3.1 MB, would take 0.6); 8 million pairs 22 + 85 us.
 #include "product.h"
 
 namespace moe {
@@ -238,7 +238,7 @@ __device__ __forceinline__ bool held(const RowArgs& a, int p) { return (uint64_t
 
 // Each wavefront takes U KB of a token's row at a time, reads it once and writes
 // it to the token's rows.  Bound by HBM: 8192 x 8 rows of 4096 bf16 columns, 604 MB,
-// 106 us (5.7 TB/s); few tokens take 1 KB a wavefront, so that they spread over the CUs.
+// 105 us (5.7 TB/s); few tokens take 1 KB a wavefront, so that they spread over the CUs.
 template <int SIZE, bool WHOLE, int POLICY, int U>
 __global__ __launch_bounds__(256) void permute_kernel(RowArgs a) {
   const int lane = threadIdx.x & 63;
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256) void permute_kernel(RowArgs a) {
 
 // Sum of a token's rows, weighted or not, in slot order in fp32: a wavefront
 // takes U KB of a token's row and has the loads of four slots in flight.  Bound by HBM:
-// the same size 103 us (5.8 TB/s); a decode step of 64 x 8 x 2048 4.4 us, a launch.
+// the same size 102 us (5.9 TB/s), weighted or not; a decode step of 64 x 8 x 2048 4.4 us, a launch.
 template <int T, bool WEIGHTED, bool WHOLE, int POLICY, int U>
 __global__ __launch_bounds__(256) void unpermute_kernel(RowArgs a) {
   typedef Type<T> E;
@@ -316,8 +316,8 @@ __global__ __launch_bounds__(256) void unpermute_kernel(RowArgs a) {
 // Gradients of the sum: a wavefront per slot reads the token's gradient and, for
 // the weight's, the slot's row, writes the row's gradient and reduces the product
 // in fp32.  A token's slots are neighbouring wavefronts, so its gradient comes
-// from the caches after the first of them.  Bound by HBM: 4097 x 8 x 7168, 1.0 GB, 190 us
-// (5.2 TB/s), 202 with ordinary accesses.
+// from the caches after the first of them.  Bound by HBM: 4097 x 8 x 7168, 1.0 GB, 190 us a
+// call (5.2 TB/s), 202 with ordinary accesses.
 template <int T, bool DROWS, bool DW, bool WHOLE, int POLICY>
 __global__ __launch_bounds__(256) void unpermute_back_kernel(RowArgs a) {
   typedef Type<T> E;
@@ -370,10 +370,10 @@ __global__ __launch_bounds__(256) void unpermute_back_kernel(RowArgs a) {
 // --- host -------------------------------------------------------------------
 
 // Pairs of a workgroup.  A short batch is one workgroup's, whose 16 wavefronts share it
-// out: 4096 pairs over 128 experts 8.2 us so and 9.5 us in two launches, 8192 11.2 and 9.3 us
-// (replayed from a graph).  Beyond that up to 256 workgroups, which each read all
-// histograms: 32768 pairs over 256 experts 9.7 us with 1024 pairs each and 11.0 with 2048,
-// 262144 14.8 and 12.7 us, 13.1 with 4096.
+// out; a longer one up to 256 workgroups', which each read all histograms.  Calls replayed
+// from a graph: 4096 pairs over 128 experts 7.9 us in one workgroup and 8.4 in two
+// launches, 8192 10.9 and 8.7; 32768 over 256 experts 9.3 us with 1024 pairs each
+// and 10.5 with 2048; 262144 14.5 us with 1024, 12.4 with 2048 and 13.3 with 4096.
 int64_t sort_per(int64_t pairs) {
   const int64_t least = pairs <= 4096 ? (pairs > 0 ? pairs : 1) : pairs <= 131072 ? 1024 : 2048, per = (pairs + 255) / 256;
   return ((per > least ? per : least) + kSortThreads - 1) / kSortThreads * kSortThreads;
